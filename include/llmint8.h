@@ -398,6 +398,122 @@ LLMINT8_API size_t llmint8_noalloc_scratch_bytes(void);
  */
 LLMINT8_API int llmint8_gemm_tile(int64_t T, int64_t N);
 
+/*
+ * The int8 key/value cache: the other tensor that a served model keeps in
+ * memory, next to its int8 weights, in the same form (absmax int8 codes with
+ * fp32 magnitudes), written as tokens arrive and attended to as it is stored.
+ *
+ * A cache is a pool of pages. A page holds `page` consecutive tokens of one
+ * sequence for every key/value head, with one magnitude per page and head for K
+ * and one for V:
+ *   K  int8 [pages, heads, page, dim]   aK fp32 [pages, heads]
+ *   V  int8 [pages, heads, dim, page]   aV fp32 [pages, heads]
+ * (V channel-major: attention sums over tokens.) A code c stands for
+ * fl32(c * fl32(a / 127)). The memory need not be initialised: a page begins
+ * when its first slot is written.
+ *
+ * A batch says which rows of the call belong to which sequence and where their
+ * tokens are: rows cu[b] .. cu[b+1]-1 are the last n_b = cu[b+1] - cu[b] tokens
+ * of sequence b, which holds len[b] tokens with them, so they stand at positions
+ * len[b] - n_b .. len[b] - 1; token j is in page table[b][j / page], slot
+ * j % page. cu rises from 0 to at most rows; any n_b may be 0. The three arrays
+ * are device memory and the host never reads them. The kernels stay inside the
+ * buffers whatever they hold: rows at negative positions (n_b > len[b]) and
+ * rows past cu[seqs] are left alone by append and gather, a page id outside
+ * [0, pages) or an entry past width is a page that does not exist (append
+ * writes nothing there, gather gives zeros, attention does not see it).
+ *
+ * Limits (LLMINT8_ERR_UNSUPPORTED): page 16, 32, 64 or 128; dim a multiple of 16
+ * up to 256; heads <= 4096; rows, width * page and 2 seqs page <= 2^29. Device
+ * pointers 16-byte aligned (cu, len, table, aK, aV: 4-byte). seqs = 0 or rows = 0
+ * is a no-op. 16-bit rows (k, v, q, outputs) are [rows, heads, dim] with dense
+ * channels; their token and head strides are given in elements, multiples of 8,
+ * and may be those of a slice of a larger tensor.
+ */
+typedef struct {
+  int8_t* K;
+  int8_t* V;
+  float* aK;
+  float* aV;
+  int64_t pages, heads, page, dim;
+} llmint8_kv_cache;
+
+typedef struct {
+  const int32_t* cu;    /* [seqs + 1] */
+  const int32_t* len;   /* [seqs] */
+  const int32_t* table; /* [seqs, width] */
+  int64_t seqs, rows, width;
+  int64_t max_len; /* host: about the largest len[b], for sizing work; 0 = width * page. Any value is correct. */
+} llmint8_kv_batch;
+
+/*
+ * Table of rotary positions: table[p][i] = fl32(mag cos(p f_i)), table[p][pairs
+ * + i] = fl32(mag sin(p f_i)) for p < rows, formed in 64 bits.
+ *   freq  HOST fp64 [pairs], read before the call returns; pairs in [1, 128]
+ *   mag   magnitude (1, or the attention factor of a long-context scaling)
+ *   table device fp32 [rows, 2 pairs], 16-byte aligned
+ */
+LLMINT8_API llmint8_status llmint8_rope_table(const double* freq, int64_t pairs, int64_t rows, double mag,
+                                              float* table, void* stream);
+
+/*
+ * Writes the batch's rows of k and v to the cache, k rotated by its positions on
+ * the way, and q rotated to q_out in the same launch.
+ *   rope  device fp32 [rope_rows, rot] from llmint8_rope_table, or NULL (no
+ *         rotation; rot is then ignored). The first rot (even, <= dim) channels
+ *         of a head turn: pairs (i, i + rot/2), or (2i, 2i+1) if interleaved:
+ *         x1' = fl32(fl32(x1 c) - fl32(x2 s)), x2' = fl32(fl32(x2 c) + fl32(x1 s)).
+ *         Positions past the table take its last row.
+ *   q     [rows, q_heads, dim] and q_out of the same type, or both NULL; q_out
+ *         may be q itself (same strides)
+ * Per touched page and head, with a = 0 where the page's slot 0 is written:
+ *   a' = max(a, max |new values|), magnitudes under 2^-64 taken as 0
+ *   new codes rne(fl32(x * fl32(127 / a'))); where a' > a the page's earlier
+ *   codes become rne(fl32(c * fl32(a / a'))).
+ * The tokens of a page are written in order; no two sequences of a call may
+ * write to the same page. Codes and magnitudes are bit-exact.
+ */
+LLMINT8_API llmint8_status llmint8_kv_append(const llmint8_kv_cache* cache, const llmint8_kv_batch* batch,
+                                             int dtype, const void* k, int64_t k_token, int64_t k_head,
+                                             const void* v, int64_t v_token, int64_t v_head,
+                                             const void* q, int64_t q_token, int64_t q_head,
+                                             void* q_out, int64_t q_out_token, int64_t q_out_head,
+                                             int64_t q_heads, const float* rope, int64_t rope_rows,
+                                             int64_t rot, int interleaved, void* stream);
+
+/*
+ * Reads the batch's tokens back: k, v [rows, heads, dim] in dtype, the values
+ * that the codes stand for, rounded once. n_b = len[b] reads a whole sequence.
+ */
+LLMINT8_API llmint8_status llmint8_kv_gather(const llmint8_kv_cache* cache, const llmint8_kv_batch* batch,
+                                             int dtype, void* k, int64_t k_token, int64_t k_head, void* v,
+                                             int64_t v_token, int64_t v_head, void* stream);
+
+/*
+ * Attention of the batch's rows over the cache (the rows' own tokens included,
+ * so append comes first). Query head i belongs to key/value head i / (q_heads /
+ * heads). A row at position p of a sequence of n tokens sees the tokens
+ *   j < n, and with causal != 0 only j <= p, and with window > 0 (causal only)
+ *   of these only j > p - window or j < sinks
+ * and gets o = sum_j softmax(scale q . k)_j v_j, rounded once, and (lse not
+ * NULL, fp32 [rows, q_heads]) log sum_j exp(scale q . k_j). A row that sees
+ * nothing gets zeros and -inf. Any mix of single tokens and longer runs is one
+ * call. Sums and statistics are fp32 or exact integers.
+ *   q_heads    a multiple of heads
+ *   scale      finite (usually 1 / sqrt(dim))
+ *   workspace  llmint8_kv_attention_workspace_bytes(...) bytes, 256-byte
+ *              aligned, contents on entry do not matter; NULL where that is 0
+ */
+LLMINT8_API size_t llmint8_kv_attention_workspace_bytes(const llmint8_kv_cache* cache,
+                                                        const llmint8_kv_batch* batch, int64_t q_heads,
+                                                        int64_t window, int64_t sinks);
+LLMINT8_API llmint8_status llmint8_kv_attention(const llmint8_kv_cache* cache, const llmint8_kv_batch* batch,
+                                                int dtype, const void* q, int64_t q_token, int64_t q_head,
+                                                int64_t q_heads, float scale, int causal, int64_t window,
+                                                int64_t sinks, void* out, int64_t out_token,
+                                                int64_t out_head, float* lse, void* workspace,
+                                                size_t workspace_bytes, void* stream);
+
 /* Largest T the fused GEMV route accepts for this K (0 if none). */
 LLMINT8_API int llmint8_gemv_max_rows(int64_t K);
 

@@ -26,6 +26,9 @@ __all__ = [
     "llmint8_dequantize_4bit", "llmint8_linear_4bit", "Linear4bit", "llmint8_linear_timed_ex",
     "llmint8_linear_backward_input_ex", "llmint8_dequantize_weight_t_ex",
     "llmint8_gemm_tile", "llmint8_linear_noalloc", "llmint8_noalloc_scratch_bytes",
+    "KVCache", "KVBatch", "llmint8_rope_table", "rope_frequencies", "llmint8_kv_append",
+    "llmint8_kv_gather", "llmint8_kv_attention", "llmint8_kv_attention_workspace_bytes",
+    "PagedSequences", "Int8SelfAttention",
 ]
 
 LLMINT8_PATH_AUTO = 0
@@ -51,6 +54,8 @@ EXPORTED_SYMBOLS = (
     "llmint8_dequantize_4bit", "llmint8_linear_4bit", "llmint8_linear_timed_ex",
     "llmint8_linear_backward_input_ex", "llmint8_dequantize_weight_t_ex",
     "llmint8_gemm_tile", "llmint8_linear_noalloc", "llmint8_noalloc_scratch_bytes",
+    "llmint8_rope_table", "llmint8_kv_append", "llmint8_kv_gather",
+    "llmint8_kv_attention_workspace_bytes", "llmint8_kv_attention",
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -143,6 +148,19 @@ def load_library():
     lib.llmint8_noalloc_scratch_bytes.restype = ctypes.c_size_t
     lib.llmint8_gemm_tile.argtypes = [_i64, _i64]
     lib.llmint8_gemm_tile.restype = ctypes.c_int
+    rows = [_vp, _i64, _i64]   # 16-bit rows: pointer, token stride, head stride
+    lib.llmint8_rope_table.argtypes = [ctypes.POINTER(ctypes.c_double), _i64, _i64, ctypes.c_double, _vp, _vp]
+    lib.llmint8_rope_table.restype = ctypes.c_int
+    lib.llmint8_kv_append.argtypes = [_vp, _vp, ctypes.c_int, *rows, *rows, *rows, *rows, _i64, _vp, _i64,
+                                      _i64, ctypes.c_int, _vp]
+    lib.llmint8_kv_append.restype = ctypes.c_int
+    lib.llmint8_kv_gather.argtypes = [_vp, _vp, ctypes.c_int, *rows, *rows, _vp]
+    lib.llmint8_kv_gather.restype = ctypes.c_int
+    lib.llmint8_kv_attention_workspace_bytes.argtypes = [_vp, _vp, _i64, _i64, _i64]
+    lib.llmint8_kv_attention_workspace_bytes.restype = ctypes.c_size_t
+    lib.llmint8_kv_attention.argtypes = [_vp, _vp, ctypes.c_int, *rows, _i64, ctypes.c_float, ctypes.c_int,
+                                         _i64, _i64, *rows, _vp, _vp, ctypes.c_size_t, _vp]
+    lib.llmint8_kv_attention.restype = ctypes.c_int
     lib.llmint8_gemv_max_rows.argtypes = [_i64]
     lib.llmint8_gemv_max_rows.restype = ctypes.c_int
     lib.llmint8_status_string.argtypes = [ctypes.c_int]
@@ -784,3 +802,8 @@ class Int8Linear:
         return Y.reshape(*shape[:-1], self.out_features)
 
     __call__ = forward
+
+
+from .kvcache import (  # noqa: E402 - the submodule uses the loader above
+    Int8SelfAttention, KVBatch, KVCache, PagedSequences, llmint8_kv_append, llmint8_kv_attention,
+    llmint8_kv_attention_workspace_bytes, llmint8_kv_gather, llmint8_rope_table, rope_frequencies)

@@ -234,6 +234,9 @@ llmint8_status run_backward_input(const void* dY, int64_t T, int64_t K, const in
 }  // namespace
 
 namespace llmint8 {
+llmint8_status abi_hip_status(hipError_t e) { return hip_status(e); }
+int abi_cu_count() { return device_cu_count(); }
+
 llmint8_status linear_static_scratch(const void* X, int dtype, int64_t T, int64_t K, const int8_t* Wq,
                                      const float* sW, int64_t N, float threshold, const void* bias,
                                      void* Y, ScratchSource scratch, size_t scratch_bytes, void* stream) {

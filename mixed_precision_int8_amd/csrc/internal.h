@@ -228,13 +228,19 @@ struct KvAttnArgs {
   KvRows q, o;
   float* lse;  // [T, q_heads] or null
   float scale;
-  int q_heads, causal, window, sinks;
-  int splits, split_tiles;  // parts of a context, and how many 64-token tiles a part has at least
-  float* part_o;            // [splits, T * q_heads, dim] unnormalised, where splits > 1
-  float* part_ml;           // [splits, T * q_heads, 2]
+  int bf16, q_heads, causal, window, sinks;
+  // Runs of rows with long contexts are cut into parts, for `extra` workgroups at
+  // most beyond one to each run and head (0: not cut); `slots` workgroups run at
+  // once. What the parts leave for the join: [max_parts, run, dim] and
+  // [max_parts, run, 2], and notes [T * q_heads, 2] of each row's parts.
+  int run, extra, slots, max_parts;
+  float* part_o;
+  float* part_ml;
+  int* notes;
 };
-int kv_attention_splits(const KvBatch& s, int heads, int q_heads, int64_t max_span, int num_cus,
-                        int* split_tiles);
-hipError_t launch_kv_attention(const KvAttnArgs& a, bool bf16, hipStream_t stream);
+int kv_attention_run(const KvBatch& s, int heads, int q_heads);  // rows of a run: 16, 32 or 64
+int kv_attention_extra(const KvBatch& s, int heads, int q_heads, int dim, int64_t max_span, int num_cus,
+                       int* slots);
+hipError_t launch_kv_attention(const KvAttnArgs& a, hipStream_t stream);
 
 }  // namespace llmint8

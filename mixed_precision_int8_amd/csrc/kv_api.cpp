@@ -132,15 +132,23 @@ llmint8_status llmint8_kv_gather(const llmint8_kv_cache* cache, const llmint8_kv
                                      static_cast<hipStream_t>(stream)));
 }
 
-// The work of an attention call: its routes and the bytes its parts take.
-static size_t kv_attention_plan(const llmint8_kv_batch* batch, int64_t window, int64_t sinks, KvAttnArgs* a) {
+// The route of an attention call and the bytes that it leaves for its join.
+static size_t kv_attention_plan(const llmint8_kv_batch* batch, int64_t window, int64_t sinks, void* workspace,
+                                KvAttnArgs* a) {
   const int64_t room = batch->width << a->c.page_shift;
   int64_t span = batch->max_len > 0 ? std::min(batch->max_len, room) : room;
-  // a run of 16 rows sees its window, the run itself and the sinks, each to whole tiles
-  if (window > 0) span = std::min(span, window + sinks + 192);
-  a->splits = kv_attention_splits(a->s, a->c.heads, a->q_heads, span, abi_cu_count(), &a->split_tiles);
-  if (a->splits <= 1) return 0;
-  return (size_t)a->splits * (size_t)a->s.T * (size_t)a->q_heads * (size_t)(a->c.dim + 2) * sizeof(float);
+  if (window > 0) span = std::min(span, window + sinks);
+  a->run = kv_attention_run(a->s, a->c.heads, a->q_heads);
+  a->extra = kv_attention_extra(a->s, a->c.heads, a->q_heads, a->c.dim, span, abi_cu_count(), &a->slots);
+  if (a->extra == 0) return 0;
+  a->max_parts = 2 * a->extra;  // parts of cut runs: each is longer than half of what the runs are cut by
+  const size_t rows = (size_t)a->max_parts * a->run;
+  if (workspace) {
+    a->part_o = static_cast<float*>(workspace);
+    a->part_ml = a->part_o + rows * a->c.dim;
+    a->notes = reinterpret_cast<int*>(a->part_ml + rows * 2);
+  }
+  return (rows * (a->c.dim + 2) + (size_t)a->s.T * a->q_heads * 2) * sizeof(float);
 }
 
 static llmint8_status check_kv_attention(const llmint8_kv_cache* cache, int64_t q_heads, int causal,
@@ -158,7 +166,7 @@ size_t llmint8_kv_attention_workspace_bytes(const llmint8_kv_cache* cache, const
   if (kv_operands(cache, batch, LLMINT8_DTYPE_F16, &a.c, &a.s, &empty) != LLMINT8_OK) return 0;
   if (check_kv_attention(cache, q_heads, 1, window, sinks) != LLMINT8_OK || empty) return 0;
   a.q_heads = (int)q_heads;
-  return kv_attention_plan(batch, window, sinks, &a);
+  return kv_attention_plan(batch, window, sinks, nullptr, &a);
 }
 
 llmint8_status llmint8_kv_attention(const llmint8_kv_cache* cache, const llmint8_kv_batch* batch, int dtype,
@@ -178,19 +186,18 @@ llmint8_status llmint8_kv_attention(const llmint8_kv_cache* cache, const llmint8
     return LLMINT8_ERR_INVALID_ARG;
   if (lse && !aligned(lse, 4)) return LLMINT8_ERR_INVALID_ARG;
   a.lse = lse;
+  a.bf16 = dtype == LLMINT8_DTYPE_BF16 ? 1 : 0;
   a.scale = scale;
   a.q_heads = (int)q_heads;
   a.causal = causal ? 1 : 0;
   a.window = (int)window;
   a.sinks = (int)sinks;
-  const size_t need = kv_attention_plan(batch, window, sinks, &a);
+  const size_t need = kv_attention_plan(batch, window, sinks, workspace, &a);
   if (need > 0) {
     if (!workspace || !aligned(workspace, kWsAlign)) return LLMINT8_ERR_INVALID_ARG;
     if (workspace_bytes < need) return LLMINT8_ERR_WORKSPACE;
-    a.part_o = static_cast<float*>(workspace);
-    a.part_ml = a.part_o + (size_t)a.splits * T * q_heads * D;
   }
-  return abi_hip_status(launch_kv_attention(a, dtype == LLMINT8_DTYPE_BF16, static_cast<hipStream_t>(stream)));
+  return abi_hip_status(launch_kv_attention(a, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -7,6 +7,14 @@
 
 namespace llmint8 {
 
+// A value that all lanes hold, moved to a scalar register.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32));
+  return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
 // Tokens of sequence b in this call: rows [row0, row0 + n), positions
 // [len - n, len). Every number is cut to what the buffers hold, so that no
 // content of cu, len or table makes a kernel leave them: cu to [0, T], n to
@@ -26,37 +34,67 @@ __device__ __forceinline__ KvSeq kv_seq(const KvBatch& s, int page_shift, int b)
   return q;
 }
 
+// kv_seq of a sequence that all lanes ask for
+__device__ __forceinline__ KvSeq kv_seq_uniform(const KvBatch& s, int page_shift, int b) {
+  KvSeq q = kv_seq(s, page_shift, b);
+  q.b = uniform(q.b);
+  q.row0 = uniform(q.row0);
+  q.n = uniform(q.n);
+  q.len = uniform(q.len);
+  return q;
+}
+
 // The sequence that work item `item` belongs to, where sequence b owns the items
 // from (cu[b] * per >> shift) + slack * b on. A sequence of n rows then has at
 // least (n * per >> shift) + slack items, which covers the tiles of 2^shift that
 // its n * per rows fill (slack 1) or the pages of 2^shift that n tokens reach
-// (slack 2), with no table of tile counts. Whole workgroup: the sequences
-// are counted in parallel, one round of loads for every kThreads of them.
-// Returns b and sets *first to its first item; -1 where no sequence owns the item
+// (slack 2), with no table of tile counts. Whole workgroup: the sequences are
+// counted in parallel, one round of loads for every kThreads of them, and the
+// owner hands its numbers, loaded in the same round, to the others (sh).
+// Sets *first to the sequence's first item; false where no sequence owns the item
 // (cu starts late, or falls).
 template <int kThreads>
-__device__ __forceinline__ int kv_find(const KvBatch& s, int item, int per, int shift, int slack,
-                                       int* first) {
+__device__ __forceinline__ bool kv_find(const KvBatch& s, int page_shift, int item, int per, int shift,
+                                        int slack, int (&sh)[4], KvSeq* out, int* first) {
+  if (s.B == 1) {
+    *out = kv_seq_uniform(s, page_shift, 0);
+    *first = (int)(((int64_t)out->row0 * per) >> shift);
+    return *first <= item;
+  }
   int b = -1;
   for (int b0 = 0; b0 < s.B; b0 += kThreads) {
     const int i = b0 + (int)threadIdx.x;
-    bool mine = false;
-    if (i < s.B) {
-      const int64_t c = min(max(s.cu[i], 0), s.T);
-      mine = (c * per >> shift) + (int64_t)slack * i <= item;
+    const int lane = min(i, s.B - 1);
+    const KvSeq q = kv_seq(s, page_shift, lane);
+    const int64_t at = (((int64_t)q.row0 * per) >> shift) + (int64_t)slack * lane;
+    const int mine = __syncthreads_count(i < s.B && at <= item);
+    if (mine > 0 && (int)threadIdx.x == mine - 1) {
+      sh[0] = q.row0;
+      sh[1] = q.n;
+      sh[2] = q.len;
+      sh[3] = (int)at;
     }
-    b += __syncthreads_count(mine);
+    b += mine;
+    if (mine < min(kThreads, s.B - b0)) break;
   }
-  if (b < 0) return b;
-  const int64_t c = min(max(s.cu[b], 0), s.T);
-  *first = (int)((c * per >> shift) + (int64_t)slack * b);
-  return b;
+  if (b < 0) return false;
+  __syncthreads();
+  out->b = b;
+  out->row0 = uniform(sh[0]);
+  out->n = uniform(sh[1]);
+  out->len = uniform(sh[2]);
+  *first = uniform(sh[3]);
+  return *first <= item;
 }
 
-// Page of token `tok` of sequence b, or -1 where the table names none that exists.
-__device__ __forceinline__ int kv_page(const KvBatch& s, int b, int entry, int64_t pages) {
-  const int p = s.table[(int64_t)b * s.width + min(entry, s.width - 1)];
-  return (entry < s.width && (uint32_t)p < (uint64_t)pages) ? p : -1;
+// Page that the table names for the tokens of an entry; may be any number. Tokens
+// past an entry's end of the table are past the sequence's end as well.
+__device__ __forceinline__ int kv_entry(const KvBatch& s, int b, int entry) {
+  return s.table[(int64_t)b * s.width + min(entry, s.width - 1)];
+}
+// The page itself, or -1 where there is none of that number.
+__device__ __forceinline__ int kv_page(int number, int64_t pages) {
+  return (uint32_t)number < (uint64_t)pages ? number : -1;
 }
 
 }  // namespace llmint8

@@ -22,6 +22,9 @@
 // so pages of any scale share a tile, and the row's sum takes each weight
 // without it.
 #include <math.h>
+#include <algorithm>
+
+#include <type_traits>
 
 #include "kv_common.h"
 
@@ -36,16 +39,41 @@ __device__ __forceinline__ v4i mfma_i8(const v4i& a, const v4i& b, const v4i& c)
   return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
 }
 
-__device__ __forceinline__ v4i load16(const int8_t* p) { return *reinterpret_cast<const v4i*>(p); }
+// STREAM: codes that nobody reads again (the hint keeps them from lingering in L2)
+template <bool STREAM>
+__device__ __forceinline__ v4i load16(const int8_t* p) {
+  if constexpr (STREAM) return __builtin_nontemporal_load(reinterpret_cast<const v4i*>(p));
+  return *reinterpret_cast<const v4i*>(p);
+}
 
-// over the four lanes that hold one query row (lanes n, n + 16, n + 32, n + 48)
+// over the four lanes that hold one query row (lanes n, n + 16, n + 32, n + 48): the swaps put the
+// other half's (the other rows of 16's) values into the second result
+__device__ __forceinline__ float swap32(float v, float* other) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  *other = __uint_as_float(r[1]);
+  return __uint_as_float(r[0]);
+}
+__device__ __forceinline__ float swap16(float v, float* other) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  *other = __uint_as_float(r[1]);
+  return __uint_as_float(r[0]);
+}
 __device__ __forceinline__ float row_max(float v) {
-  v = fmaxf(v, __shfl_xor(v, 16, 64));
-  return fmaxf(v, __shfl_xor(v, 32, 64));
+  float o;
+  v = swap32(v, &o);
+  v = swap16(fmaxf(v, o), &o);
+  return fmaxf(v, o);
 }
 __device__ __forceinline__ float row_sum(float v) {
-  v += __shfl_xor(v, 16, 64);
-  return v + __shfl_xor(v, 32, 64);
+  float o;
+  v = swap32(v, &o);
+  v = swap16(v + o, &o);
+  return v + o;
+}
+
+__device__ __forceinline__ uint2 pack4(const v4f& v, int bf16) {
+  return bf16 ? make_uint2(Act16<true>::pack2(v[0], v[1]), Act16<true>::pack2(v[2], v[3]))
+              : make_uint2(Act16<false>::pack2(v[0], v[1]), Act16<false>::pack2(v[2], v[3]));
 }
 
 // The tiles of 64 tokens that a run of rows at positions [pos_lo, pos_hi] sees:
@@ -68,293 +96,610 @@ __device__ __forceinline__ Span visible_span(int len, int pos_lo, int pos_hi, in
 
 }  // namespace
 
-template <int DP, bool BF16>
-__global__ __launch_bounds__(256) void kv_step(KvAttnArgs a) {
+// What a sequence asks of the call: its rows in runs of 16 RT (the query rows of a
+// head's group, token by token), and the tiles that any of them sees.
+struct SeqWork {
+  int runs, tiles;
+  Span span;
+};
+template <int RT>
+__device__ __forceinline__ SeqWork seq_work(const KvAttnArgs& a, const KvSeq& s) {
+  SeqWork w;
+  const int G = a.q_heads / a.c.heads;
+  w.runs = (int)(((int64_t)s.n * G + 16 * RT - 1) / (16 * RT));
+  w.span = visible_span(s.len, s.len - s.n, s.len - 1, a.causal, a.window, a.sinks);
+  w.tiles = max(w.span.count(), 1);  // rows that see nothing are written too
+  return w;
+}
+
+// A part of a run's tiles, the work of one workgroup: the tiles of every run and
+// head are cut into equal parts of at most `share` tiles, numbered sequence by
+// sequence, head by head, run by run.
+struct Part {
+  int h, run, part, parts;
+  int slot;  // of a part of several: where its result goes
+};
+// How finely the call is cut. With few runs and heads, as many parts as run at
+// once; with more, twice that many beyond the runs' own, which evens out runs of
+// different lengths. A part of its own costs about 8 us of loads that wait for
+// each other and of joining, so none gets less than `least` tiles (16: about 9 us
+// of work), and more where the runs by themselves fill half the chip. Measured
+// (32 query and 8 key/value heads of 128, us): 32 sequences of 2000-8000 tokens
+// 73 (85 cut into one part per resident workgroup, 102 uncut), 64 of 500-8000 95
+// (119 uncut), one of 131000 54.
+struct Cutting {
+  int64_t extra;  // parts beyond one to each run and head
+  int least;      // tiles of a part
+};
+__host__ __device__ inline Cutting cutting(int64_t runs, int slots) {
+  return {runs * 4 <= slots ? slots - runs : (int64_t)2 * slots, runs * 2 >= slots ? 48 : 16};
+}
+
+// Exclusive sums of two numbers over the workgroup's 256 threads, and their totals.
+__device__ __forceinline__ void sum_256(int64_t& x, int64_t& y, int64_t (&sums)[8], int64_t* all_x, int64_t* all_y) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t x0 = x, y0 = y;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int64_t u = __shfl_up(x, o, 64), v = __shfl_up(y, o, 64);
+    if (lane >= o) {
+      x += u;
+      y += v;
+    }
+  }
+  __syncthreads();
+  if (lane == 63) {
+    sums[wave] = x;
+    sums[4 + wave] = y;
+  }
+  __syncthreads();
+  *all_x = *all_y = 0;
+  x -= x0;
+  y -= y0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (k < wave) {
+      x += sums[k];
+      y += sums[4 + k];
+    }
+    *all_x += sums[k];
+    *all_y += sums[4 + k];
+  }
+}
+
+// Part w of the call: the sequences' tiles are summed 256 sequences at a time,
+// which gives the share (a.extra parts at most beyond one to each run and head),
+// then their parts. False past the last part.
+template <int RT>
+__device__ __forceinline__ bool find_part(const KvAttnArgs& a, int w, int64_t (&sums)[8], int (&found)[8], KvSeq* seq,
+                                          Part* p) {
+  const int tid = threadIdx.x, H = a.c.heads;
+  int64_t tiles = 0, runs = 0;
+  KvSeq q{};
+  SeqWork work{};
+  for (int b0 = 0; b0 < a.s.B; b0 += 256) {
+    q = kv_seq(a.s, a.c.page_shift, min(b0 + tid, a.s.B - 1));
+    work = seq_work<RT>(a, q);
+    int64_t x = 0, y = b0 + tid < a.s.B ? (int64_t)H * work.runs : 0, all_x, all_y;
+    x = y * work.tiles;
+    sum_256(x, y, sums, &all_x, &all_y);
+    tiles += all_x;
+    runs += all_y;
+  }
+  const Cutting how = cutting(runs, a.slots);
+  const int64_t extra = min((int64_t)a.extra, how.extra);
+  const int share = (int)max((int64_t)how.least, (tiles + extra - 1) / extra);
+  int64_t before = 0, cut = 0;
+  if (tid == 0) found[0] = -1;
+  for (int b0 = 0; b0 < a.s.B; b0 += 256) {
+    if (a.s.B > 256) {
+      q = kv_seq(a.s, a.c.page_shift, min(b0 + tid, a.s.B - 1));
+      work = seq_work<RT>(a, q);
+    }
+    const int parts = (work.tiles + share - 1) / share;
+    const int64_t mine = b0 + tid < a.s.B ? (int64_t)H * work.runs * parts : 0;
+    int64_t x = mine, y = parts > 1 ? mine : 0, all_x, all_y;
+    sum_256(x, y, sums, &all_x, &all_y);
+    x += before;
+    if (x <= w && w < x + mine) {
+      const int in = (int)(w - x);
+      found[0] = b0 + tid;
+      found[1] = q.row0;
+      found[2] = q.n;
+      found[3] = q.len;
+      found[4] = in;
+      found[5] = parts;
+      found[6] = (int)(y + cut) + in;
+    }
+    before += all_x;
+    cut += all_y;
+  }
+  __syncthreads();
+  seq->b = uniform(found[0]);
+  if (seq->b < 0) return false;
+  seq->row0 = uniform(found[1]);
+  seq->n = uniform(found[2]);
+  seq->len = uniform(found[3]);
+  p->parts = uniform(found[5]);
+  p->slot = uniform(found[6]);
+  const int in = uniform(found[4]), run = in / p->parts;
+  const SeqWork mine = seq_work<RT>(a, *seq);
+  p->part = in - run * p->parts;
+  p->h = run / mine.runs;
+  p->run = run - p->h * mine.runs;
+  return true;
+}
+
+// A workgroup takes the tiles of a run of 16 RT rows: 4 / RT wavefronts to each
+// sixteen, which share its tiles, each with its own running maximum, sum and
+// output, and join at the end. The sixteens go over the same tiles at about the
+// same time, so that the codes come from memory once. K's codes of a wavefront's next
+// tile are asked for as soon as the first product has read the present ones, V's
+// after the second product, into the same registers: a tile is always on the way
+// while another is computed, and three wavefronts fit a SIMD (dim 128).
+//
+// CUT: long runs are cut into parts (find_part); what a part has of its run goes
+// to the workspace for kv_join. Otherwise one workgroup to each run and head.
+// ONE: a tile is within one page (pages of 64 tokens and more), whose address is
+// then scalar. FULL: dim = DP.
+template <int DP, bool FULL, bool ONE, bool CUT, int RT>
+__global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void kv_step(KvAttnArgs a) {
+  constexpr int WT = 4 / RT;  // wavefronts that share a sixteen's tiles
   constexpr int NK = DP / 64;  // 64-channel steps of the first product
   constexpr int ND = DP / 16;  // 16-channel blocks of the second
-  __shared__ float sh_o[2][16][DP];
+  __shared__ float sh_o[RT < 4 ? 2 : 1][16][DP];
   __shared__ float sh_ml[4][16][2];
-  const int P = 1 << a.c.page_shift, D = a.c.dim, H = a.c.heads, G = a.q_heads / H;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __shared__ int sh_seq[4];
+  __shared__ int sh_found[8];
+  __shared__ int64_t sh_sums[8];
+  const int D = FULL ? DP : a.c.dim;
+  const int shift = a.c.page_shift, P = 1 << shift, H = a.c.heads, G = a.q_heads / H;
+  const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
   const int g = lane >> 4, nn = lane & 15;
-  int first;
-  const int b = kv_find<256>(a.s, blockIdx.x, G, 4, 1, &first);
-  if (b < 0) return;
-  const KvSeq sq = kv_seq(a.s, a.c.page_shift, b);
-  const int h = blockIdx.y;
-  const int row_tile = (int)blockIdx.x - first;
-  const int rows = sq.n * G;
-  if (row_tile * 16 >= rows) return;
-  const int r = row_tile * 16 + nn;
-  const bool live = r < rows;
-  const int tok = min(r, rows - 1) / G, head = min(r, rows - 1) - tok * G;
+  const int64_t page_bytes = (int64_t)P * D;
+  // a lane's place in a tile's codes: K row 16 (nn / 4) + nn % 4 (+ 4 j), channels 16 g (+ 64 ks);
+  // V channel nn (+ 16 d), tokens 16 g ..
+  const int k_tok = 16 * (nn >> 2), v_tok = 16 * g;
+  uint32_t k_off[NK], v_off[ND];
+#pragma unroll
+  for (int ks = 0; ks < NK; ++ks) {
+    const int c0 = ks * 64 + g * 16;  // channels past dim: any codes do, q is zero there
+    k_off[ks] = (uint32_t)((nn & 3) + (ONE ? k_tok : 0)) * D + (FULL || c0 < D ? c0 : 0);
+  }
+#pragma unroll
+  for (int d = 0; d < ND; ++d)
+    v_off[d] = (uint32_t)(FULL ? d * 16 + nn : min(d * 16 + nn, D - 1)) * P + (ONE ? v_tok : 0);
+
+  KvSeq sq;
+  Part p{};
+  if (CUT) {
+    if (!find_part<RT>(a, blockIdx.x, sh_sums, sh_found, &sq, &p)) return;
+  } else {
+    int first;
+    if (!kv_find<256>(a.s, shift, blockIdx.y, G, RT == 4 ? 6 : 3 + RT, 1, sh_seq, &sq, &first)) return;
+    p.h = blockIdx.x;  // neighbours share a page
+    p.run = (int)blockIdx.y - first;
+    p.parts = 1;
+    if (sq.n == 0 || p.run >= seq_work<RT>(a, sq).runs) return;
+  }
+  const int h = p.h;
+  const int b = sq.b, rows = sq.n * G, row_first = p.run * 16 * RT;
+  const int row_mine = row_first + 16 * (wave / WT);  // of this wavefront's sixteen
+  const int r = min(row_mine + nn, rows - 1), tok = r / G;
   const int pos = sq.len - sq.n + tok;
   const int64_t qrow = sq.row0 + tok;
-  const int qh = h * G + head;
+  const int qh = h * G + (r - tok * G);
+  const int pos_lo = sq.len - sq.n + row_first / G;  // of the run
+  const int pos_hi = sq.len - sq.n + min(row_first + 16 * RT - 1, rows - 1) / G;
+  const Span span = CUT ? seq_work<RT>(a, sq).span
+                        : visible_span(sq.len, pos_lo, pos_hi, a.causal, a.window, a.sinks);
+  int i0 = 0, i1 = span.count();
+  if (CUT && p.parts > 1) {
+    const int tiles = i1;
+    i0 = (int)((int64_t)tiles * p.part / p.parts);
+    i1 = (int)((int64_t)tiles * (p.part + 1) / p.parts);
+  }
+
+  // the numbers of a tile's pages: of the K rows that the lane loads, of the tokens that it holds
+  struct Pages {
+    int k, v;
+  };
+  auto pages_of = [&](int it) {
+    const int base = span.tile(it) << 6;
+    Pages p;
+    if (ONE) {
+      p.k = p.v = kv_entry(a.s, b, base >> shift);
+    } else {
+      p.k = kv_entry(a.s, b, (base + k_tok) >> shift);
+      p.v = kv_entry(a.s, b, (base + v_tok) >> shift);
+    }
+    return p;
+  };
+  v4i kf[4][NK], vf[ND];
+  auto load_k = [&](int it, const Pages& p, float* ak, float* av, int* page) {
+    const int base = span.tile(it) << 6;
+    const int pk = kv_page(ONE ? uniform(p.k) : p.k, a.c.pages), pv = kv_page(ONE ? uniform(p.v) : p.v, a.c.pages);
+    const int8_t* kp = a.c.K + ((int64_t)max(pk, 0) * H + h) * page_bytes +
+                       ((ONE ? base : base + k_tok) & (P - 1)) * D;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int ks = 0; ks < NK; ++ks) kf[j][ks] = load16<RT == 1>(kp + (k_off[ks] + 4 * j * D));
+    const int64_t hv = (int64_t)max(pv, 0) * H + h;
+    *ak = a.c.aK[hv];
+    *av = a.c.aV[hv];
+    *page = pv;
+  };
+  auto load_v = [&](int it, const Pages& p) {
+    const int base = span.tile(it) << 6;
+    const int pv = kv_page(ONE ? uniform(p.v) : p.v, a.c.pages);
+    const int8_t* vp = a.c.V + ((int64_t)max(pv, 0) * H + h) * page_bytes + ((ONE ? base : base + v_tok) & (P - 1));
+#pragma unroll
+    for (int d = 0; d < ND; ++d) vf[d] = load16<RT == 1>(vp + v_off[d]);
+  };
+
+  int it = row_mine < rows ? i0 + wave % WT : i1, page = -1;
+  float ak = 0.0f, av = 0.0f;
+  Pages next{-1, -1};
 
   // q: 16-bit integers in two planes, and what one unit of S stands for
   v4i qhi[NK], qlo[NK];
   float unit;
   {
-    const uint16_t* qp = a.q.p + qrow * a.q.token + (int64_t)qh * a.q.head;
-    float f[NK][16], m = 0.0f;
+    uint32_t w[NK][8];
+    {
+      const uint16_t* qp = a.q.p + qrow * a.q.token + (int64_t)qh * a.q.head;
 #pragma unroll
-    for (int ks = 0; ks < NK; ++ks) {
-      const int c0 = ks * 64 + g * 16;
-      uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-      if (c0 < D) {
-        w[0] = *reinterpret_cast<const uint4*>(qp + c0);
-        w[1] = *reinterpret_cast<const uint4*>(qp + c0 + 8);
-      }
-      const uint32_t* u = &w[0].x;
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        f[ks][j] = Act16<BF16>::to_f32((u[j >> 1] >> (16 * (j & 1))) & 0xffffu);
-        m = fmaxf(m, fabsf(f[ks][j]));
+      for (int ks = 0; ks < NK; ++ks) {
+        const int c0 = ks * 64 + g * 16;
+        uint4 x = make_uint4(0, 0, 0, 0), y = x;
+        if (FULL || c0 < D) {
+          x = *reinterpret_cast<const uint4*>(qp + c0);
+          y = *reinterpret_cast<const uint4*>(qp + c0 + 8);
+        }
+        w[ks][0] = x.x, w[ks][1] = x.y, w[ks][2] = x.z, w[ks][3] = x.w;
+        w[ks][4] = y.x, w[ks][5] = y.y, w[ks][6] = y.z, w[ks][7] = y.w;
       }
     }
-    m = row_max(m);
-    const float sc = m > 0.0f ? 32639.0f / m : 0.0f;
-    unit = m * (1.0f / 32639.0f) * a.scale * 1.44269504088896341f * (1.0f / 127.0f);
+    if (it < i1) {
+      const Pages p = pages_of(it);
+      next = pages_of(min(it + WT, i1 - 1));
+      load_k(it, p, &ak, &av, &page);
+      load_v(it, p);
+    }
+    {
+      float f[NK][16], m = 0.0f;
+      if (a.bf16) {
 #pragma unroll
-    for (int ks = 0; ks < NK; ++ks) {
-      uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
+        for (int ks = 0; ks < NK; ++ks)
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const int v = (int)rintf(f[ks][j] * sc);
-        const int vh = (v + 128) >> 8;
-        hi[j >> 2] |= (uint32_t)(vh & 0xff) << (8 * (j & 3));
-        lo[j >> 2] |= (uint32_t)((v - (vh << 8)) & 0xff) << (8 * (j & 3));
+          for (int j = 0; j < 16; ++j) f[ks][j] = bf16_bits_to_float((w[ks][j >> 1] >> (16 * (j & 1))) & 0xffffu);
+      } else {
+#pragma unroll
+        for (int ks = 0; ks < NK; ++ks)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) f[ks][j] = half_bits_to_float((w[ks][j >> 1] >> (16 * (j & 1))) & 0xffffu);
       }
-      qhi[ks] = v4i{(int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
-      qlo[ks] = v4i{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3]};
+#pragma unroll
+      for (int ks = 0; ks < NK; ++ks)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) m = fmaxf(m, fabsf(f[ks][j]));
+      m = row_max(m);
+      const float sc = m > 0.0f ? 32639.0f / m : 0.0f;
+      unit = m * (1.0f / 32639.0f) * a.scale * 1.44269504088896341f * (1.0f / 127.0f);
+#pragma unroll
+      for (int ks = 0; ks < NK; ++ks) {
+        uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const int v = (int)rintf(f[ks][j] * sc);
+          const int vh = (v + 128) >> 8;
+          hi[j >> 2] |= (uint32_t)(vh & 0xff) << (8 * (j & 3));
+          lo[j >> 2] |= (uint32_t)((v - (vh << 8)) & 0xff) << (8 * (j & 3));
+        }
+        qhi[ks] = v4i{(int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+        qlo[ks] = v4i{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3]};
+      }
     }
   }
-
-  // this part's share of the tiles that any row of the run sees
-  const int pos_lo = sq.len - sq.n + row_tile * 16 / G;
-  const int pos_hi = sq.len - sq.n + (min(row_tile * 16 + 15, rows - 1)) / G;
-  const Span span = visible_span(sq.len, pos_lo, pos_hi, a.causal, a.window, a.sinks);
-  const int total = span.count();
-  const int share = max(a.split_tiles, (total + a.splits - 1) / a.splits);
-  const int i0 = min((int)blockIdx.z * share, total), i1 = min(i0 + share, total);
 
   v4f acc[ND];
 #pragma unroll
   for (int d = 0; d < ND; ++d) acc[d] = v4f{0, 0, 0, 0};
   float m_run = kNegInf, l_run = 0.0f;
-  const int64_t page_bytes = (int64_t)P * D;
-  for (int it = i0 + wave; it < i1; it += 4) {
-    const int base = span.tile(it) << 6;
-    // pages of the token rows that this lane loads and of the tokens that it holds
-    const int tk = base + 16 * (nn >> 2), tv = base + 16 * g;
-    const int pk = kv_page(a.s, b, tk >> a.c.page_shift, a.c.pages);
-    const int pv = kv_page(a.s, b, tv >> a.c.page_shift, a.c.pages);
-    const int8_t* kp = a.c.K + ((int64_t)max(pk, 0) * H + h) * page_bytes +
-                       ((tk & (P - 1)) + (nn & 3)) * D;
-    const int64_t hv = (int64_t)max(pv, 0) * H + h;
-    const int8_t* vp = a.c.V + hv * page_bytes + (tv & (P - 1));
-    v4i kf[4][NK], vf[ND];
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-      for (int ks = 0; ks < NK; ++ks) {
-        const int c0 = ks * 64 + g * 16;
-        kf[t][ks] = load16(kp + 4 * t * D + (c0 < D ? c0 : 0));
-      }
-#pragma unroll
-    for (int d = 0; d < ND; ++d) vf[d] = load16(vp + (int64_t)min(d * 16 + nn, D - 1) * P);
-    const float ak = a.c.aK[hv], av = a.c.aV[hv];
+  // the last token that a row sees, but for its window; < 0: none
+  const int last = a.causal ? min(pos, sq.len - 1) : sq.len - 1;
+  const int all_end = a.causal ? min(pos_lo, sq.len - 1) : sq.len - 1;  // seen by every row, up to its window
+  const int all_begin = a.window > 0 ? pos_hi - a.window + 1 : 0;
 
+  auto tile = [&](auto more) {
+    constexpr bool MORE = decltype(more)::value;
+    const int base = span.tile(it) << 6;
+    // The page numbers of the tile after next go out before the next tile's codes: loads
+    // complete in order, and a wait for them must not be one for these.
+    Pages after{-1, -1};
+    if (MORE) after = pages_of(min(it + 2 * WT, i1 - 1));
     // S in units of q's and the page's scales
-    float u[16];
-    const float fk = unit * ak;
+    const float akh = ak;
     // a page of zeros takes the smallest scale there is: its weights only enter the row's sum, and
     // must not set the scale of the others'
     const float vs = (av > kMinMag ? av : kMinMag) * (1.0f / 127.0f);
     const float lv = __builtin_amdgcn_logf(vs);  // log2
+    v4i s[4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      v4i s = {0, 0, 0, 0};
+      for (int j = 0; j < 4; ++j) {
+        s[j] = v4i{0, 0, 0, 0};
 #pragma unroll
-      for (int ks = 0; ks < NK; ++ks) s = mfma_i8(kf[t][ks], qhi[ks], s);
+        for (int ks = 0; ks < NK; ++ks) s[j] = mfma_i8(kf[j][ks], qhi[ks], s[j]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[i] <<= 8;
+        for (int i = 0; i < 4; ++i) s[j][i] <<= 8;
+      }
 #pragma unroll
-      for (int ks = 0; ks < NK; ++ks) s = mfma_i8(kf[t][ks], qlo[ks], s);
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) u[4 * t + i] = __builtin_fmaf((float)s[i], fk, lv);
+        for (int ks = 0; ks < NK; ++ks) s[j] = mfma_i8(kf[j][ks], qlo[ks], s[j]);
+    const int here = page;
+    if (MORE) load_k(it + WT, next, &ak, &av, &page);
+    {
+      float u[16];
+      const float fk = unit * akh;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u[4 * j + i] = __builtin_fmaf((float)s[j][i], fk, lv);
+      // what a row does not see; tiles inside every row's range need no look at single tokens
+      if (base + 63 > all_end || base < all_begin || (ONE ? here < 0 : __any(here < 0))) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const int x = base + v_tok + j;
+          const bool see = here >= 0 && x <= last && (a.window <= 0 || x > pos - a.window || x < a.sinks);
+          u[j] = see ? u[j] : kNegInf;
+        }
+      }
+      float mt = u[0];
+#pragma unroll
+      for (int j = 1; j < 16; ++j) mt = fmaxf(mt, u[j]);
+      mt = row_max(mt);
+      const float mt0 = mt == kNegInf ? 0.0f : mt;
+      if (__any(mt > m_run)) {  // a new maximum of some row: what was summed moves to it
+        const float m_new = fmaxf(m_run, mt);
+        const float alpha = m_run == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m_run - m_new);
+        m_run = m_new;
+        l_run *= alpha;
+#pragma unroll
+        for (int d = 0; d < ND; ++d) acc[d] *= alpha;
+      }
+      const float beta = mt == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mt - m_run);
+      float sum = 0.0f;
+      uint32_t w[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const float e = __builtin_amdgcn_exp2f(u[j] - mt0);
+        sum += e;
+        // rne(32639 e) + 128 in the low 16 bits: high plane, and low plane + 128
+        w[j] = __float_as_uint(__builtin_fmaf(e, 32639.0f, 12582912.0f + 128.0f));
+      }
+      l_run = __builtin_fmaf(sum * beta, __builtin_amdgcn_rcpf(vs), l_run);
+      v4i phi, plo;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t h01 = __builtin_amdgcn_perm(w[4 * j + 1], w[4 * j], 0x0c0c0501u);
+        const uint32_t h23 = __builtin_amdgcn_perm(w[4 * j + 3], w[4 * j + 2], 0x0c0c0501u);
+        const uint32_t l01 = __builtin_amdgcn_perm(w[4 * j + 1], w[4 * j], 0x0c0c0400u);
+        const uint32_t l23 = __builtin_amdgcn_perm(w[4 * j + 3], w[4 * j + 2], 0x0c0c0400u);
+        phi[j] = (int)__builtin_amdgcn_perm(h23, h01, 0x05040100u);
+        plo[j] = (int)(__builtin_amdgcn_perm(l23, l01, 0x05040100u) ^ 0x80808080u);
+      }
+      const float bu = beta * (1.0f / 32639.0f);
+#pragma unroll
+      for (int d = 0; d < ND; ++d) {
+        v4i o = mfma_i8(vf[d], phi, v4i{0, 0, 0, 0});
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] <<= 8;
+        o = mfma_i8(vf[d], plo, o);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[d][i] = __builtin_fmaf((float)o[i], bu, acc[d][i]);
+      }
     }
-    // what the row does not see
-    const int last = a.causal ? min(pos, sq.len - 1) : sq.len - 1;  // < 0: nothing
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const int t = tv + j;
-      const bool see = pv >= 0 && t <= last && (a.window <= 0 || t > pos - a.window || t < a.sinks);
-      u[j] = see ? u[j] : kNegInf;
-    }
-    float mt = u[0];
-#pragma unroll
-    for (int j = 1; j < 16; ++j) mt = fmaxf(mt, u[j]);
-    mt = row_max(mt);
-    const float mt0 = mt == kNegInf ? 0.0f : mt;
-    const float m_new = fmaxf(m_run, mt);
-    const float m0 = m_new == kNegInf ? 0.0f : m_new;
-    const float alpha = __builtin_amdgcn_exp2f(m_run - m0), beta = __builtin_amdgcn_exp2f(mt - m0);
-    m_run = m_new;
-    float sum = 0.0f;
-    uint32_t w[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const float e = __builtin_amdgcn_exp2f(u[j] - mt0);
-      sum += e;
-      // rne(32639 e) + 128 in the low 16 bits: high plane, and low plane + 128
-      w[j] = __builtin_bit_cast(uint32_t, __builtin_fmaf(e, 32639.0f, 12582912.0f + 128.0f));
-    }
-    l_run = l_run * alpha + sum * beta * __builtin_amdgcn_rcpf(vs);
-    v4i phi, plo;
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const uint32_t h01 = __builtin_amdgcn_perm(w[4 * t + 1], w[4 * t], 0x0c0c0501u);
-      const uint32_t h23 = __builtin_amdgcn_perm(w[4 * t + 3], w[4 * t + 2], 0x0c0c0501u);
-      const uint32_t l01 = __builtin_amdgcn_perm(w[4 * t + 1], w[4 * t], 0x0c0c0400u);
-      const uint32_t l23 = __builtin_amdgcn_perm(w[4 * t + 3], w[4 * t + 2], 0x0c0c0400u);
-      phi[t] = (int)__builtin_amdgcn_perm(h23, h01, 0x05040100u);
-      plo[t] = (int)(__builtin_amdgcn_perm(l23, l01, 0x05040100u) ^ 0x80808080u);
-    }
-    const float bu = beta * (1.0f / 32639.0f);
-#pragma unroll
-    for (int d = 0; d < ND; ++d) {
-      v4i o = mfma_i8(vf[d], phi, v4i{0, 0, 0, 0});
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] <<= 8;
-      o = mfma_i8(vf[d], plo, o);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[d][i] = __builtin_fmaf((float)o[i], bu, acc[d][i] * alpha);
-    }
+    if (MORE) load_v(it + WT, next);
+    next = after;
+  };
+  // the last tile stands alone, so that the loop's loads are unconditional and its waits exact
+  if (it < i1) {
+    for (; it + WT < i1; it += WT) tile(std::true_type{});
+    tile(std::false_type{});
   }
 
-  // join the four wavefronts
+  // join the WT wavefronts of a sixteen
   l_run = row_sum(l_run);
-  if (g == 0) {
-    sh_ml[wave][nn][0] = m_run;
-    sh_ml[wave][nn][1] = l_run;
-  }
-  __syncthreads();
-  float m_all = sh_ml[0][nn][0];
-#pragma unroll
-  for (int w = 1; w < 4; ++w) m_all = fmaxf(m_all, sh_ml[w][nn][0]);
-  const float m0 = m_all == kNegInf ? 0.0f : m_all;
-  float l_all = 0.0f;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) l_all += sh_ml[w][nn][1] * __builtin_amdgcn_exp2f(sh_ml[w][nn][0] - m0);
-  const float mine = __builtin_amdgcn_exp2f(m_run - m0);
-#pragma unroll
-  for (int d = 0; d < ND; ++d) acc[d] *= mine;
-#pragma unroll
-  for (int half = 2; half > 0; half >>= 1) {
-    if (wave >= half && wave < 2 * half)
-#pragma unroll
-      for (int d = 0; d < ND; ++d) *reinterpret_cast<v4f*>(&sh_o[wave - half][nn][d * 16 + 4 * g]) = acc[d];
-    __syncthreads();
-    if (wave < half)
-#pragma unroll
-      for (int d = 0; d < ND; ++d) acc[d] += *reinterpret_cast<const v4f*>(&sh_o[wave][nn][d * 16 + 4 * g]);
-    __syncthreads();
-  }
-  if (wave != 0 || !live) return;
-  const int64_t row = qrow * a.q_heads + qh;
-  if (a.splits > 1) {
-    const int64_t at = (int64_t)blockIdx.z * ((int64_t)a.s.T * a.q_heads) + row;
-#pragma unroll
-    for (int d = 0; d < ND; ++d)
-      if (d * 16 < D) *reinterpret_cast<v4f*>(a.part_o + at * D + d * 16 + 4 * g) = acc[d];
+  const int t = wave / WT, w0 = t * WT;
+  if (WT > 1) {
     if (g == 0) {
-      a.part_ml[at * 2] = m_all;
-      a.part_ml[at * 2 + 1] = l_all;
+      sh_ml[wave][nn][0] = m_run;
+      sh_ml[wave][nn][1] = l_run;
     }
-    return;
-  }
-  const float inv = l_all > 0.0f ? 1.0f / l_all : 0.0f;
-  uint16_t* op = a.o.p + qrow * a.o.token + (int64_t)qh * a.o.head;
+    __syncthreads();
+    float m_all = m_run;
 #pragma unroll
-  for (int d = 0; d < ND; ++d)
-    if (d * 16 < D)
-      *reinterpret_cast<uint2*>(op + d * 16 + 4 * g) = make_uint2(Act16<BF16>::pack2(acc[d][0] * inv, acc[d][1] * inv),
-                                                                 Act16<BF16>::pack2(acc[d][2] * inv, acc[d][3] * inv));
-  if (a.lse && g == 0) a.lse[row] = l_all > 0.0f ? (m_all + log2f(l_all)) * 0.693147180559945309f : kNegInf;
+    for (int w = 0; w < WT; ++w) m_all = fmaxf(m_all, sh_ml[w0 + w][nn][0]);
+    const float m0 = m_all == kNegInf ? 0.0f : m_all;
+    const float mine = __builtin_amdgcn_exp2f(m_run - m0);
+    m_run = m_all;
+    l_run = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WT; ++w) l_run += sh_ml[w0 + w][nn][1] * __builtin_amdgcn_exp2f(sh_ml[w0 + w][nn][0] - m0);
+#pragma unroll
+    for (int d = 0; d < ND; ++d) acc[d] *= mine;
+    const int sub = wave % WT;
+#pragma unroll
+    for (int half = WT / 2; half > 0; half >>= 1) {
+      if (sub >= half && sub < 2 * half)
+#pragma unroll
+        for (int d = 0; d < ND; ++d) *reinterpret_cast<v4f*>(&sh_o[t * (WT / 2) + sub - half][nn][d * 16 + 4 * g]) = acc[d];
+      __syncthreads();
+      if (sub < half)
+#pragma unroll
+        for (int d = 0; d < ND; ++d) acc[d] += *reinterpret_cast<const v4f*>(&sh_o[t * (WT / 2) + sub][nn][d * 16 + 4 * g]);
+      if (half > 1) __syncthreads();
+    }
+  }
+  // which parts there are of a row, for the join
+  if (CUT && p.part == 0 && g == 0 && wave % WT == 0 && row_mine + nn < rows)
+    *reinterpret_cast<v2i*>(a.notes + (qrow * a.q_heads + qh) * 2) =
+        v2i{p.parts > 1 ? (p.slot << 6 | 16 * t | nn) : -1, p.parts};
+  if (wave % WT == 0 && row_mine < rows) {
+    if (CUT && p.parts > 1) {
+      const int64_t to = (int64_t)p.slot * (16 * RT) + 16 * t + nn;
+      if (g == 0) *reinterpret_cast<v2f*>(a.part_ml + to * 2) = v2f{m_run, l_run};
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+        if (FULL || d * 16 < D) *reinterpret_cast<v4f*>(a.part_o + to * D + d * 16 + 4 * g) = acc[d];
+    } else if (row_mine + nn < rows) {
+      const float inv = l_run > 0.0f ? 1.0f / l_run : 0.0f;
+      uint16_t* op = a.o.p + qrow * a.o.token + (int64_t)qh * a.o.head;
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+        if (FULL || d * 16 < D)
+          *reinterpret_cast<uint2*>(op + d * 16 + 4 * g) = pack4(acc[d] * inv, a.bf16);
+      if (a.lse && g == 0)
+        a.lse[qrow * a.q_heads + qh] = l_run > 0.0f ? (m_run + log2f(l_run)) * 0.693147180559945309f : kNegInf;
+    }
+  }
 }
 
-// Joins the parts of a row: a wavefront to a row.
-template <bool BF16>
+// Joins the parts of the rows that have several, ROWS rows to a workgroup:
+// groups of lanes that hold a row's channels four by four take every (256 / ROWS
+// / group)-th part, four parts to a round of loads.
+template <int ROWS>
 __global__ __launch_bounds__(256) void kv_join(KvAttnArgs a) {
-  const int64_t rows = (int64_t)a.s.T * a.q_heads;
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
-  if (row >= rows) return;
+  constexpr int kLanes = 256 / ROWS;
+  __shared__ v4f sh_o[256];
+  __shared__ float sh_ml[256][2];
+  const int D = a.c.dim, per = D >> 2, groups = kLanes / per;
+  const int tid = threadIdx.x % kLanes, first = threadIdx.x - tid;
+  const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / kLanes;
   const int t = (int)(row / a.q_heads);
-  const int last = min(max(a.s.cu[a.s.B], 0), a.s.T);
-  if (t >= last) return;  // rows past the batch are not written
-  float m = kNegInf;
-  for (int s = 0; s < a.splits; ++s) m = fmaxf(m, a.part_ml[(s * rows + row) * 2]);
-  const float m0 = m == kNegInf ? 0.0f : m;
-  const int D = a.c.dim;
-  float l = 0.0f;
+  // rows outside the batch have no note
+  const bool in = t >= max(a.s.cu[0], 0) && t < min(a.s.cu[a.s.B], a.s.T);
+  const v2i note = in ? *reinterpret_cast<const v2i*>(a.notes + row * 2) : v2i{-1, 0};
+  const int slot = note[0] >> 6, nn = note[0] & 63;
+  const int parts = note[0] < 0 || note[1] < 0 || note[1] > a.max_parts - slot ? 0 : note[1];
+  if (ROWS == 1 && parts == 0) return;
+  const int64_t qrow = t;
+  const int qh = (int)(row - (int64_t)t * a.q_heads);
+  const int grp = tid / per, c = tid - grp * per;
+  float m = kNegInf, l = 0.0f;
   v4f o = {0, 0, 0, 0};
-  for (int s = 0; s < a.splits; ++s) {
-    const float w = __builtin_amdgcn_exp2f(a.part_ml[(s * rows + row) * 2] - m0);
-    if (w == 0.0f) continue;
-    l += w * a.part_ml[(s * rows + row) * 2 + 1];
-    if (lane * 4 < D) {
-      const v4f p = *reinterpret_cast<const v4f*>(a.part_o + (s * rows + row) * D + lane * 4);
+  if (grp < groups)
+    for (int p0 = grp; p0 < parts; p0 += 4 * groups) {
+      v2f ml[4];
+      v4f x[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] += w * p[i];
+      for (int k = 0; k < 4; ++k) {
+        const int p = min(p0 + k * groups, parts - 1);
+        const int64_t from = (int64_t)(slot + p) * a.run + nn;
+        ml[k] = *reinterpret_cast<const v2f*>(a.part_ml + from * 2);
+        x[k] = *reinterpret_cast<const v4f*>(a.part_o + from * D + c * 4);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const bool mine = p0 + k * groups < parts;
+        const float mk = mine ? ml[k][0] : kNegInf;
+        const float top = fmaxf(m, mk), ref = top == kNegInf ? 0.0f : top;
+        const float keep = __builtin_amdgcn_exp2f(m - ref), add = __builtin_amdgcn_exp2f(mk - ref);
+        m = top;
+        l = l * keep + ml[k][1] * add;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = o[i] * keep + x[k][i] * add;
+      }
     }
+  sh_o[first + tid] = o;
+  sh_ml[first + tid][0] = m;
+  sh_ml[first + tid][1] = l;
+  __syncthreads();
+  if (tid >= per || parts == 0) return;
+  float top = m;
+  for (int s = 1; s < groups; ++s) top = fmaxf(top, sh_ml[first + s * per + tid][0]);
+  const float ref = top == kNegInf ? 0.0f : top;
+  const float keep = __builtin_amdgcn_exp2f(m - ref);
+  l *= keep;
+  o *= keep;
+  for (int s = 1; s < groups; ++s) {
+    const float add = __builtin_amdgcn_exp2f(sh_ml[first + s * per + tid][0] - ref);
+    l += sh_ml[first + s * per + tid][1] * add;
+    const v4f x = sh_o[first + s * per + tid];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] += x[i] * add;
   }
   const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-  const int h = (int)(row - (int64_t)t * a.q_heads);
-  if (lane * 4 < D)
-    *reinterpret_cast<uint2*>(a.o.p + t * a.o.token + h * a.o.head + lane * 4) =
-        make_uint2(Act16<BF16>::pack2(o[0] * inv, o[1] * inv), Act16<BF16>::pack2(o[2] * inv, o[3] * inv));
-  if (a.lse && lane == 0) a.lse[row] = l > 0.0f ? (m + log2f(l)) * 0.693147180559945309f : kNegInf;
+  *reinterpret_cast<uint2*>(a.o.p + qrow * a.o.token + (int64_t)qh * a.o.head + tid * 4) = pack4(o * inv, a.bf16);
+  if (a.lse && tid == 0) a.lse[row] = l > 0.0f ? (top + log2f(l)) * 0.693147180559945309f : kNegInf;
 }
 
-int kv_attention_splits(const KvBatch& s, int heads, int q_heads, int64_t max_span, int num_cus,
-                        int* split_tiles) {
-  const int64_t items = (((int64_t)s.T * (q_heads / heads)) >> 4) + s.B;
-  const int64_t tiles = (max_span + 63) / 64;
-  // enough parts for 8 workgroups a CU, none under 4 tiles (one for each wavefront)
-  int64_t n = (8 * num_cus) / (items * heads);
-  n = std::max<int64_t>(1, std::min<int64_t>(n, (tiles + 3) / 4));
-  n = std::min<int64_t>(n, 256);
-  *split_tiles = (int)std::max<int64_t>(1, (tiles + n - 1) / n);
-  return (int)n;
+// Rows of a run: a sequence's rows together if they fit, so that its codes are
+// read once.
+int kv_attention_run(const KvBatch& s, int heads, int q_heads) {
+  const int64_t rows = (int64_t)s.T * (q_heads / heads), per = (rows + s.B - 1) / s.B;
+  return per <= 16 ? 16 : per <= 32 ? 32 : 64;
 }
 
-hipError_t launch_kv_attention(const KvAttnArgs& a, bool bf16, hipStream_t stream) {
-  const int G = a.q_heads / a.c.heads;
-  const dim3 grid((unsigned)((((int64_t)a.s.T * G) >> 4) + a.s.B), a.c.heads, a.splits);
-#define STEP(DP)                                                                     \
-  do {                                                                               \
-    if (bf16)                                                                        \
-      hipLaunchKernelGGL((kv_step<DP, true>), grid, dim3(256), 0, stream, a);        \
-    else                                                                             \
-      hipLaunchKernelGGL((kv_step<DP, false>), grid, dim3(256), 0, stream, a);       \
-  } while (0)
-  if (a.c.dim <= 64)
-    STEP(64);
-  else if (a.c.dim <= 128)
-    STEP(128);
-  else
-    STEP(256);
-#undef STEP
-  if (a.splits > 1) {
-    const unsigned blocks = (unsigned)(((int64_t)a.s.T * a.q_heads + 3) / 4);
-    if (bf16)
-      hipLaunchKernelGGL(kv_join<true>, dim3(blocks), dim3(256), 0, stream, a);
+static int64_t runs_at_most(const KvBatch& s, int heads, int q_heads) {
+  return (int64_t)s.T * (q_heads / heads) / kv_attention_run(s, heads, q_heads) + s.B;
+}
+
+// Whether a call's runs are cut into parts, and how many more workgroups that
+// takes at most. 0: not cut, where the longest context is no more than 2048
+// tokens, or 4096 and the runs fill half the chip: there the join costs more than
+// the cut gains (one sequence of 2000 tokens: 19 us uncut, 24 cut; 64 of 1000-2000
+// 41 and 56). *slots: workgroups that run at once, three, two or one to a CU by
+// the registers of the head size.
+int kv_attention_extra(const KvBatch& s, int heads, int q_heads, int dim, int64_t max_span, int num_cus, int* slots) {
+  *slots = num_cus * (dim <= 64 ? 3 : dim <= 128 ? 2 : 1);
+  const int64_t runs =
+      std::max<int64_t>(s.B, (int64_t)s.T * (q_heads / heads) / kv_attention_run(s, heads, q_heads)) * heads;
+  if (max_span <= (runs * 2 >= *slots ? 4096 : 2048)) return 0;
+  const int64_t tiles = (max_span + 63) / 64, most = (tiles + 15) / 16 - 1;
+  return (int)std::min<int64_t>(2 * *slots, most * runs_at_most(s, heads, q_heads) * heads);
+}
+
+template <int DP, bool FULL, bool ONE, int RT>
+static void launch_runs(const KvAttnArgs& a, hipStream_t stream) {
+  const unsigned runs = (unsigned)runs_at_most(a.s, a.c.heads, a.q_heads);
+  if (a.extra > 0) {
+    hipLaunchKernelGGL((kv_step<DP, FULL, ONE, true, RT>), dim3(runs * a.c.heads + a.extra), dim3(256), 0, stream, a);
+    const int64_t rows = (int64_t)a.s.T * a.q_heads;
+    if (a.c.dim > 128 || rows <= 2048)
+      hipLaunchKernelGGL(kv_join<1>, dim3((unsigned)rows), dim3(256), 0, stream, a);
     else
-      hipLaunchKernelGGL(kv_join<false>, dim3(blocks), dim3(256), 0, stream, a);
+      hipLaunchKernelGGL(kv_join<4>, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, a);
+  } else {
+    hipLaunchKernelGGL((kv_step<DP, FULL, ONE, false, RT>), dim3(a.c.heads, runs), dim3(256), 0, stream, a);
   }
+}
+
+template <int DP, bool FULL, bool ONE>
+static void launch_step(const KvAttnArgs& a, hipStream_t stream) {
+  switch (a.run) {
+    case 16: launch_runs<DP, FULL, ONE, 1>(a, stream); break;
+    case 32: launch_runs<DP, FULL, ONE, 2>(a, stream); break;
+    default: launch_runs<DP, FULL, ONE, 4>(a, stream);
+  }
+}
+
+hipError_t launch_kv_attention(const KvAttnArgs& a, hipStream_t stream) {
+#define STEP(DP, FULL) (a.c.page_shift >= 6 ? launch_step<DP, FULL, true>(a, stream) : launch_step<DP, FULL, false>(a, stream))
+  switch (a.c.dim) {
+    case 64: STEP(64, true); break;
+    case 128: STEP(128, true); break;
+    default:
+      if (a.c.dim < 64)
+        STEP(64, false);
+      else if (a.c.dim < 128)
+        STEP(128, false);
+      else
+        STEP(256, false);
+  }
+#undef STEP
   return hipGetLastError();
 }
 

@@ -111,10 +111,11 @@ template <bool BF16>
 __global__ __launch_bounds__(256) void kc_append(KvAppendArgs a) {
   __shared__ float red[4];
   const int P = 1 << a.c.page_shift, D = a.c.dim, H = a.c.heads;
+  __shared__ int sh_seq[4];
   int first;
-  const int b = kv_find<256>(a.s, blockIdx.x, 1, a.c.page_shift, 2, &first);
-  if (b < 0) return;
-  const KvSeq q = kv_seq(a.s, a.c.page_shift, b);
+  KvSeq q;
+  if (!kv_find<256>(a.s, a.c.page_shift, blockIdx.x, 1, a.c.page_shift, 2, sh_seq, &q, &first)) return;
+  const int b = q.b;
   const int pos0 = q.len - q.n;                             // position of row0 (< 0: those rows are dropped)
   const int entry = (max(pos0, 0) >> a.c.page_shift) + ((int)blockIdx.x - first);
   const int base = entry << a.c.page_shift;                 // position of slot 0
@@ -151,7 +152,7 @@ __global__ __launch_bounds__(256) void kc_append(KvAppendArgs a) {
   }
   const bool isv = y >= H;
   const int h = isv ? y - H : y;
-  const int page = kv_page(a.s, b, entry, a.c.pages);
+  const int page = kv_page(kv_entry(a.s, b, entry), a.c.pages);
   if (page < 0) return;
   const KvRows src = isv ? a.v : a.k;
   const float* rope = isv ? nullptr : a.rope;
@@ -221,10 +222,11 @@ hipError_t launch_kv_append(const KvAppendArgs& a, bool bf16, hipStream_t stream
 template <bool BF16>
 __global__ __launch_bounds__(256) void kc_gather(KvCache c, KvBatch s, KvRows k, KvRows v) {
   const int P = 1 << c.page_shift, D = c.dim, H = c.heads;
+  __shared__ int sh_seq[4];
   int first;
-  const int b = kv_find<256>(s, blockIdx.x, 1, c.page_shift, 2, &first);
-  if (b < 0) return;
-  const KvSeq q = kv_seq(s, c.page_shift, b);
+  KvSeq q;
+  if (!kv_find<256>(s, c.page_shift, blockIdx.x, 1, c.page_shift, 2, sh_seq, &q, &first)) return;
+  const int b = q.b;
   const int pos0 = q.len - q.n;
   const int entry = (max(pos0, 0) >> c.page_shift) + ((int)blockIdx.x - first);
   const int base = entry << c.page_shift;
@@ -232,7 +234,7 @@ __global__ __launch_bounds__(256) void kc_gather(KvCache c, KvBatch s, KvRows k,
   if (q.n == 0 || t0 >= t1) return;
   const bool isv = (int)blockIdx.y >= H;
   const int h = isv ? blockIdx.y - H : blockIdx.y;
-  const int page = kv_page(s, b, entry, c.pages);
+  const int page = kv_page(kv_entry(s, b, entry), c.pages);
   const int64_t ph = (int64_t)max(page, 0) * H + h;
   const int8_t* codes = (isv ? c.V : c.K) + ph * ((int64_t)P * D);
   const float st = page < 0 ? 0.0f : (isv ? c.aV : c.aK)[ph] / 127.0f;

@@ -233,14 +233,21 @@ struct KvAttnArgs {
   // most beyond one to each run and head (0: not cut); `slots` workgroups run at
   // once. What the parts leave for the join: [max_parts, run, dim] and
   // [max_parts, run, 2], and notes [T * q_heads, 2] of each row's parts.
+  int prompt;  // kv_prompt instead of kv_step; splits: parts of its tokens (1: not cut)
+  int splits;
   int run, extra, slots, max_parts;
   float* part_o;
   float* part_ml;
   int* notes;
 };
-int kv_attention_run(const KvBatch& s, int heads, int q_heads);  // rows of a run: 16, 32 or 64
+constexpr int kKvNoteShift = 8;  // a note: part << shift | row of the part, number of parts
+int kv_attention_run(const KvBatch& s, int heads, int q_heads);  // rows of a run: 16 or 32
 int kv_attention_extra(const KvBatch& s, int heads, int q_heads, int dim, int64_t max_span, int num_cus,
                        int* slots);
+bool kv_attention_prompt(const KvBatch& s, int heads, int q_heads);
+int kv_prompt_splits(const KvBatch& s, int heads, int q_heads, int dim, int page_shift, int64_t max_span,
+                     int num_cus, int* run, int* max_parts);
+hipError_t launch_kv_prompt(const KvAttnArgs& a, hipStream_t stream);
 hipError_t launch_kv_attention(const KvAttnArgs& a, hipStream_t stream);
 
 }  // namespace llmint8

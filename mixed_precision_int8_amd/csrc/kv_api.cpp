@@ -138,10 +138,18 @@ static size_t kv_attention_plan(const llmint8_kv_batch* batch, int64_t window, i
   const int64_t room = batch->width << a->c.page_shift;
   int64_t span = batch->max_len > 0 ? std::min(batch->max_len, room) : room;
   if (window > 0) span = std::min(span, window + sinks);
-  a->run = kv_attention_run(a->s, a->c.heads, a->q_heads);
-  a->extra = kv_attention_extra(a->s, a->c.heads, a->q_heads, a->c.dim, span, abi_cu_count(), &a->slots);
-  if (a->extra == 0) return 0;
-  a->max_parts = 2 * a->extra;  // parts of cut runs: each is longer than half of what the runs are cut by
+  const int cus = abi_cu_count();
+  a->prompt = kv_attention_prompt(a->s, a->c.heads, a->q_heads) ? 1 : 0;
+  a->splits = 1;
+  if (a->prompt) {
+    a->splits = kv_prompt_splits(a->s, a->c.heads, a->q_heads, a->c.dim, a->c.page_shift, span, cus, &a->run,
+                                 &a->max_parts);
+  } else {
+    a->run = kv_attention_run(a->s, a->c.heads, a->q_heads);
+    a->extra = kv_attention_extra(a->s, a->c.heads, a->q_heads, a->c.dim, span, cus, &a->slots);
+    a->max_parts = 2 * a->extra;  // parts of cut runs: each is longer than half of what the runs are cut by
+  }
+  if (a->max_parts == 0) return 0;
   const size_t rows = (size_t)a->max_parts * a->run;
   if (workspace) {
     a->part_o = static_cast<float*>(workspace);

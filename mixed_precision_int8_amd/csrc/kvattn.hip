@@ -131,8 +131,8 @@ struct Cutting {
   int64_t extra;  // parts beyond one to each run and head
   int least;      // tiles of a part
 };
-__host__ __device__ inline Cutting cutting(int64_t runs, int slots) {
-  return {runs * 4 <= slots ? slots - runs : (int64_t)2 * slots, runs * 2 >= slots ? 48 : 16};
+__host__ __device__ inline Cutting cutting(int64_t runs, int slots, int rt) {
+  return {runs * 4 <= slots ? slots - runs : (int64_t)2 * slots, (runs * 2 >= slots ? 48 : 16) / rt};
 }
 
 // Exclusive sums of two numbers over the workgroup's 256 threads, and their totals.
@@ -186,7 +186,7 @@ __device__ __forceinline__ bool find_part(const KvAttnArgs& a, int w, int64_t (&
     tiles += all_x;
     runs += all_y;
   }
-  const Cutting how = cutting(runs, a.slots);
+  const Cutting how = cutting(runs, a.slots, RT);
   const int64_t extra = min((int64_t)a.extra, how.extra);
   const int share = (int)max((int64_t)how.least, (tiles + extra - 1) / extra);
   int64_t before = 0, cut = 0;
@@ -247,7 +247,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void kv_step(KvAttnArgs a) 
   constexpr int WT = 4 / RT;  // wavefronts that share a sixteen's tiles
   constexpr int NK = DP / 64;  // 64-channel steps of the first product
   constexpr int ND = DP / 16;  // 16-channel blocks of the second
-  __shared__ float sh_o[RT < 4 ? 2 : 1][16][DP];
+  __shared__ float sh_o[2][16][DP];
   __shared__ float sh_ml[4][16][2];
   __shared__ int sh_seq[4];
   __shared__ int sh_found[8];
@@ -276,9 +276,9 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void kv_step(KvAttnArgs a) 
     if (!find_part<RT>(a, blockIdx.x, sh_sums, sh_found, &sq, &p)) return;
   } else {
     int first;
-    if (!kv_find<256>(a.s, shift, blockIdx.y, G, RT == 4 ? 6 : 3 + RT, 1, sh_seq, &sq, &first)) return;
-    p.h = blockIdx.x;  // neighbours share a page
-    p.run = (int)blockIdx.y - first;
+    if (!kv_find<256>(a.s, shift, blockIdx.x / H, G, 3 + RT, 1, sh_seq, &sq, &first)) return;
+    p.h = (int)(blockIdx.x % H);  // neighbours share a page
+    p.run = (int)(blockIdx.x / H) - first;
     p.parts = 1;
     if (sq.n == 0 || p.run >= seq_work<RT>(a, sq).runs) return;
   }
@@ -546,7 +546,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void kv_step(KvAttnArgs a) 
   // which parts there are of a row, for the join
   if (CUT && p.part == 0 && g == 0 && wave % WT == 0 && row_mine + nn < rows)
     *reinterpret_cast<v2i*>(a.notes + (qrow * a.q_heads + qh) * 2) =
-        v2i{p.parts > 1 ? (p.slot << 6 | 16 * t | nn) : -1, p.parts};
+        v2i{p.parts > 1 ? (p.slot << kKvNoteShift | 16 * t | nn) : -1, p.parts};
   if (wave % WT == 0 && row_mine < rows) {
     if (CUT && p.parts > 1) {
       const int64_t to = (int64_t)p.slot * (16 * RT) + 16 * t + nn;
@@ -582,7 +582,7 @@ __global__ __launch_bounds__(256) void kv_join(KvAttnArgs a) {
   // rows outside the batch have no note
   const bool in = t >= max(a.s.cu[0], 0) && t < min(a.s.cu[a.s.B], a.s.T);
   const v2i note = in ? *reinterpret_cast<const v2i*>(a.notes + row * 2) : v2i{-1, 0};
-  const int slot = note[0] >> 6, nn = note[0] & 63;
+  const int slot = note[0] >> kKvNoteShift, nn = note[0] & ((1 << kKvNoteShift) - 1);
   const int parts = note[0] < 0 || note[1] < 0 || note[1] > a.max_parts - slot ? 0 : note[1];
   if (ROWS == 1 && parts == 0) return;
   const int64_t qrow = t;
@@ -640,7 +640,16 @@ __global__ __launch_bounds__(256) void kv_join(KvAttnArgs a) {
 // read once.
 int kv_attention_run(const KvBatch& s, int heads, int q_heads) {
   const int64_t rows = (int64_t)s.T * (q_heads / heads), per = (rows + s.B - 1) / s.B;
-  return per <= 16 ? 16 : per <= 32 ? 32 : 64;
+  return per <= 16 ? 16 : 32;
+}
+
+// Whether a call's sequences have rows enough, on average, for kv_prompt: more than
+// the 32 of a run of kv_step, which would read the codes again for the next ones.
+// Measured, 16 sequences of 1000-6000 tokens (us, kv_step / kv_prompt): 20 rows
+// 40 / 56, 32 rows 40 / 57, 80 rows (3000-6000) 127 / 79; 64 of 500-4000 with 64
+// rows 282 / 129.
+bool kv_attention_prompt(const KvBatch& s, int heads, int q_heads) {
+  return (int64_t)s.T * (q_heads / heads) > (int64_t)32 * s.B;
 }
 
 static int64_t runs_at_most(const KvBatch& s, int heads, int q_heads) {
@@ -657,49 +666,55 @@ int kv_attention_extra(const KvBatch& s, int heads, int q_heads, int dim, int64_
   *slots = num_cus * (dim <= 64 ? 3 : dim <= 128 ? 2 : 1);
   const int64_t runs =
       std::max<int64_t>(s.B, (int64_t)s.T * (q_heads / heads) / kv_attention_run(s, heads, q_heads)) * heads;
-  if (max_span <= (runs * 2 >= *slots ? 4096 : 2048)) return 0;
-  const int64_t tiles = (max_span + 63) / 64, most = (tiles + 15) / 16 - 1;
+  const int rt = kv_attention_run(s, heads, q_heads) / 16;
+  if (max_span * rt <= (runs * 2 >= *slots ? 4096 : 2048)) return 0;
+  const int64_t tiles = (max_span + 63) / 64, least = cutting(1, *slots, rt).least, most = (tiles + least - 1) / least - 1;
   return (int)std::min<int64_t>(2 * *slots, most * runs_at_most(s, heads, q_heads) * heads);
 }
 
 template <int DP, bool FULL, bool ONE, int RT>
 static void launch_runs(const KvAttnArgs& a, hipStream_t stream) {
   const unsigned runs = (unsigned)runs_at_most(a.s, a.c.heads, a.q_heads);
-  if (a.extra > 0) {
+  if (a.extra > 0)
     hipLaunchKernelGGL((kv_step<DP, FULL, ONE, true, RT>), dim3(runs * a.c.heads + a.extra), dim3(256), 0, stream, a);
+  else
+    hipLaunchKernelGGL((kv_step<DP, FULL, ONE, false, RT>), dim3(runs * a.c.heads), dim3(256), 0, stream, a);
+}
+
+template <int DP, bool FULL, bool ONE>
+static void launch_step(const KvAttnArgs& a, hipStream_t stream) {
+  if (a.run == 16)
+    launch_runs<DP, FULL, ONE, 1>(a, stream);
+  else
+    launch_runs<DP, FULL, ONE, 2>(a, stream);
+}
+
+static void launch_kv_step(const KvAttnArgs& a, hipStream_t stream) {
+  const bool one = a.c.page_shift >= 6;
+  if (a.c.dim == 64)
+    one ? launch_step<64, true, true>(a, stream) : launch_step<64, true, false>(a, stream);
+  else if (a.c.dim < 64)
+    one ? launch_step<64, false, true>(a, stream) : launch_step<64, false, false>(a, stream);
+  else if (a.c.dim == 128)
+    one ? launch_step<128, true, true>(a, stream) : launch_step<128, true, false>(a, stream);
+  else if (a.c.dim < 128)
+    one ? launch_step<128, false, true>(a, stream) : launch_step<128, false, false>(a, stream);
+  else
+    one ? launch_step<256, false, true>(a, stream) : launch_step<256, false, false>(a, stream);
+}
+
+hipError_t launch_kv_attention(const KvAttnArgs& a, hipStream_t stream) {
+  if (a.prompt)
+    launch_kv_prompt(a, stream);
+  else
+    launch_kv_step(a, stream);
+  if (a.max_parts > 0) {
     const int64_t rows = (int64_t)a.s.T * a.q_heads;
     if (a.c.dim > 128 || rows <= 2048)
       hipLaunchKernelGGL(kv_join<1>, dim3((unsigned)rows), dim3(256), 0, stream, a);
     else
       hipLaunchKernelGGL(kv_join<4>, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, a);
-  } else {
-    hipLaunchKernelGGL((kv_step<DP, FULL, ONE, false, RT>), dim3(a.c.heads, runs), dim3(256), 0, stream, a);
   }
-}
-
-template <int DP, bool FULL, bool ONE>
-static void launch_step(const KvAttnArgs& a, hipStream_t stream) {
-  switch (a.run) {
-    case 16: launch_runs<DP, FULL, ONE, 1>(a, stream); break;
-    case 32: launch_runs<DP, FULL, ONE, 2>(a, stream); break;
-    default: launch_runs<DP, FULL, ONE, 4>(a, stream);
-  }
-}
-
-hipError_t launch_kv_attention(const KvAttnArgs& a, hipStream_t stream) {
-#define STEP(DP, FULL) (a.c.page_shift >= 6 ? launch_step<DP, FULL, true>(a, stream) : launch_step<DP, FULL, false>(a, stream))
-  switch (a.c.dim) {
-    case 64: STEP(64, true); break;
-    case 128: STEP(128, true); break;
-    default:
-      if (a.c.dim < 64)
-        STEP(64, false);
-      else if (a.c.dim < 128)
-        STEP(128, false);
-      else
-        STEP(256, false);
-  }
-#undef STEP
   return hipGetLastError();
 }
 

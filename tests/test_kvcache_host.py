@@ -19,7 +19,7 @@ from mixed_precision_int8_amd.kvcache import _Batch, _Cache
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 PKG = os.path.join(ROOT, "mixed_precision_int8_amd")
-KV_SOURCES = ("kvcache.hip", "kvattn.hip")
+KV_SOURCES = ("kvcache.hip", "kvattn.hip", "kvprompt.hip")
 OK, INVALID, UNSUPPORTED, WORKSPACE = 0, -1, -2, -3
 F16, F32, BF16 = m8.LLMINT8_DTYPE_F16, m8.LLMINT8_DTYPE_F32, m8.LLMINT8_DTYPE_BF16
 

@@ -214,7 +214,7 @@ struct KvAppendArgs {
 };
 hipError_t launch_kv_append(const KvAppendArgs& a, bool bf16, hipStream_t stream);
 hipError_t launch_kv_gather(const KvCache& c, const KvBatch& s, const KvRows& k, const KvRows& v, bool bf16,
-                            hipStream_t stream);
+                            int num_cus, hipStream_t stream);
 // rope[p][i] = mag cos(p f[i]), rope[p][n + i] = mag sin(p f[i])
 constexpr int kRopeMaxPairs = 128;
 struct RopeFreq {

@@ -128,8 +128,8 @@ llmint8_status llmint8_kv_gather(const llmint8_kv_cache* cache, const llmint8_kv
   if (!kv_rows(k, k_token, k_head, batch->rows, cache->heads, cache->dim, &kr) ||
       !kv_rows(v, v_token, v_head, batch->rows, cache->heads, cache->dim, &vr))
     return LLMINT8_ERR_INVALID_ARG;
-  return abi_hip_status(launch_kv_gather(c, s, kr, vr, dtype == LLMINT8_DTYPE_BF16,
-                                     static_cast<hipStream_t>(stream)));
+  return abi_hip_status(launch_kv_gather(c, s, kr, vr, dtype == LLMINT8_DTYPE_BF16, abi_cu_count(),
+                                        static_cast<hipStream_t>(stream)));
 }
 
 // The route of an attention call and the bytes that it leaves for its join.

@@ -45,34 +45,37 @@ __device__ __forceinline__ KvSeq kv_seq_uniform(const KvBatch& s, int page_shift
 }
 
 // The sequence that work item `item` belongs to, where sequence b owns the items
-// from (cu[b] * per >> shift) + slack * b on. A sequence of n rows then has at
-// least (n * per >> shift) + slack items, which covers the tiles of 2^shift that
-// its n * per rows fill (slack 1) or the pages of 2^shift that n tokens reach
-// (slack 2), with no table of tile counts. Whole workgroup: the sequences are
-// counted in parallel, one round of loads for every kThreads of them, and the
-// owner hands its numbers, loaded in the same round, to the others (sh).
-// Sets *first to the sequence's first item; false where no sequence owns the item
-// (cu starts late, or falls).
+// from (cu[b] * per >> shift) + b on. A sequence of n rows then has at least (n *
+// per >> shift) + 1 items: enough for the tiles of 2^shift that its n * per rows
+// fill, and one less at most than the pages of 2^shift that n tokens reach, with
+// no table of counts. Whole workgroup: the sequences are counted in parallel, one
+// round of loads for every kThreads of them, and the owner hands its numbers,
+// loaded in the same round, to the others (sh). Sets *index to the item's number
+// in the sequence and *count to the sequence's items; false where no sequence owns
+// the item (cu starts late, or falls).
 template <int kThreads>
 __device__ __forceinline__ bool kv_find(const KvBatch& s, int page_shift, int item, int per, int shift,
-                                        int slack, int (&sh)[4], KvSeq* out, int* first) {
+                                        int (&sh)[5], KvSeq* out, int* index, int* count) {
   if (s.B == 1) {
     *out = kv_seq_uniform(s, page_shift, 0);
-    *first = (int)(((int64_t)out->row0 * per) >> shift);
-    return *first <= item;
+    const int first = (int)(((int64_t)out->row0 * per) >> shift);
+    *index = item - first;
+    *count = (int)(((int64_t)(out->row0 + out->n) * per) >> shift) + 1 - first;
+    return first <= item;
   }
   int b = -1;
   for (int b0 = 0; b0 < s.B; b0 += kThreads) {
     const int i = b0 + (int)threadIdx.x;
     const int lane = min(i, s.B - 1);
     const KvSeq q = kv_seq(s, page_shift, lane);
-    const int64_t at = (((int64_t)q.row0 * per) >> shift) + (int64_t)slack * lane;
+    const int64_t at = (((int64_t)q.row0 * per) >> shift) + lane;
     const int mine = __syncthreads_count(i < s.B && at <= item);
     if (mine > 0 && (int)threadIdx.x == mine - 1) {
       sh[0] = q.row0;
       sh[1] = q.n;
       sh[2] = q.len;
       sh[3] = (int)at;
+      sh[4] = (int)((((int64_t)(q.row0 + q.n) * per) >> shift) + lane + 1 - at);
     }
     b += mine;
     if (mine < min(kThreads, s.B - b0)) break;
@@ -83,8 +86,9 @@ __device__ __forceinline__ bool kv_find(const KvBatch& s, int page_shift, int it
   out->row0 = uniform(sh[0]);
   out->n = uniform(sh[1]);
   out->len = uniform(sh[2]);
-  *first = uniform(sh[3]);
-  return *first <= item;
+  *index = item - uniform(sh[3]);
+  *count = uniform(sh[4]);
+  return *index >= 0;
 }
 
 // Page that the table names for the tokens of an entry; may be any number. Tokens

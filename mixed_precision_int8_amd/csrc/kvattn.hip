@@ -249,7 +249,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void kv_step(KvAttnArgs a) 
   constexpr int ND = DP / 16;  // 16-channel blocks of the second
   __shared__ float sh_o[2][16][DP];
   __shared__ float sh_ml[4][16][2];
-  __shared__ int sh_seq[4];
+  __shared__ int sh_seq[5];
   __shared__ int sh_found[8];
   __shared__ int64_t sh_sums[8];
   const int D = FULL ? DP : a.c.dim;
@@ -275,10 +275,9 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void kv_step(KvAttnArgs a) 
   if (CUT) {
     if (!find_part<RT>(a, blockIdx.x, sh_sums, sh_found, &sq, &p)) return;
   } else {
-    int first;
-    if (!kv_find<256>(a.s, shift, blockIdx.x / H, G, 3 + RT, 1, sh_seq, &sq, &first)) return;
+    int count;
+    if (!kv_find<256>(a.s, shift, blockIdx.x / H, G, 3 + RT, sh_seq, &sq, &p.run, &count)) return;
     p.h = (int)(blockIdx.x % H);  // neighbours share a page
-    p.run = (int)(blockIdx.x / H) - first;
     p.parts = 1;
     if (sq.n == 0 || p.run >= seq_work<RT>(a, sq).runs) return;
   }
@@ -673,48 +672,40 @@ int kv_attention_extra(const KvBatch& s, int heads, int q_heads, int dim, int64_
 }
 
 template <int DP, bool FULL, bool ONE, int RT>
-static void launch_runs(const KvAttnArgs& a, hipStream_t stream) {
-  const unsigned runs = (unsigned)runs_at_most(a.s, a.c.heads, a.q_heads);
+static hipError_t launch_runs(const KvAttnArgs& a, hipStream_t stream) {
+  const int64_t blocks = runs_at_most(a.s, a.c.heads, a.q_heads) * a.c.heads + a.extra;
+  if (blocks > INT32_MAX) return hipErrorInvalidConfiguration;
   if (a.extra > 0)
-    hipLaunchKernelGGL((kv_step<DP, FULL, ONE, true, RT>), dim3(runs * a.c.heads + a.extra), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((kv_step<DP, FULL, ONE, true, RT>), dim3((unsigned)blocks), dim3(256), 0, stream, a);
   else
-    hipLaunchKernelGGL((kv_step<DP, FULL, ONE, false, RT>), dim3(runs * a.c.heads), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((kv_step<DP, FULL, ONE, false, RT>), dim3((unsigned)blocks), dim3(256), 0, stream, a);
+  return hipGetLastError();
 }
 
-template <int DP, bool FULL, bool ONE>
-static void launch_step(const KvAttnArgs& a, hipStream_t stream) {
-  if (a.run == 16)
-    launch_runs<DP, FULL, ONE, 1>(a, stream);
-  else
-    launch_runs<DP, FULL, ONE, 2>(a, stream);
+template <int DP, bool FULL>
+static hipError_t launch_step(const KvAttnArgs& a, hipStream_t stream) {
+  if (a.c.page_shift >= 6)
+    return a.run == 16 ? launch_runs<DP, FULL, true, 1>(a, stream) : launch_runs<DP, FULL, true, 2>(a, stream);
+  return a.run == 16 ? launch_runs<DP, FULL, false, 1>(a, stream) : launch_runs<DP, FULL, false, 2>(a, stream);
 }
 
-static void launch_kv_step(const KvAttnArgs& a, hipStream_t stream) {
-  const bool one = a.c.page_shift >= 6;
-  if (a.c.dim == 64)
-    one ? launch_step<64, true, true>(a, stream) : launch_step<64, true, false>(a, stream);
-  else if (a.c.dim < 64)
-    one ? launch_step<64, false, true>(a, stream) : launch_step<64, false, false>(a, stream);
-  else if (a.c.dim == 128)
-    one ? launch_step<128, true, true>(a, stream) : launch_step<128, true, false>(a, stream);
-  else if (a.c.dim < 128)
-    one ? launch_step<128, false, true>(a, stream) : launch_step<128, false, false>(a, stream);
-  else
-    one ? launch_step<256, false, true>(a, stream) : launch_step<256, false, false>(a, stream);
+static hipError_t launch_kv_step(const KvAttnArgs& a, hipStream_t stream) {
+  if (a.c.dim == 64) return launch_step<64, true>(a, stream);
+  if (a.c.dim < 64) return launch_step<64, false>(a, stream);
+  if (a.c.dim == 128) return launch_step<128, true>(a, stream);
+  if (a.c.dim < 128) return launch_step<128, false>(a, stream);
+  return launch_step<256, false>(a, stream);
 }
 
 hipError_t launch_kv_attention(const KvAttnArgs& a, hipStream_t stream) {
-  if (a.prompt)
-    launch_kv_prompt(a, stream);
+  const hipError_t e = a.prompt ? launch_kv_prompt(a, stream) : launch_kv_step(a, stream);
+  if (e != hipSuccess || a.max_parts == 0) return e;
+  const int64_t rows = (int64_t)a.s.T * a.q_heads;
+  if (rows > INT32_MAX) return hipErrorInvalidConfiguration;
+  if (a.c.dim > 128 || rows <= 2048)
+    hipLaunchKernelGGL(kv_join<1>, dim3((unsigned)rows), dim3(256), 0, stream, a);
   else
-    launch_kv_step(a, stream);
-  if (a.max_parts > 0) {
-    const int64_t rows = (int64_t)a.s.T * a.q_heads;
-    if (a.c.dim > 128 || rows <= 2048)
-      hipLaunchKernelGGL(kv_join<1>, dim3((unsigned)rows), dim3(256), 0, stream, a);
-    else
-      hipLaunchKernelGGL(kv_join<4>, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, a);
-  }
+    hipLaunchKernelGGL(kv_join<4>, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 

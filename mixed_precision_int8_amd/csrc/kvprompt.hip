@@ -84,18 +84,18 @@ __global__ __launch_bounds__(64 * W, DP <= 128 ? 2 : 1) void kv_prompt(KvAttnArg
   constexpr int kKPitch = 2 * DP + 16, kVPitch = 2 * 64 + 16;
   constexpr int kKBytes = 64 * kKPitch, kVBytes = DP * kVPitch;
   __shared__ __attribute__((aligned(16))) char smem_k[2 * kKBytes], smem_v[2 * kVBytes];
-  __shared__ int sh_seq[4];
+  __shared__ int sh_seq[5];
   const int D = FULL ? DP : a.c.dim;
   const int shift = a.c.page_shift, P = 1 << shift, H = a.c.heads, G = a.q_heads / H;
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int hf = lane >> 5, nn = lane & 31;
-  int first;
+  int run, count;
   KvSeq sq;
   // the last rows of a sequence see the most: they start first
   const unsigned whole = gridDim.x / a.splits, at = blockIdx.x % whole;
   const int h = (int)(at % H), item = (int)((whole - 1 - at) / H), part = (int)(blockIdx.x / whole);
-  if (!kv_find<kThreads>(a.s, shift, item, G, W == 4 ? 7 : 8, 1, sh_seq, &sq, &first)) return;
-  const int64_t rows = (int64_t)sq.n * G, row0 = (int64_t)(item - first) * kRows;
+  if (!kv_find<kThreads>(a.s, shift, item, G, W == 4 ? 7 : 8, sh_seq, &sq, &run, &count)) return;
+  const int64_t rows = (int64_t)sq.n * G, row0 = (int64_t)run * kRows;
   if (row0 >= rows) return;
   const int b = sq.b;
   const int r = (int)min(row0 + wave * 32 + nn, rows - 1);
@@ -429,24 +429,24 @@ int kv_prompt_splits(const KvBatch& s, int heads, int q_heads, int dim, int page
 }
 
 template <int DP, bool FULL, bool ONE, int W>
-static void launch_prompt(const KvAttnArgs& a, hipStream_t stream) {
-  const unsigned items = (unsigned)prompt_items(a.s, a.q_heads / a.c.heads, W);
-  hipLaunchKernelGGL((kv_prompt<DP, FULL, ONE, W>), dim3(items * a.c.heads * a.splits), dim3(64 * W), 0, stream, a);
+static hipError_t launch_prompt(const KvAttnArgs& a, hipStream_t stream) {
+  const int64_t blocks = prompt_items(a.s, a.q_heads / a.c.heads, W) * a.c.heads * a.splits;
+  if (blocks > INT32_MAX) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL((kv_prompt<DP, FULL, ONE, W>), dim3((unsigned)blocks), dim3(64 * W), 0, stream, a);
+  return hipGetLastError();
 }
 
 hipError_t launch_kv_prompt(const KvAttnArgs& a, hipStream_t stream) {
   const bool one = a.c.page_shift >= 6;
   if (a.c.dim == 64)
-    one ? launch_prompt<64, true, true, 4>(a, stream) : launch_prompt<64, true, false, 4>(a, stream);
-  else if (a.c.dim < 64)
-    one ? launch_prompt<64, false, true, 4>(a, stream) : launch_prompt<64, false, false, 4>(a, stream);
-  else if (a.c.dim == 128)
-    one ? launch_prompt<128, true, true, 4>(a, stream) : launch_prompt<128, true, false, 8>(a, stream);
-  else if (a.c.dim < 128)
-    one ? launch_prompt<128, false, true, 4>(a, stream) : launch_prompt<128, false, false, 8>(a, stream);
-  else
-    one ? launch_prompt<256, false, true, 4>(a, stream) : launch_prompt<256, false, false, 4>(a, stream);
-  return hipGetLastError();
+    return one ? launch_prompt<64, true, true, 4>(a, stream) : launch_prompt<64, true, false, 4>(a, stream);
+  if (a.c.dim < 64)
+    return one ? launch_prompt<64, false, true, 4>(a, stream) : launch_prompt<64, false, false, 4>(a, stream);
+  if (a.c.dim == 128)
+    return one ? launch_prompt<128, true, true, 4>(a, stream) : launch_prompt<128, true, false, 8>(a, stream);
+  if (a.c.dim < 128)
+    return one ? launch_prompt<128, false, true, 4>(a, stream) : launch_prompt<128, false, false, 8>(a, stream);
+  return one ? launch_prompt<256, false, true, 4>(a, stream) : launch_prompt<256, false, false, 4>(a, stream);
 }
 
 }  // namespace llmint8

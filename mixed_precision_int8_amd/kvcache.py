@@ -27,6 +27,18 @@ def _m8():
     return m8
 
 
+def _stream(stream, device):
+    """The stream's handle. The current one's is asked for without a Stream object around it where torch
+    has such a call (0.1 us, 2 us otherwise: a sixth of a short call's time on the host)."""
+    import torch
+    if stream is not None:
+        return stream.cuda_stream
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None or device.index is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return raw(device.index)
+
+
 class KVCache:
     """A pool of cache pages: K int8 [pages, heads, page, dim], V int8 [pages, heads, dim, page] and the
     magnitudes aK, aV fp32 [pages, heads], held by the caller (see ``KVCache.empty``)."""
@@ -158,7 +170,7 @@ def llmint8_rope_table(freq, rows, magnitude=1.0, table=None, device="cuda", str
     m8._need(table, torch.float32, (rows, 2 * n), "table")
     arr = (ctypes.c_double * max(n, 1))(*[float(x) for x in freq])
     m8._check(lib.llmint8_rope_table(arr, n, rows, float(magnitude), table.data_ptr(),
-                                     m8._stream(stream, table.device)),
+                                     _stream(stream, table.device)),
               "llmint8_rope_table")
     return table
 
@@ -198,7 +210,7 @@ def llmint8_kv_append(cache, batch, k, v, q=None, rope=None, interleaved=False, 
         table_rows, rot = rope.shape
         table = rope.data_ptr()
     m8._check(lib.llmint8_kv_append(cache._ref, batch._ref, code, *kr, *vr, *qr, *orr, heads, table,
-                                    table_rows, rot, 1 if interleaved else 0, m8._stream(stream, dev)),
+                                    table_rows, rot, 1 if interleaved else 0, _stream(stream, dev)),
               "llmint8_kv_append")
     return q_out
 
@@ -217,7 +229,7 @@ def llmint8_kv_gather(cache, batch, dtype=None, k=None, v=None, stream=None):
     if v is None:
         v = torch.empty(shape, dtype=dtype, device=dev)
     m8._check(lib.llmint8_kv_gather(cache._ref, batch._ref, code, *_rows(k, dtype, *shape, dev, "k"),
-                                    *_rows(v, dtype, *shape, dev, "v"), m8._stream(stream, dev)),
+                                    *_rows(v, dtype, *shape, dev, "v"), _stream(stream, dev)),
               "llmint8_kv_gather")
     return k, v
 
@@ -253,7 +265,7 @@ def llmint8_kv_attention(cache, batch, q, scale=None, causal=True, window=0, sin
                                        1.0 / math.sqrt(cache.dim) if scale is None else float(scale),
                                        1 if causal else 0, window, sinks, *orr,
                                        None if lse is None else lse.data_ptr(), m8._ptr(workspace),
-                                       m8._ws_bytes(workspace), m8._stream(stream, dev)),
+                                       m8._ws_bytes(workspace), _stream(stream, dev)),
               "llmint8_kv_attention")
     return out
 

@@ -119,20 +119,22 @@ struct Part {
   int h, run, part, parts;
   int slot;  // of a part of several: where its result goes
 };
-// How finely the call is cut. With few runs and heads, as many parts as run at
-// once; with more, twice that many beyond the runs' own, which evens out runs of
-// different lengths. A part of its own costs about 8 us of loads that wait for
-// each other and of joining, so none gets less than `least` tiles (16: about 9 us
-// of work), and more where the runs by themselves fill half the chip. Measured
-// (32 query and 8 key/value heads of 128, us): 32 sequences of 2000-8000 tokens
-// 73 (85 cut into one part per resident workgroup, 102 uncut), 64 of 500-8000 95
-// (119 uncut), one of 131000 54.
+// How finely the call is cut. With few runs and heads, about as many parts as run
+// at once (a run's last part is half of one on average: cut for that half, 16
+// sequences of 1000-8000 tokens take 36.5 us, and 37.7 without it); with more,
+// twice that many beyond the runs' own, which evens out runs of different lengths.
+// A part of its own costs about 8 us of loads that wait for each other and of
+// joining, so none gets less than `least` tiles (16: about 9 us of work), and more
+// where the runs by themselves fill half the chip. Measured (32 query and 8
+// key/value heads of 128, us): 32 sequences of 2000-8000 tokens 73 (85 cut into
+// one part per resident workgroup, 102 uncut), 64 of 500-8000 94 (119 uncut), one
+// of 131000 53.
 struct Cutting {
   int64_t extra;  // parts beyond one to each run and head
   int least;      // tiles of a part
 };
 __host__ __device__ inline Cutting cutting(int64_t runs, int slots, int rt) {
-  return {runs * 4 <= slots ? slots - runs : (int64_t)2 * slots, (runs * 2 >= slots ? 48 : 16) / rt};
+  return {runs * 4 <= slots ? slots - runs / 2 : (int64_t)2 * slots, (runs * 2 >= slots ? 48 : 16) / rt};
 }
 
 // Exclusive sums of two numbers over the workgroup's 256 threads, and their totals.
@@ -580,7 +582,9 @@ __global__ __launch_bounds__(256) void kv_join(KvAttnArgs a) {
   const int t = (int)(row / a.q_heads);
   // rows outside the batch have no note
   const bool in = t >= max(a.s.cu[0], 0) && t < min(a.s.cu[a.s.B], a.s.T);
-  const v2i note = in ? *reinterpret_cast<const v2i*>(a.notes + row * 2) : v2i{-1, 0};
+  // read beside cu, not after it
+  v2i note = *reinterpret_cast<const v2i*>(a.notes + min(row, (int64_t)a.s.T * a.q_heads - 1) * 2);
+  if (!in) note = v2i{-1, 0};
   const int slot = note[0] >> kKvNoteShift, nn = note[0] & ((1 << kKvNoteShift) - 1);
   const int parts = note[0] < 0 || note[1] < 0 || note[1] > a.max_parts - slot ? 0 : note[1];
   if (ROWS == 1 && parts == 0) return;

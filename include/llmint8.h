@@ -471,7 +471,9 @@ LLMINT8_API llmint8_status llmint8_rope_table(const double* freq, int64_t pairs,
  *   new codes rne(fl32(x * fl32(127 / a'))); where a' > a the page's earlier
  *   codes become rne(fl32(c * fl32(a / a'))).
  * The tokens of a page are written in order; no two sequences of a call may
- * write to the same page. Codes and magnitudes are bit-exact.
+ * write to the same page. Codes and magnitudes are bit-exact. A NaN or infinity
+ * makes the magnitude one: all tokens of that page and head then read as NaN (and
+ * a row that sees one of them gets NaN), until its slot 0 is written again.
  */
 LLMINT8_API llmint8_status llmint8_kv_append(const llmint8_kv_cache* cache, const llmint8_kv_batch* batch,
                                              int dtype, const void* k, int64_t k_token, int64_t k_head,
@@ -499,7 +501,7 @@ LLMINT8_API llmint8_status llmint8_kv_gather(const llmint8_kv_cache* cache, cons
  * NULL, fp32 [rows, q_heads]) log sum_j exp(scale q . k_j). A row that sees
  * nothing gets zeros and -inf. Any mix of single tokens and longer runs is one
  * call. Sums and statistics are fp32 or exact integers.
- *   q_heads    a multiple of heads
+ *   q_heads    a multiple of heads; rows * q_heads <= 2^30
  *   scale      finite (usually 1 / sqrt(dim))
  *   workspace  llmint8_kv_attention_workspace_bytes(...) bytes, 256-byte
  *              aligned, contents on entry do not matter; NULL where that is 0

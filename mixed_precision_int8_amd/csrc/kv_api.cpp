@@ -159,11 +159,11 @@ static size_t kv_attention_plan(const llmint8_kv_batch* batch, int64_t window, i
   return (rows * (a->c.dim + 2) + (size_t)a->s.T * a->q_heads * 2) * sizeof(float);
 }
 
-static llmint8_status check_kv_attention(const llmint8_kv_cache* cache, int64_t q_heads, int causal,
-                                         int64_t window, int64_t sinks) {
+static llmint8_status check_kv_attention(const llmint8_kv_cache* cache, const llmint8_kv_batch* batch,
+                                         int64_t q_heads, int causal, int64_t window, int64_t sinks) {
   if (q_heads < 1 || q_heads > kKvMaxQHeads || q_heads % cache->heads != 0) return LLMINT8_ERR_INVALID_ARG;
   if (window < 0 || sinks < 0 || (window > 0 && !causal)) return LLMINT8_ERR_INVALID_ARG;
-  if (window > kKvMax || sinks > kKvMax) return LLMINT8_ERR_UNSUPPORTED;
+  if (window > kKvMax || sinks > kKvMax || batch->rows * q_heads > kKvMaxQRows) return LLMINT8_ERR_UNSUPPORTED;
   return LLMINT8_OK;
 }
 
@@ -172,7 +172,7 @@ size_t llmint8_kv_attention_workspace_bytes(const llmint8_kv_cache* cache, const
   KvAttnArgs a{};
   bool empty = false;
   if (kv_operands(cache, batch, LLMINT8_DTYPE_F16, &a.c, &a.s, &empty) != LLMINT8_OK) return 0;
-  if (check_kv_attention(cache, q_heads, 1, window, sinks) != LLMINT8_OK || empty) return 0;
+  if (check_kv_attention(cache, batch, q_heads, 1, window, sinks) != LLMINT8_OK || empty) return 0;
   a.q_heads = (int)q_heads;
   return kv_attention_plan(batch, window, sinks, nullptr, &a);
 }
@@ -185,7 +185,7 @@ llmint8_status llmint8_kv_attention(const llmint8_kv_cache* cache, const llmint8
   KvAttnArgs a{};
   bool empty = false;
   llmint8_status st = kv_operands(cache, batch, dtype, &a.c, &a.s, &empty);
-  if (st == LLMINT8_OK) st = check_kv_attention(cache, q_heads, causal, window, sinks);
+  if (st == LLMINT8_OK) st = check_kv_attention(cache, batch, q_heads, causal, window, sinks);
   if (st != LLMINT8_OK) return st;
   if (!std::isfinite(scale)) return LLMINT8_ERR_INVALID_ARG;
   if (empty) return LLMINT8_OK;

@@ -61,8 +61,8 @@ __device__ __forceinline__ float swap16(float v, float* other) {
 __device__ __forceinline__ float row_max(float v) {
   float o;
   v = swap32(v, &o);
-  v = swap16(fmaxf(v, o), &o);
-  return fmaxf(v, o);
+  v = swap16(max_or_nan(v, o), &o);
+  return max_or_nan(v, o);
 }
 __device__ __forceinline__ float row_sum(float v) {
   float o;
@@ -384,7 +384,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void kv_step(KvAttnArgs a) 
 #pragma unroll
       for (int ks = 0; ks < NK; ++ks)
 #pragma unroll
-        for (int j = 0; j < 16; ++j) m = fmaxf(m, fabsf(f[ks][j]));
+        for (int j = 0; j < 16; ++j) m = max_or_nan(m, fabsf(f[ks][j]));
       m = row_max(m);
       const float sc = m > 0.0f ? 32639.0f / m : 0.0f;
       unit = m * (1.0f / 32639.0f) * a.scale * 1.44269504088896341f * (1.0f / 127.0f);
@@ -424,7 +424,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void kv_step(KvAttnArgs a) 
     const float akh = ak;
     // a page of zeros takes the smallest scale there is: its weights only enter the row's sum, and
     // must not set the scale of the others'
-    const float vs = (av > kMinMag ? av : kMinMag) * (1.0f / 127.0f);
+    const float vs = (av < kMinMag ? kMinMag : av) * (1.0f / 127.0f);
     const float lv = __builtin_amdgcn_logf(vs);  // log2
     v4i s[4];
 #pragma unroll
@@ -480,7 +480,9 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void kv_step(KvAttnArgs a) 
         // rne(32639 e) + 128 in the low 16 bits: high plane, and low plane + 128
         w[j] = __float_as_uint(__builtin_fmaf(e, 32639.0f, 12582912.0f + 128.0f));
       }
-      l_run = __builtin_fmaf(sum * beta, __builtin_amdgcn_rcpf(vs), l_run);
+      sum *= beta;
+      // a page that the row does not see may have any magnitude
+      l_run = sum == 0.0f ? l_run : __builtin_fmaf(sum, __builtin_amdgcn_rcpf(vs), l_run);
       v4i phi, plo;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -556,14 +558,14 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void kv_step(KvAttnArgs a) 
       for (int d = 0; d < ND; ++d)
         if (FULL || d * 16 < D) *reinterpret_cast<v4f*>(a.part_o + to * D + d * 16 + 4 * g) = acc[d];
     } else if (row_mine + nn < rows) {
-      const float inv = l_run > 0.0f ? 1.0f / l_run : 0.0f;
+      const float inv = l_run == 0.0f ? 0.0f : 1.0f / l_run;
       uint16_t* op = a.o.p + qrow * a.o.token + (int64_t)qh * a.o.head;
 #pragma unroll
       for (int d = 0; d < ND; ++d)
         if (FULL || d * 16 < D)
           *reinterpret_cast<uint2*>(op + d * 16 + 4 * g) = pack4(acc[d] * inv, a.bf16);
       if (a.lse && g == 0)
-        a.lse[qrow * a.q_heads + qh] = l_run > 0.0f ? (m_run + log2f(l_run)) * 0.693147180559945309f : kNegInf;
+        a.lse[qrow * a.q_heads + qh] = l_run == 0.0f ? kNegInf : (m_run + log2f(l_run)) * 0.693147180559945309f;
     }
   }
 }
@@ -634,9 +636,9 @@ __global__ __launch_bounds__(256) void kv_join(KvAttnArgs a) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[i] += x[i] * add;
   }
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   *reinterpret_cast<uint2*>(a.o.p + qrow * a.o.token + (int64_t)qh * a.o.head + tid * 4) = pack4(o * inv, a.bf16);
-  if (a.lse && tid == 0) a.lse[row] = l > 0.0f ? (top + log2f(l)) * 0.693147180559945309f : kNegInf;
+  if (a.lse && tid == 0) a.lse[row] = l == 0.0f ? kNegInf : (top + log2f(l)) * 0.693147180559945309f;
 }
 
 // Rows of a run: a sequence's rows together if they fit, so that its codes are

@@ -14,7 +14,8 @@
 // The magnitude of a page only grows, and the codes that it held are moved to
 // the new scale in the same pass, so that a page always has one scale whatever
 // the steps it was written in. Magnitudes under 2^-64 count as zero, so
-// that reciprocals and ratios of magnitudes stay in fp32.
+// that reciprocals and ratios of magnitudes stay in fp32. A NaN or infinity makes
+// the page's magnitude one, its codes zeros, and all that is read of them NaN.
 #include <algorithm>
 
 #include "kv_common.h"
@@ -240,17 +241,17 @@ __global__ __launch_bounds__(256, VEC ? 4 : 2) void kc_append(KvAppendArgs a, in
     float m = 0.0f;
     auto reduce = [&]() {
 #pragma unroll
-      for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
+      for (int o = 32; o > 0; o >>= 1) m = max_or_nan(m, __shfl_xor(m, o, 64));
       if constexpr (NT == 256) {
         if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
         __syncthreads();
-        m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+        m = max_or_nan(max_or_nan(red[0], red[1]), max_or_nan(red[2], red[3]));
       }
     };
     float now = 0.0f, scale = 0.0f;
     auto settle = [&]() {  // the page's new magnitude, and the codes that were there moved to it
       reduce();
-      now = fmaxf(old, m);
+      now = max_or_nan(old, m);
       now = now < kTiny ? 0.0f : now;
       scale = now > 0.0f ? 127.0f / now : 0.0f;
       if (tid == 0) *amax = now;
@@ -288,7 +289,7 @@ __global__ __launch_bounds__(256, VEC ? 4 : 2) void kc_append(KvAppendArgs a, in
       auto turn = [&](int t, int u, const Angles& ang, const uint4 raw[2], float f[16]) {
         turn_unit<BF16>(rope, rows + (int64_t)t * src.token, u, t0 + t, ang, raw, f);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) m = fmaxf(m, fabsf(f[j]));
+        for (int j = 0; j < 16; ++j) m = max_or_nan(m, fabsf(f[j]));
       };
       auto get = [&](int t, int u, float f[16]) {
         Angles ang;
@@ -348,7 +349,7 @@ __global__ __launch_bounds__(256, VEC ? 4 : 2) void kc_append(KvAppendArgs a, in
         float f[8];
         widen8<BF16>(raw[j], f);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(f[k]));
+        for (int k = 0; k < 8; ++k) m = max_or_nan(m, fabsf(f[k]));
       }
     };
     auto put = [&](int x, const uint4 raw[4]) {

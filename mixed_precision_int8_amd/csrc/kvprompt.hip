@@ -136,7 +136,7 @@ __global__ __launch_bounds__(64 * W, DP <= 128 ? 2 : 1) void kv_prompt(KvAttnArg
       }
       const float m = pair_max(bf16_bits_to_float(top));
       // powers of two 2^(13 - e) and its inverse, e the exponent of the row's largest channel
-      const int e = min(max((int)(__float_as_uint(m) >> 23) - 127, -100), 100);
+      const int e = min(max((int)(__float_as_uint(m) >> 23) - 127, -100), 127);
       const float up = __uint_as_float((uint32_t)(13 - e + 127) << 23);
       unit *= __uint_as_float((uint32_t)(e - 13 + 127) << 23);
 #pragma unroll
@@ -291,7 +291,7 @@ __global__ __launch_bounds__(64 * W, DP <= 128 ? 2 : 1) void kv_prompt(KvAttnArg
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int x = ONE ? 0 : k;
-      const float v = (sc.av[x] > kMinMag ? sc.av[x] : kMinMag) * (1.0f / 127.0f);
+      const float v = (sc.av[x] < kMinMag ? kMinMag : sc.av[x]) * (1.0f / 127.0f);
       f[k] = unit * sc.ak[x];
       lv[k] = __builtin_amdgcn_logf(v);  // log2
       rv[k] = __builtin_amdgcn_rcpf(v);
@@ -300,15 +300,18 @@ __global__ __launch_bounds__(64 * W, DP <= 128 ? 2 : 1) void kv_prompt(KvAttnArg
     if (base + 63 > all_end || base < all_begin || gone) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
+        bool any = false;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int x = base + 16 * k + 8 * hf + j;
           const bool see = !sc.gone[ONE ? 0 : k] && x <= last && (a.window <= 0 || x > pos - a.window || x < a.sinks);
           const float u = __builtin_fmaf(s[k >> 1][(k & 1) * 8 + j], f[k], lv[k]);
           s[k >> 1][(k & 1) * 8 + j] = see ? u : kNegInf;
+          any |= see;
         }
         f[k] = 1.0f;
         lv[k] = 0.0f;
+        rv[k] = any ? rv[k] : 0.0f;  // a page that the row does not see may have any magnitude
       }
     }
     float mt = kNegInf;
@@ -390,7 +393,7 @@ __global__ __launch_bounds__(64 * W, DP <= 128 ? 2 : 1) void kv_prompt(KvAttnArg
     }
     return;
   }
-  const float inv = l_run > 0.0f ? 1.0f / l_run : 0.0f;
+  const float inv = l_run == 0.0f ? 0.0f : 1.0f / l_run;
   uint16_t* op = a.o.p + qrow * a.o.token + (int64_t)qh * a.o.head;
 #pragma unroll
   for (int d = 0; d < ND; ++d)
@@ -403,7 +406,7 @@ __global__ __launch_bounds__(64 * W, DP <= 128 ? 2 : 1) void kv_prompt(KvAttnArg
       *reinterpret_cast<uint2*>(op + c) = a.bf16 ? make_uint2(Act16<true>::pack2(x0, x1), Act16<true>::pack2(x2, x3))
                                                  : make_uint2(Act16<false>::pack2(x0, x1), Act16<false>::pack2(x2, x3));
     }
-  if (a.lse && hf == 0) a.lse[row] = l_run > 0.0f ? (m_run - 8.0f + log2f(l_run)) * 0.693147180559945309f : kNegInf;
+  if (a.lse && hf == 0) a.lse[row] = l_run == 0.0f ? kNegInf : (m_run - 8.0f + log2f(l_run)) * 0.693147180559945309f;
 }
 
 // Wavefronts of a workgroup: four, two workgroups to a CU. Heads of 65 to 128

@@ -78,6 +78,7 @@ inline int admit_linear_4bit(int64_t T, int64_t K, int64_t N) {
 // (an item's first token is below len + rows + 2 seqs page < 2^31)
 constexpr int64_t kKvMax = int64_t(1) << 29;
 constexpr int64_t kKvMaxQHeads = 65536;
+constexpr int64_t kKvMaxQRows = int64_t(1) << 30;  // rows times query heads of an attention call
 inline int admit_kv_cache(int64_t pages, int64_t heads, int64_t page, int64_t dim) {
   if (pages <= 0 || heads <= 0 || page <= 0 || dim <= 0) return LLMINT8_ERR_INVALID_ARG;
   if (page != 16 && page != 32 && page != 64 && page != 128) return LLMINT8_ERR_UNSUPPORTED;

@@ -482,3 +482,111 @@ def test_attention_layer_over_steps():
         mine = m8.llmint8_kv_attention(c, batch, torch.from_numpy(q).cuda().half(), window=30, sinks=2)
         assert (np.abs(mine.double().cpu().numpy() - o) <= tol).all()
         assert torch.equal(layer.out(mine.view(-1, q_heads * dim)), got)
+
+
+MORE = [
+    # lens, counts, heads, q_heads, dim, page, dtype, options
+    ([3 + 7 * b % 90 for b in range(300)], [b % 3 for b in range(300)], 2, 4, 32, 16, "f16", {}),     # many sequences
+    ([40] * 520 + [5000], [1] * 521, 1, 2, 64, 16, "bf16", {}),                 # and one of them is cut
+    ([5000] + [30] * 99, [1] * 100, 1, 32, 32, 64, "f16", {}),                  # more than 2048 rows to join
+    ([2600, 3, 4100], [20, 3, 17], 2, 4, 128, 16, "bf16", {"window": 2500, "sinks": 40}),
+    ([5000], [200], 1, 1, 128, 64, "f16", {}),                                  # a prompt's tokens in parts
+    ([5000], [200], 1, 1, 80, 16, "bf16", {}),
+    ([3000, 2500], [90, 300], 1, 2, 256, 32, "f16", {"window": 1500, "sinks": 7}),
+    ([3000], [130], 2, 2, 64, 128, "bf16", {"causal": False}),
+    ([4000], [140], 1, 1, 48, 16, "f16", {}),
+    ([200, 90], [130, 90], 1, 3, 256, 16, "bf16", {}),                          # every width of page and head
+    ([200, 90], [130, 90], 1, 3, 176, 128, "f16", {}),
+    ([200, 90], [130, 90], 1, 3, 96, 32, "bf16", {}),
+    ([200, 90], [130, 90], 1, 3, 16, 32, "f16", {}),
+    ([70, 20], [2, 1], 1, 130, 16, 16, "f16", {}),                              # a group longer than a run
+    ([70, 20], [40, 20], 1, 257, 16, 64, "bf16", {}),
+    ([129, 1], [129, 1], 1, 128, 32, 16, "bf16", {}),
+]
+
+
+@pytest.mark.parametrize("case", MORE)
+def test_attention_of_many_sequences_long_contexts_and_other_heads(case):
+    lens, counts, heads, q_heads, dim, page, dtype, kw = case
+    _say(f"attention {len(lens)} sequences to {max(lens)} {case[2:]}")
+    s = Setup(61, lens, counts, heads, dim, page)
+    check_attention(s, q_heads, dtype, hints=(0, max(lens)), **kw)
+
+
+def test_append_and_gather_of_many_sequences():
+    n = 530
+    s = Setup(63, [1 + 13 * b % 70 for b in range(n)], [1 + b % 2 if b % 70 else 0 for b in range(n)], 2, 48, 32)
+    k, kx = s.values(2, "bf16")
+    v, vx = s.values(2, "bf16")
+    m8.llmint8_kv_append(s.cache, s.batch(), k, v)
+    s.ref.append(s.cu, s.lens, s.table, kx, vx)
+    s.same_cache()
+    gk, gv = m8.llmint8_kv_gather(s.cache, s.batch(), torch.bfloat16)
+    for b in range(n):
+        kx, vx, _ = s.ref.tokens(s.table, b, max(s.lens[b] - s.counts[b], 0), s.lens[b])
+        rows = slice(s.cu[b + 1] - len(kx), s.cu[b + 1])
+        assert torch.equal(gk[rows].cpu(), torch.from_numpy(kx).bfloat16()), b
+        assert torch.equal(gv[rows].cpu(), torch.from_numpy(vx).bfloat16()), b
+
+
+@pytest.mark.parametrize("lens,counts", [([6000, 5000, 40], [4, 4, 4]), ([600, 500, 40], [80, 80, 80])])
+def test_hostile_batches_on_cut_and_prompt_calls(lens, counts):
+    s = Setup(65, lens, counts, 2, 64, 16)
+    q, _ = s.values(4, "bf16")
+    n = s.rows
+    guard = torch.full((3 * n, 4, 64), 9.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((3 * n, 4), 9.0, device="cuda")
+    for cu in ([0, n - 4, 4, n], [0, 4, 90000, n], [-5, 4, 8, n], [3, 3, 3, 3], [n, 8, 4, 0], [0, 4, 8, 2 ** 31 - 1]):
+        for length in (lens, [2 ** 31 - 1, -7, 0]):
+            print(f"[case] {cu} {length}", flush=True)
+            m8.llmint8_kv_attention(s.cache, s.batch(max(lens), cu, length), q, out=guard[n:2 * n], lse=lse[n:2 * n])
+            torch.cuda.synchronize()
+            for x in (guard, lse):
+                assert (x[:n] == 9).all() and (x[2 * n:] == 9).all()
+
+
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("counts", [[1, 1], [4, 20], [300, 40]])
+def test_values_that_are_not_finite(counts, page):
+    """A NaN among a head's keys, an infinity among another's values: all of their pages reads as NaN and what
+    sees one of their tokens gets NaN; every other row gets what it does without them."""
+    lens, heads, q_heads, dim, dtype = [300, 40], 3, 6, 64, "bf16"
+    s = Setup(67, lens, lens, heads, dim, page)
+    k, kx = s.values(heads, dtype)
+    v, vx = s.values(heads, dtype)
+    s.ref.append(s.cu, s.lens, s.table, kx, vx)
+    nan_at, inf_at = 150, 260  # of the first sequence
+    k[nan_at, 0, 5] = math.nan
+    v[inf_at, 1, 63] = -math.inf
+    m8.llmint8_kv_append(s.cache, s.batch(), k, v)
+    gk, gv = m8.llmint8_kv_gather(s.cache, s.batch(), torch.bfloat16)
+    kx, vx, _ = s.ref.tokens(s.table, 0, 0, 300)
+    want_k, want_v = (torch.from_numpy(x).bfloat16() for x in (kx, vx))
+    pages = [slice(x // page * page, min(x // page * page + page, 300)) for x in (nan_at, inf_at)]
+    want_k[pages[0], 0] = math.nan
+    want_v[pages[1], 1] = math.nan
+    for got, want in ((gk[:300].cpu(), want_k), (gv[:300].cpu(), want_v)):
+        assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.nan_to_num(), want.nan_to_num())
+    s.counts = counts
+    s.cu = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    s.rows = int(s.cu[-1])
+    for kw in ({}, {"window": 60, "sinks": 2}):
+        q, qx = s.values(q_heads, dtype)
+        bad = counts[0] - 1  # a row with a NaN of its own, on the head of neither
+        q[bad, 5, 9] = math.nan
+        want, want_lse, (vmax, d) = s.ref.attention(s.cu, s.lens, s.table, qx, **kw)
+        lse = torch.empty((s.rows, q_heads), device="cuda")
+        for hint in (0, 300):
+            o = m8.llmint8_kv_attention(s.cache, s.batch(hint), q, lse=lse, **kw).double().cpu().numpy()
+            L = lse.double().cpu().numpy()
+            pos = 300 - counts[0] + np.arange(counts[0])
+            no = np.zeros((s.rows, q_heads), bool)
+            for h, sl in ((0, pages[0]), (1, pages[1])):
+                sees = (pos >= sl.start) & ((pos - kw["window"] < sl.stop - 1) if kw else True)
+                no[:counts[0], 2 * h:2 * h + 2] = sees[:, None]
+            no[bad, 5] = True
+            assert np.array_equal(np.isnan(o).any(2), no) and np.array_equal(np.isnan(o).all(2), no)
+            assert np.array_equal(np.isnan(L), no)
+            tol = U[dtype] * np.abs(want) + (vmax * (2.0 ** -10 + 2 * d + 2.0 ** -13))[..., None] + 2.0 ** -24
+            assert (np.abs(o - want)[~no] <= tol[~no]).all()
+            assert (np.abs(L - want_lse)[~no] <= (d + 2.0 ** -13 + 2.0 ** -20 * np.abs(want_lse))[~no]).all()

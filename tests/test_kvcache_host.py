@@ -204,3 +204,9 @@ def test_no_packed_fp32_or_scalar_writes_in_device_code():
             assert not re.search(r"^\s*s_(store|buffer_store|atomic|buffer_atomic|scratch_store|dcache_wb|dcache_discard)",
                                  text, re.M), src
             assert not re.search(r"\.vgpr_spill_count:\s*[1-9]", text), src
+
+
+def test_refusal_of_more_rows_than_the_kernels_index(lib):
+    assert attend(lib, b=batch(rows=1 << 26)) == UNSUPPORTED  # 2^31 rows of 32 heads
+    w = lib.llmint8_kv_attention_workspace_bytes
+    assert w(ctypes.byref(cache()), ctypes.byref(batch(rows=1 << 26)), 32, 0, 0) == 0

@@ -15,13 +15,13 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
   return (int64_t)((uint64_t)hi << 32 | lo);
 }
 
+// the larger of two, NaN if one of them is (fmaxf takes the other)
+__device__ __forceinline__ float max_or_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
 // Tokens of sequence b in this call: rows [row0, row0 + n), positions
 // [len - n, len). Every number is cut to what the buffers hold, so that no
 // content of cu, len or table makes a kernel leave them: cu to [0, T], n to
 // >= 0, len to [0, width * page].
-// the larger of two, NaN if one of them is (fmaxf takes the other)
-__device__ __forceinline__ float max_or_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }
-
 struct KvSeq {
   int b, row0, n, len;
 };

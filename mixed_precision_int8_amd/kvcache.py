@@ -114,7 +114,7 @@ class KVBatch:
 
 def _rows(t, dtype, rows, heads, dim, device, name):
     """(pointer, token stride, head stride) of 16-bit rows [rows, heads, dim] with dense channels."""
-    if t.dtype != dtype or t.dim() != 3 or tuple(t.shape) != (rows, heads, dim) or t.device != device:
+    if t.dtype != dtype or t.shape != (rows, heads, dim) or t.device != device:
         raise ValueError(f"{name}: expected {dtype} {(rows, heads, dim)} on {device}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
     st, sh, sc = t.stride()

@@ -590,3 +590,13 @@ def test_values_that_are_not_finite(counts, page):
             tol = U[dtype] * np.abs(want) + (vmax * (2.0 ** -10 + 2 * d + 2.0 ** -13))[..., None] + 2.0 ** -24
             assert (np.abs(o - want)[~no] <= tol[~no]).all()
             assert (np.abs(L - want_lse)[~no] <= (d + 2.0 ** -13 + 2.0 ** -20 * np.abs(want_lse))[~no]).all()
+
+
+def test_example_of_a_server():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "paged_decode.py")
+    spec = importlib.util.spec_from_file_location("paged_decode", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    example.main("--layers 1 --users 3 --steps 4 --q-heads 8 --heads 2 --dim 64 --context 300".split())

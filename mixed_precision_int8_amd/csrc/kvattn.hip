@@ -124,17 +124,17 @@ struct Part {
 // sequences of 1000-8000 tokens take 36.5 us, and 37.7 without it); with more,
 // twice that many beyond the runs' own, which evens out runs of different lengths.
 // A part of its own costs about 8 us of loads that wait for each other and of
-// joining, so none gets less than `least` tiles (16: about 9 us of work), and more
-// where the runs by themselves fill half the chip. Measured (32 query and 8
-// key/value heads of 128, us): 32 sequences of 2000-8000 tokens 73 (85 cut into
-// one part per resident workgroup, 102 uncut), 64 of 500-8000 94 (119 uncut), one
-// of 131000 53.
+// joining, so none gets less than `least` tiles (16, or 8 of two sixteens: about 9
+// us of work), and more where the runs by themselves fill half the chip. Measured
+// (32 query and 8 key/value heads of 128, us): 32 sequences of 2000-8000 tokens 73
+// (85 cut into one part per resident workgroup, 102 uncut), 64 of 500-8000 94 (119
+// uncut), one of 131000 53.
 struct Cutting {
   int64_t extra;  // parts beyond one to each run and head
   int least;      // tiles of a part
 };
 __host__ __device__ inline Cutting cutting(int64_t runs, int slots, int rt) {
-  return {runs * 4 <= slots ? slots - runs / 2 : (int64_t)2 * slots, (runs * 2 >= slots ? 48 : 16) / rt};
+  return {runs * 4 <= slots ? slots - runs / 2 : (int64_t)2 * slots, runs * 2 >= slots ? 48 : 16 / rt};
 }
 
 // Exclusive sums of two numbers over the workgroup's 256 threads, and their totals.
@@ -232,25 +232,38 @@ __device__ __forceinline__ bool find_part(const KvAttnArgs& a, int w, int64_t (&
   return true;
 }
 
-// A workgroup takes the tiles of a run of 16 RT rows: 4 / RT wavefronts to each
-// sixteen, which share its tiles, each with its own running maximum, sum and
-// output, and join at the end. The sixteens go over the same tiles at about the
-// same time, so that the codes come from memory once. K's codes of a wavefront's next
-// tile are asked for as soon as the first product has read the present ones, V's
-// after the second product, into the same registers: a tile is always on the way
-// while another is computed, and three wavefronts fit a SIMD (dim 128).
+// A workgroup of four wavefronts takes the tiles of a run of 16 RT rows, NT
+// sixteens to a wavefront; those of a sixteen share its tiles, each with its own
+// running maximum, sum and output, and join at the end. K's codes of a wavefront's
+// next tile are asked for as soon as the first product has read the present ones,
+// V's after the second product, into the same registers: a tile is always on the
+// way while another is computed, 16 KB of dim 128 for each of two wavefronts to a
+// SIMD. That, not the arithmetic (about 0.6 us of a SIMD's time to a tile and
+// sixteen), bounds the rate: 5.1 TB/s on one sequence of 131000 tokens, 4.9 on 64 of
+// 500-8000.
+//
+// Two sixteens: NT = 1 gives each two wavefronts, which go over the same tiles at
+// about the same time, so that the codes come from memory once; half as many
+// different ones are then on the way. NT = 2 takes both in the same wavefronts, one
+// after the other between the loads, with q in LDS: more to do before a part's
+// first and after its last tile. NT = 2 where the runs fill half the chip. Measured
+// (us, NT 1 / 2): 40 sequences of 1000-6000 tokens with 32 rows 83 / 67 (3.9 TB/s),
+// 16 of them 39 / 40, one of 1800 17 / 20.
 //
 // CUT: long runs are cut into parts (find_part); what a part has of its run goes
 // to the workspace for kv_join. Otherwise one workgroup to each run and head.
 // ONE: a tile is within one page (pages of 64 tokens and more), whose address is
 // then scalar. FULL: dim = DP.
-template <int DP, bool FULL, bool ONE, bool CUT, int RT>
+template <int DP, bool FULL, bool ONE, bool CUT, int RT, int NT>
 __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void kv_step(KvAttnArgs a) {
-  constexpr int WT = 4 / RT;  // wavefronts that share a sixteen's tiles
-  constexpr int NK = DP / 64;  // 64-channel steps of the first product
+  constexpr int WT = 4 * NT / RT;  // wavefronts that share a sixteen's tiles
+  constexpr int NK = (DP + 63) / 64;  // 64-channel steps of the first product
+  constexpr bool kWhole = FULL && DP % 64 == 0;  // which are all of them channels of the head
   constexpr int ND = DP / 16;  // 16-channel blocks of the second
-  __shared__ float sh_o[2][16][DP];
-  __shared__ float sh_ml[4][16][2];
+  __shared__ float sh_o[NT][2][16][DP];
+  __shared__ float sh_ml[NT][4][16][2];
+  __shared__ v4i sh_q[NT > 1 ? NT * NK * 2 * 64 : 1];
+  __shared__ float sh_unit[NT][16];
   __shared__ int sh_seq[5];
   __shared__ int sh_found[8];
   __shared__ int64_t sh_sums[8];
@@ -266,11 +279,11 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void kv_step(KvAttnArgs a) 
 #pragma unroll
   for (int ks = 0; ks < NK; ++ks) {
     const int c0 = ks * 64 + g * 16;  // channels past dim: any codes do, q is zero there
-    k_off[ks] = (uint32_t)((nn & 3) + (ONE ? k_tok : 0)) * D + (FULL || c0 < D ? c0 : 0);
+    k_off[ks] = (uint32_t)((nn & 3) + (ONE ? k_tok : 0)) * D + (kWhole || c0 < D ? c0 : 0);
   }
 #pragma unroll
   for (int d = 0; d < ND; ++d)
-    v_off[d] = (uint32_t)(FULL ? d * 16 + nn : min(d * 16 + nn, D - 1)) * P + (ONE ? v_tok : 0);
+    v_off[d] = (uint32_t)((FULL || d * 16 < D ? d * 16 : 0) + nn) * P + (ONE ? v_tok : 0);  // as for K
 
   KvSeq sq;
   Part p{};
@@ -285,11 +298,16 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void kv_step(KvAttnArgs a) 
   }
   const int h = p.h;
   const int b = sq.b, rows = sq.n * G, row_first = p.run * 16 * RT;
-  const int row_mine = row_first + 16 * (wave / WT);  // of this wavefront's sixteen
-  const int r = min(row_mine + nn, rows - 1), tok = r / G;
-  const int pos = sq.len - sq.n + tok;
-  const int64_t qrow = sq.row0 + tok;
-  const int qh = h * G + (r - tok * G);
+  const int sub = wave % WT, six = wave / WT;  // place in the sixteen's wavefronts, and first sixteen
+  // row nn of this wavefront's t-th sixteen: its place in q and the outputs, and its position
+  struct Row {
+    int64_t row;
+    int head, pos;
+  };
+  auto row_of = [&](int t) {
+    const int r = min(row_first + 16 * (six + t) + nn, rows - 1), tok = r / G;
+    return Row{sq.row0 + tok, h * G + (r - tok * G), sq.len - sq.n + tok};
+  };
   const int pos_lo = sq.len - sq.n + row_first / G;  // of the run
   const int pos_hi = sq.len - sq.n + min(row_first + 16 * RT - 1, rows - 1) / G;
   const Span span = CUT ? seq_work<RT>(a, sq).span
@@ -325,7 +343,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void kv_step(KvAttnArgs a) 
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int ks = 0; ks < NK; ++ks) kf[j][ks] = load16<RT == 1>(kp + (k_off[ks] + 4 * j * D));
+      for (int ks = 0; ks < NK; ++ks) kf[j][ks] = load16<NT == RT>(kp + (k_off[ks] + 4 * j * D));
     const int64_t hv = (int64_t)max(pv, 0) * H + h;
     *ak = a.c.aK[hv];
     *av = a.c.aV[hv];
@@ -336,25 +354,27 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void kv_step(KvAttnArgs a) 
     const int pv = kv_page(ONE ? uniform(p.v) : p.v, a.c.pages);
     const int8_t* vp = a.c.V + ((int64_t)max(pv, 0) * H + h) * page_bytes + ((ONE ? base : base + v_tok) & (P - 1));
 #pragma unroll
-    for (int d = 0; d < ND; ++d) vf[d] = load16<RT == 1>(vp + v_off[d]);
+    for (int d = 0; d < ND; ++d) vf[d] = load16<NT == RT>(vp + v_off[d]);
   };
 
-  int it = row_mine < rows ? i0 + wave % WT : i1, page = -1;
+  int it = row_first + 16 * six < rows ? i0 + sub : i1, page = -1;
   float ak = 0.0f, av = 0.0f;
   Pages next{-1, -1};
 
-  // q: 16-bit integers in two planes, and what one unit of S stands for
+  // q: 16-bit integers in two planes, and what one unit of S stands for. One sixteen's stay in registers; of
+  // two each is prepared by one wavefront and read from LDS by all.
   v4i qhi[NK], qlo[NK];
-  float unit;
+  float unit[NT];
   {
+    const Row mine = row_of(wave % NT);
     uint32_t w[NK][8];
     {
-      const uint16_t* qp = a.q.p + qrow * a.q.token + (int64_t)qh * a.q.head;
+      const uint16_t* qp = a.q.p + mine.row * a.q.token + (int64_t)mine.head * a.q.head;
 #pragma unroll
       for (int ks = 0; ks < NK; ++ks) {
         const int c0 = ks * 64 + g * 16;
         uint4 x = make_uint4(0, 0, 0, 0), y = x;
-        if (FULL || c0 < D) {
+        if (kWhole || c0 < D) {
           x = *reinterpret_cast<const uint4*>(qp + c0);
           y = *reinterpret_cast<const uint4*>(qp + c0 + 8);
         }
@@ -387,7 +407,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void kv_step(KvAttnArgs a) 
         for (int j = 0; j < 16; ++j) m = max_or_nan(m, fabsf(f[ks][j]));
       m = row_max(m);
       const float sc = m > 0.0f ? 32639.0f / m : 0.0f;
-      unit = m * (1.0f / 32639.0f) * a.scale * 1.44269504088896341f * (1.0f / 127.0f);
+      unit[0] = m * (1.0f / 32639.0f) * a.scale * 1.44269504088896341f * (1.0f / 127.0f);
 #pragma unroll
       for (int ks = 0; ks < NK; ++ks) {
         uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
@@ -404,12 +424,36 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void kv_step(KvAttnArgs a) 
     }
   }
 
-  v4f acc[ND];
+  if constexpr (NT > 1) {
+    if (wave < NT) {
 #pragma unroll
-  for (int d = 0; d < ND; ++d) acc[d] = v4f{0, 0, 0, 0};
-  float m_run = kNegInf, l_run = 0.0f;
-  // the last token that a row sees, but for its window; < 0: none
-  const int last = a.causal ? min(pos, sq.len - 1) : sq.len - 1;
+      for (int ks = 0; ks < NK; ++ks) {
+        sh_q[((wave * NK + ks) * 2) * 64 + lane] = qhi[ks];
+        sh_q[((wave * NK + ks) * 2 + 1) * 64 + lane] = qlo[ks];
+      }
+      if (g == 0) sh_unit[wave][nn] = unit[0];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < NT; ++t) unit[t] = sh_unit[t][nn];
+  }
+  auto q_plane = [&](int t, int ks, int lo) {
+    if constexpr (NT > 1) return sh_q[((t * NK + ks) * 2 + lo) * 64 + lane];
+    return lo ? qlo[ks] : qhi[ks];
+  };
+
+  v4f acc[NT][ND];
+  float m_run[NT], l_run[NT];
+  int pos[NT], last[NT];  // last: the last token that a row sees, but for its window; < 0: none
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+#pragma unroll
+    for (int d = 0; d < ND; ++d) acc[t][d] = v4f{0, 0, 0, 0};
+    m_run[t] = kNegInf;
+    l_run[t] = 0.0f;
+    pos[t] = row_of(t).pos;
+    last[t] = a.causal ? min(pos[t], sq.len - 1) : sq.len - 1;
+  }
   const int all_end = a.causal ? min(pos_lo, sq.len - 1) : sq.len - 1;  // seen by every row, up to its window
   const int all_begin = a.window > 0 ? pos_hi - a.window + 1 : 0;
 
@@ -426,34 +470,40 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void kv_step(KvAttnArgs a) 
     // must not set the scale of the others'
     const float vs = (av < kMinMag ? kMinMag : av) * (1.0f / 127.0f);
     const float lv = __builtin_amdgcn_logf(vs);  // log2
-    v4i s[4];
+    v4i s[NT][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        s[j] = v4i{0, 0, 0, 0};
+        s[t][j] = v4i{0, 0, 0, 0};
 #pragma unroll
-        for (int ks = 0; ks < NK; ++ks) s[j] = mfma_i8(kf[j][ks], qhi[ks], s[j]);
+        for (int ks = 0; ks < NK; ++ks) s[t][j] = mfma_i8(kf[j][ks], q_plane(t, ks, 0), s[t][j]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[j][i] <<= 8;
+        for (int i = 0; i < 4; ++i) s[t][j][i] <<= 8;
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int ks = 0; ks < NK; ++ks) s[j] = mfma_i8(kf[j][ks], qlo[ks], s[j]);
+        for (int ks = 0; ks < NK; ++ks) s[t][j] = mfma_i8(kf[j][ks], q_plane(t, ks, 1), s[t][j]);
+    }
     const int here = page;
     if (MORE) load_k(it + WT, next, &ak, &av, &page);
-    {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      if (t > 0 && row_first + 16 * t >= rows) break;  // t > 0: six is 0
+      if (NT > 1) __builtin_amdgcn_sched_barrier(0);
       float u[16];
-      const float fk = unit * akh;
+      const float fk = unit[t] * akh;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) u[4 * j + i] = __builtin_fmaf((float)s[j][i], fk, lv);
+        for (int i = 0; i < 4; ++i) u[4 * j + i] = __builtin_fmaf((float)s[t][j][i], fk, lv);
       // what a row does not see; tiles inside every row's range need no look at single tokens
       if (base + 63 > all_end || base < all_begin || (ONE ? here < 0 : __any(here < 0))) {
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           const int x = base + v_tok + j;
-          const bool see = here >= 0 && x <= last && (a.window <= 0 || x > pos - a.window || x < a.sinks);
+          const bool see = here >= 0 && x <= last[t] && (a.window <= 0 || x > pos[t] - a.window || x < a.sinks);
           u[j] = see ? u[j] : kNegInf;
         }
       }
@@ -462,15 +512,15 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void kv_step(KvAttnArgs a) 
       for (int j = 1; j < 16; ++j) mt = fmaxf(mt, u[j]);
       mt = row_max(mt);
       const float mt0 = mt == kNegInf ? 0.0f : mt;
-      if (__any(mt > m_run)) {  // a new maximum of some row: what was summed moves to it
-        const float m_new = fmaxf(m_run, mt);
-        const float alpha = m_run == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m_run - m_new);
-        m_run = m_new;
-        l_run *= alpha;
+      if (__any(mt > m_run[t])) {  // a new maximum of some row: what was summed moves to it
+        const float m_new = fmaxf(m_run[t], mt);
+        const float alpha = m_run[t] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m_run[t] - m_new);
+        m_run[t] = m_new;
+        l_run[t] *= alpha;
 #pragma unroll
-        for (int d = 0; d < ND; ++d) acc[d] *= alpha;
+        for (int d = 0; d < ND; ++d) acc[t][d] *= alpha;
       }
-      const float beta = mt == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mt - m_run);
+      const float beta = mt == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mt - m_run[t]);
       float sum = 0.0f;
       uint32_t w[16];
 #pragma unroll
@@ -482,7 +532,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void kv_step(KvAttnArgs a) 
       }
       sum *= beta;
       // a page that the row does not see may have any magnitude
-      l_run = sum == 0.0f ? l_run : __builtin_fmaf(sum, __builtin_amdgcn_rcpf(vs), l_run);
+      l_run[t] = sum == 0.0f ? l_run[t] : __builtin_fmaf(sum, __builtin_amdgcn_rcpf(vs), l_run[t]);
       v4i phi, plo;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -501,7 +551,8 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void kv_step(KvAttnArgs a) 
         for (int i = 0; i < 4; ++i) o[i] <<= 8;
         o = mfma_i8(vf[d], plo, o);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[d][i] = __builtin_fmaf((float)o[i], bu, acc[d][i]);
+        for (int i = 0; i < 4; ++i) acc[t][d][i] = __builtin_fmaf((float)o[i], bu, acc[t][d][i]);
+        if (NT > 1 && d % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // or the products' results take the registers
       }
     }
     if (MORE) load_v(it + WT, next);
@@ -513,59 +564,76 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void kv_step(KvAttnArgs a) 
     tile(std::false_type{});
   }
 
-  // join the WT wavefronts of a sixteen
-  l_run = row_sum(l_run);
-  const int t = wave / WT, w0 = t * WT;
-  if (WT > 1) {
+  // join a sixteen's wavefronts
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    l_run[t] = row_sum(l_run[t]);
     if (g == 0) {
-      sh_ml[wave][nn][0] = m_run;
-      sh_ml[wave][nn][1] = l_run;
-    }
-    __syncthreads();
-    float m_all = m_run;
-#pragma unroll
-    for (int w = 0; w < WT; ++w) m_all = fmaxf(m_all, sh_ml[w0 + w][nn][0]);
-    const float m0 = m_all == kNegInf ? 0.0f : m_all;
-    const float mine = __builtin_amdgcn_exp2f(m_run - m0);
-    m_run = m_all;
-    l_run = 0.0f;
-#pragma unroll
-    for (int w = 0; w < WT; ++w) l_run += sh_ml[w0 + w][nn][1] * __builtin_amdgcn_exp2f(sh_ml[w0 + w][nn][0] - m0);
-#pragma unroll
-    for (int d = 0; d < ND; ++d) acc[d] *= mine;
-    const int sub = wave % WT;
-#pragma unroll
-    for (int half = WT / 2; half > 0; half >>= 1) {
-      if (sub >= half && sub < 2 * half)
-#pragma unroll
-        for (int d = 0; d < ND; ++d) *reinterpret_cast<v4f*>(&sh_o[t * (WT / 2) + sub - half][nn][d * 16 + 4 * g]) = acc[d];
-      __syncthreads();
-      if (sub < half)
-#pragma unroll
-        for (int d = 0; d < ND; ++d) acc[d] += *reinterpret_cast<const v4f*>(&sh_o[t * (WT / 2) + sub][nn][d * 16 + 4 * g]);
-      if (half > 1) __syncthreads();
+      sh_ml[t][wave][nn][0] = m_run[t];
+      sh_ml[t][wave][nn][1] = l_run[t];
     }
   }
-  // which parts there are of a row, for the join
-  if (CUT && p.part == 0 && g == 0 && wave % WT == 0 && row_mine + nn < rows)
-    *reinterpret_cast<v2i*>(a.notes + (qrow * a.q_heads + qh) * 2) =
-        v2i{p.parts > 1 ? (p.slot << kKvNoteShift | 16 * t | nn) : -1, p.parts};
-  if (wave % WT == 0 && row_mine < rows) {
+  __syncthreads();
+  auto give = [&](int t, int to) {
+#pragma unroll
+    for (int d = 0; d < ND; ++d) *reinterpret_cast<v4f*>(&sh_o[t][to][nn][d * 16 + 4 * g]) = acc[t][d];
+  };
+  auto take = [&](int t, int from) {
+#pragma unroll
+    for (int d = 0; d < ND; ++d) acc[t][d] += *reinterpret_cast<const v4f*>(&sh_o[t][from][nn][d * 16 + 4 * g]);
+  };
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    float m_all = m_run[t];
+#pragma unroll
+    for (int w = 0; w < WT; ++w) m_all = fmaxf(m_all, sh_ml[t][six * WT + w][nn][0]);
+    const float m0 = m_all == kNegInf ? 0.0f : m_all;
+    const float mine = __builtin_amdgcn_exp2f(m_run[t] - m0);
+    m_run[t] = m_all;
+    l_run[t] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WT; ++w)
+      l_run[t] += sh_ml[t][six * WT + w][nn][1] * __builtin_amdgcn_exp2f(sh_ml[t][six * WT + w][nn][0] - m0);
+#pragma unroll
+    for (int d = 0; d < ND; ++d) acc[t][d] *= mine;
+    if (sub >= WT / 2) give(t, WT == 4 ? sub - 2 : six);
+  }
+  __syncthreads();
+  if (WT == 4) {  // halves to halves, then wavefront t ends with sixteen t
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      if (sub >= 2) break;
+      take(t, sub);
+      if (sub != t) give(t, sub);  // where it read from itself
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int row_mine = row_first + 16 * (six + t);
+    if (sub != t || row_mine >= rows) continue;
+    take(t, WT == 4 ? 1 - sub : six);
+    const Row r = row_of(t);
+    const bool in = row_mine + nn < rows;
+    // which parts there are of a row, for the join
+    if (CUT && p.part == 0 && g == 0 && in)
+      *reinterpret_cast<v2i*>(a.notes + (r.row * a.q_heads + r.head) * 2) =
+          v2i{p.parts > 1 ? (p.slot << kKvNoteShift | 16 * (six + t) | nn) : -1, p.parts};
     if (CUT && p.parts > 1) {
-      const int64_t to = (int64_t)p.slot * (16 * RT) + 16 * t + nn;
-      if (g == 0) *reinterpret_cast<v2f*>(a.part_ml + to * 2) = v2f{m_run, l_run};
+      const int64_t to = (int64_t)p.slot * (16 * RT) + 16 * (six + t) + nn;
+      if (g == 0) *reinterpret_cast<v2f*>(a.part_ml + to * 2) = v2f{m_run[t], l_run[t]};
 #pragma unroll
       for (int d = 0; d < ND; ++d)
-        if (FULL || d * 16 < D) *reinterpret_cast<v4f*>(a.part_o + to * D + d * 16 + 4 * g) = acc[d];
-    } else if (row_mine + nn < rows) {
-      const float inv = l_run == 0.0f ? 0.0f : 1.0f / l_run;
-      uint16_t* op = a.o.p + qrow * a.o.token + (int64_t)qh * a.o.head;
+        if (FULL || d * 16 < D) *reinterpret_cast<v4f*>(a.part_o + to * D + d * 16 + 4 * g) = acc[t][d];
+    } else if (in) {
+      const float inv = l_run[t] == 0.0f ? 0.0f : 1.0f / l_run[t];
+      uint16_t* op = a.o.p + r.row * a.o.token + (int64_t)r.head * a.o.head;
 #pragma unroll
       for (int d = 0; d < ND; ++d)
-        if (FULL || d * 16 < D)
-          *reinterpret_cast<uint2*>(op + d * 16 + 4 * g) = pack4(acc[d] * inv, a.bf16);
+        if (FULL || d * 16 < D) *reinterpret_cast<uint2*>(op + d * 16 + 4 * g) = pack4(acc[t][d] * inv, a.bf16);
       if (a.lse && g == 0)
-        a.lse[qrow * a.q_heads + qh] = l_run == 0.0f ? kNegInf : (m_run + log2f(l_run)) * 0.693147180559945309f;
+        a.lse[r.row * a.q_heads + r.head] =
+            l_run[t] == 0.0f ? kNegInf : (m_run[t] + log2f(l_run[t])) * 0.693147180559945309f;
     }
   }
 }
@@ -657,49 +725,60 @@ bool kv_attention_prompt(const KvBatch& s, int heads, int q_heads) {
   return (int64_t)s.T * (q_heads / heads) > (int64_t)32 * s.B;
 }
 
+static int64_t runs_about(const KvBatch& s, int heads, int q_heads) {
+  return std::max<int64_t>(s.B, (int64_t)s.T * (q_heads / heads) / kv_attention_run(s, heads, q_heads)) * heads;
+}
 static int64_t runs_at_most(const KvBatch& s, int heads, int q_heads) {
   return (int64_t)s.T * (q_heads / heads) / kv_attention_run(s, heads, q_heads) + s.B;
 }
 
 // Whether a call's runs are cut into parts, and how many more workgroups that
-// takes at most. 0: not cut, where the longest context is no more than 2048
-// tokens, or 4096 and the runs fill half the chip: there the join costs more than
-// the cut gains (one sequence of 2000 tokens: 19 us uncut, 24 cut; 64 of 1000-2000
-// 41 and 56). *slots: workgroups that run at once, three, two or one to a CU by
-// the registers of the head size.
+// takes at most. 0: not cut, where the longest context (twice, for runs of two
+// sixteens) is no more than 4096 tokens, or, with fewer runs than a quarter of
+// what the chip holds, than 2304 over the share of the chip that they leave idle:
+// there the join costs more than the cut gains. Measured, us uncut / cut: one
+// sequence of 2000 tokens 19 / 24; 16 of 2000-3000 29 / 28 and of 2000-4000 36 /
+// 29; 24 of 2000-4000 37 / 42; 64 of 1000-2000 41 / 56. *slots: workgroups that
+// run at once, three, two or one to a CU by the registers of the head size.
 int kv_attention_extra(const KvBatch& s, int heads, int q_heads, int dim, int64_t max_span, int num_cus, int* slots) {
   *slots = num_cus * (dim <= 64 ? 3 : dim <= 128 ? 2 : 1);
-  const int64_t runs =
-      std::max<int64_t>(s.B, (int64_t)s.T * (q_heads / heads) / kv_attention_run(s, heads, q_heads)) * heads;
+  const int64_t runs = runs_about(s, heads, q_heads);
   const int rt = kv_attention_run(s, heads, q_heads) / 16;
-  if (max_span * rt <= (runs * 2 >= *slots ? 4096 : 2048)) return 0;
+  if (max_span * rt <= (runs * 4 > *slots ? 4096 : 2304 * *slots / (*slots - runs))) return 0;
   const int64_t tiles = (max_span + 63) / 64, least = cutting(1, *slots, rt).least, most = (tiles + least - 1) / least - 1;
   return (int)std::min<int64_t>(2 * *slots, most * runs_at_most(s, heads, q_heads) * heads);
 }
 
-template <int DP, bool FULL, bool ONE, int RT>
+template <int DP, bool FULL, bool ONE, int RT, int NT>
 static hipError_t launch_runs(const KvAttnArgs& a, hipStream_t stream) {
   const int64_t blocks = runs_at_most(a.s, a.c.heads, a.q_heads) * a.c.heads + a.extra;
   if (blocks > INT32_MAX) return hipErrorInvalidConfiguration;
   if (a.extra > 0)
-    hipLaunchKernelGGL((kv_step<DP, FULL, ONE, true, RT>), dim3((unsigned)blocks), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((kv_step<DP, FULL, ONE, true, RT, NT>), dim3((unsigned)blocks), dim3(256), 0, stream, a);
   else
-    hipLaunchKernelGGL((kv_step<DP, FULL, ONE, false, RT>), dim3((unsigned)blocks), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((kv_step<DP, FULL, ONE, false, RT, NT>), dim3((unsigned)blocks), dim3(256), 0, stream, a);
   return hipGetLastError();
+}
+
+template <int DP, bool FULL, bool ONE>
+static hipError_t launch_pages(const KvAttnArgs& a, hipStream_t stream) {
+  if (a.run == 16) return launch_runs<DP, FULL, ONE, 1, 1>(a, stream);
+  if (runs_about(a.s, a.c.heads, a.q_heads) * 2 >= a.slots) return launch_runs<DP, FULL, ONE, 2, 2>(a, stream);
+  return launch_runs<DP, FULL, ONE, 2, 1>(a, stream);
 }
 
 template <int DP, bool FULL>
 static hipError_t launch_step(const KvAttnArgs& a, hipStream_t stream) {
-  if (a.c.page_shift >= 6)
-    return a.run == 16 ? launch_runs<DP, FULL, true, 1>(a, stream) : launch_runs<DP, FULL, true, 2>(a, stream);
-  return a.run == 16 ? launch_runs<DP, FULL, false, 1>(a, stream) : launch_runs<DP, FULL, false, 2>(a, stream);
+  return a.c.page_shift >= 6 ? launch_pages<DP, FULL, true>(a, stream) : launch_pages<DP, FULL, false>(a, stream);
 }
 
 static hipError_t launch_kv_step(const KvAttnArgs& a, hipStream_t stream) {
   if (a.c.dim == 64) return launch_step<64, true>(a, stream);
   if (a.c.dim < 64) return launch_step<64, false>(a, stream);
+  if (a.c.dim < 96) return launch_step<96, false>(a, stream);
+  if (a.c.dim == 96) return launch_step<96, true>(a, stream);
+  if (a.c.dim == 112) return launch_step<112, true>(a, stream);
   if (a.c.dim == 128) return launch_step<128, true>(a, stream);
-  if (a.c.dim < 128) return launch_step<128, false>(a, stream);
   return launch_step<256, false>(a, stream);
 }
 

@@ -592,6 +592,22 @@ def test_values_that_are_not_finite(counts, page):
             assert (np.abs(L - want_lse)[~no] <= (d + 2.0 ** -13 + 2.0 ** -20 * np.abs(want_lse))[~no]).all()
 
 
+@pytest.mark.parametrize("dim,page,dtype,longest", [(64, 64, "bf16", 200), (64, 16, "f16", 4400), (80, 32, "bf16", 4400),
+                                                    (96, 64, "f16", 4400), (96, 16, "f16", 150), (112, 16, "bf16", 150),
+                                                    (112, 128, "bf16", 4400), (128, 64, "f16", 150), (48, 16, "f16", 150),
+                                                    (128, 32, "bf16", 4400), (256, 64, "f16", 4400), (192, 16, "f16", 99)])
+def test_attention_of_drafted_tokens_of_a_large_batch(dim, page, dtype, longest):
+    """Runs of two sixteens, enough of them to fill half the chip: some of one sixteen only, some of no rows."""
+    heads, G = 16, 5
+    counts = [(0, 3, 4, 5, 6, 9)[b % 6] for b in range(26)]
+    lens = [max(n, 5 + 37 * b % 150) for b, n in enumerate(counts)]
+    lens[4] = longest
+    s = Setup(71, lens, counts, heads, dim, page)
+    _say(f"drafts {dim} {page} {dtype} {longest}")
+    check_attention(s, heads * G, dtype, hints=(0, 1))
+    check_attention(s, heads * G, dtype, window=64, sinks=2)
+
+
 def test_example_of_a_server():
     import importlib.util
     import os

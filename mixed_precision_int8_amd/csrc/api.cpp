@@ -234,6 +234,7 @@ llmint8_status run_backward_input(const void* dY, int64_t T, int64_t K, const in
 }  // namespace
 
 namespace llmint8 {
+// for kv_api.cpp
 llmint8_status abi_hip_status(hipError_t e) { return hip_status(e); }
 int abi_cu_count() { return device_cu_count(); }
 

@@ -128,10 +128,6 @@ int linear_static_scratch(const void* X, int dtype, int64_t T, int64_t K, const 
                           const float* sW, int64_t N, float threshold, const void* bias, void* Y,
                           ScratchSource scratch, size_t scratch_bytes, void* stream);
 
-// api.cpp: the status of a HIP result (kept for llmint8_last_hip_error), the device's CUs
-int abi_hip_status(hipError_t e);
-int abi_cu_count();
-
 // Launchers (each enqueues exactly one kernel on `stream`).
 hipError_t launch_quantize_weight(const uint16_t* W, int N, int K, int8_t* Wq, float* sW, bool bf16,
                                   hipStream_t stream);
@@ -180,74 +176,5 @@ hipError_t launch_dequantize_4bit(const uint8_t* packed, const float* absmax, in
                                   hipStream_t stream);
 hipError_t launch_linear_4bit(const FourBitArgs& a, const Code4& book, bool bf16, int num_cus,
                               hipStream_t stream);
-
-// ---- the int8 key/value cache
-
-// The cache: codes K [pages, heads, page, dim], V [pages, heads, dim, page] and the
-// largest magnitudes aK, aV [pages, heads].
-struct KvCache {
-  int8_t* K;
-  int8_t* V;
-  float* aK;
-  float* aV;
-  int64_t pages;
-  int heads, dim, page_shift;
-};
-// The sequences of a call (device arrays) and their sizes.
-struct KvBatch {
-  const int32_t* cu;     // [B + 1]
-  const int32_t* len;    // [B]
-  const int32_t* table;  // [B, width]
-  int B, T, width;
-};
-// 16-bit rows [T, heads, dim]: strides in elements, channels dense
-struct KvRows {
-  uint16_t* p;
-  int64_t token, head;
-};
-struct KvAppendArgs {
-  KvCache c;
-  KvBatch s;
-  KvRows k, v, q, qo;  // q.p null: no q
-  const float* rope;   // [rope_rows, rot] (cos, then sin), or null
-  int q_heads, rope_rows, rot, interleaved;
-};
-hipError_t launch_kv_append(const KvAppendArgs& a, bool bf16, hipStream_t stream);
-hipError_t launch_kv_gather(const KvCache& c, const KvBatch& s, const KvRows& k, const KvRows& v, bool bf16,
-                            int num_cus, hipStream_t stream);
-// rope[p][i] = mag cos(p f[i]), rope[p][n + i] = mag sin(p f[i])
-constexpr int kRopeMaxPairs = 128;
-struct RopeFreq {
-  double f[kRopeMaxPairs];
-};
-hipError_t launch_rope_table(const RopeFreq& f, int pairs, int rows, double mag, float* table,
-                             hipStream_t stream);
-struct KvAttnArgs {
-  KvCache c;
-  KvBatch s;
-  KvRows q, o;
-  float* lse;  // [T, q_heads] or null
-  float scale;
-  int bf16, q_heads, causal, window, sinks;
-  // Runs of rows with long contexts are cut into parts, for `extra` workgroups at
-  // most beyond one to each run and head (0: not cut); `slots` workgroups run at
-  // once. What the parts leave for the join: [max_parts, run, dim] and
-  // [max_parts, run, 2], and notes [T * q_heads, 2] of each row's parts.
-  int prompt;  // kv_prompt instead of kv_step; splits: parts of its tokens (1: not cut)
-  int splits;
-  int run, extra, slots, max_parts;
-  float* part_o;
-  float* part_ml;
-  int* notes;
-};
-constexpr int kKvNoteShift = 8;  // a note: part << shift | row of the part, number of parts
-int kv_attention_run(const KvBatch& s, int heads, int q_heads);  // rows of a run: 16 or 32
-int kv_attention_extra(const KvBatch& s, int heads, int q_heads, int dim, int64_t max_span, int num_cus,
-                       int* slots);
-bool kv_attention_prompt(const KvBatch& s, int heads, int q_heads);
-int kv_prompt_splits(const KvBatch& s, int heads, int q_heads, int dim, int page_shift, int64_t max_span,
-                     int num_cus, int* run, int* max_parts);
-hipError_t launch_kv_prompt(const KvAttnArgs& a, hipStream_t stream);
-hipError_t launch_kv_attention(const KvAttnArgs& a, hipStream_t stream);
 
 }  // namespace llmint8

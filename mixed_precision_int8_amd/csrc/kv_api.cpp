@@ -9,7 +9,7 @@
 #include <cstdint>
 
 #include "../../include/llmint8.h"
-#include "internal.h"
+#include "kv_internal.h"
 
 using namespace llmint8;
 

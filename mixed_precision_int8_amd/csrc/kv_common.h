@@ -3,9 +3,11 @@
 #pragma once
 
 #include "device_util.h"
-#include "internal.h"
+#include "kv_internal.h"
 
 namespace llmint8 {
+
+typedef int v2i __attribute__((ext_vector_type(2)));
 
 // A value that all lanes hold, moved to a scalar register.
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }

@@ -1,0 +1,98 @@
+// The int8 key/value cache's part of internal.h: admission limits, what the
+// kernels take, launchers.
+#pragma once
+
+#include "internal.h"
+#include "ranges.h"
+
+namespace llmint8 {
+
+// api.cpp: the status of a HIP result (kept for llmint8_last_hip_error), the device's CUs
+int abi_hip_status(hipError_t e);
+int abi_cu_count();
+
+// The kernels index tokens, rows and work items in 32 bits
+// (an item's first token is below len + rows + 2 seqs page < 2^31)
+constexpr int64_t kKvMax = int64_t(1) << 29;
+constexpr int64_t kKvMaxQHeads = 65536;
+constexpr int64_t kKvMaxQRows = int64_t(1) << 30;  // rows times query heads of an attention call
+inline int admit_kv_cache(int64_t pages, int64_t heads, int64_t page, int64_t dim) {
+  if (pages <= 0 || heads <= 0 || page <= 0 || dim <= 0) return LLMINT8_ERR_INVALID_ARG;
+  if (page != 16 && page != 32 && page != 64 && page != 128) return LLMINT8_ERR_UNSUPPORTED;
+  if (dim % 16 != 0 || dim > 256 || heads > 4096 || pages >= kTwo31) return LLMINT8_ERR_UNSUPPORTED;
+  return LLMINT8_OK;
+}
+inline int admit_kv_batch(int64_t seqs, int64_t rows, int64_t width, int64_t page) {
+  if (seqs < 0 || rows < 0 || width <= 0) return LLMINT8_ERR_INVALID_ARG;
+  if (rows > kKvMax || width > kKvMax / page || seqs > kKvMax / (2 * page)) return LLMINT8_ERR_UNSUPPORTED;
+  return LLMINT8_OK;
+}
+
+// The cache: codes K [pages, heads, page, dim], V [pages, heads, dim, page] and the
+// largest magnitudes aK, aV [pages, heads].
+struct KvCache {
+  int8_t* K;
+  int8_t* V;
+  float* aK;
+  float* aV;
+  int64_t pages;
+  int heads, dim, page_shift;
+};
+// The sequences of a call (device arrays) and their sizes.
+struct KvBatch {
+  const int32_t* cu;     // [B + 1]
+  const int32_t* len;    // [B]
+  const int32_t* table;  // [B, width]
+  int B, T, width;
+};
+// 16-bit rows [T, heads, dim]: strides in elements, channels dense
+struct KvRows {
+  uint16_t* p;
+  int64_t token, head;
+};
+struct KvAppendArgs {
+  KvCache c;
+  KvBatch s;
+  KvRows k, v, q, qo;  // q.p null: no q
+  const float* rope;   // [rope_rows, rot] (cos, then sin), or null
+  int q_heads, rope_rows, rot, interleaved;
+};
+hipError_t launch_kv_append(const KvAppendArgs& a, bool bf16, hipStream_t stream);
+hipError_t launch_kv_gather(const KvCache& c, const KvBatch& s, const KvRows& k, const KvRows& v, bool bf16,
+                            int num_cus, hipStream_t stream);
+// rope[p][i] = mag cos(p f[i]), rope[p][n + i] = mag sin(p f[i])
+constexpr int kRopeMaxPairs = 128;
+struct RopeFreq {
+  double f[kRopeMaxPairs];
+};
+hipError_t launch_rope_table(const RopeFreq& f, int pairs, int rows, double mag, float* table,
+                             hipStream_t stream);
+struct KvAttnArgs {
+  KvCache c;
+  KvBatch s;
+  KvRows q, o;
+  float* lse;  // [T, q_heads] or null
+  float scale;
+  int bf16, q_heads, causal, window, sinks;
+  // Runs of rows with long contexts are cut into parts, for `extra` workgroups at
+  // most beyond one to each run and head (0: not cut); `slots` workgroups run at
+  // once. What the parts leave for the join: [max_parts, run, dim] and
+  // [max_parts, run, 2], and notes [T * q_heads, 2] of each row's parts.
+  int prompt;  // kv_prompt instead of kv_step; splits: parts of its tokens (1: not cut)
+  int splits;
+  int run, extra, slots, max_parts;
+  float* part_o;
+  float* part_ml;
+  int* notes;
+};
+constexpr int kKvNoteShift = 8;  // a note: part << shift | row of the part, number of parts
+int kv_attention_run(const KvBatch& s, int heads, int q_heads);  // rows of a run: 16 or 32
+int kv_attention_extra(const KvBatch& s, int heads, int q_heads, int dim, int64_t max_span, int num_cus,
+                       int* slots);
+bool kv_attention_prompt(const KvBatch& s, int heads, int q_heads);
+int kv_prompt_splits(const KvBatch& s, int heads, int q_heads, int dim, int page_shift, int64_t max_span,
+                     int num_cus, int* run, int* max_parts);
+hipError_t launch_kv_prompt(const KvAttnArgs& a, hipStream_t stream);
+hipError_t launch_kv_attention(const KvAttnArgs& a, hipStream_t stream);
+
+}  // namespace llmint8

@@ -74,23 +74,6 @@ inline int admit_linear_4bit(int64_t T, int64_t K, int64_t N) {
   return LLMINT8_OK;
 }
 
-// int8 key/value cache: the kernels index tokens, rows and work items in 32 bits
-// (an item's first token is below len + rows + 2 seqs page < 2^31)
-constexpr int64_t kKvMax = int64_t(1) << 29;
-constexpr int64_t kKvMaxQHeads = 65536;
-constexpr int64_t kKvMaxQRows = int64_t(1) << 30;  // rows times query heads of an attention call
-inline int admit_kv_cache(int64_t pages, int64_t heads, int64_t page, int64_t dim) {
-  if (pages <= 0 || heads <= 0 || page <= 0 || dim <= 0) return LLMINT8_ERR_INVALID_ARG;
-  if (page != 16 && page != 32 && page != 64 && page != 128) return LLMINT8_ERR_UNSUPPORTED;
-  if (dim % 16 != 0 || dim > 256 || heads > 4096 || pages >= kTwo31) return LLMINT8_ERR_UNSUPPORTED;
-  return LLMINT8_OK;
-}
-inline int admit_kv_batch(int64_t seqs, int64_t rows, int64_t width, int64_t page) {
-  if (seqs < 0 || rows < 0 || width <= 0) return LLMINT8_ERR_INVALID_ARG;
-  if (rows > kKvMax || width > kKvMax / page || seqs > kKvMax / (2 * page)) return LLMINT8_ERR_UNSUPPORTED;
-  return LLMINT8_OK;
-}
-
 // ---- windows (host and device): bytes of each resource a kernel builds
 
 // column scan: row groups and the window of one group's rows

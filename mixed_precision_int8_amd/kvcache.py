@@ -198,15 +198,15 @@ def llmint8_kv_append(cache, batch, k, v, q=None, rope=None, interleaved=False, 
         heads = q.shape[1] if q.dim() == 3 else -1
         qr = _rows(q, k.dtype, n, heads, cache.dim, dev, "q")
         if q_out is None:
-            q_out = torch.empty((n, heads, cache.dim), dtype=k.dtype, device=dev)
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
         orr = _rows(q_out, k.dtype, n, heads, cache.dim, dev, "q_out")
     elif q_out is not None:
         raise ValueError("q_out without q")
     table, table_rows, rot = None, 0, 0
     if rope is not None:
-        if rope.dim() != 2:
-            raise ValueError(f"rope: expected [positions, rot], got {tuple(rope.shape)}")
-        m8._need(rope, torch.float32, tuple(rope.shape), "rope")
+        if rope.dim() != 2 or rope.dtype != torch.float32 or not rope.is_contiguous() or rope.device != dev:
+            raise ValueError(f"rope: expected contiguous fp32 [positions, rot] on {dev}, got {rope.dtype} "
+                             f"{tuple(rope.shape)} on {rope.device}")
         table_rows, rot = rope.shape
         table = rope.data_ptr()
     m8._check(lib.llmint8_kv_append(cache._ref, batch._ref, code, *kr, *vr, *qr, *orr, heads, table,
@@ -227,7 +227,7 @@ def llmint8_kv_gather(cache, batch, dtype=None, k=None, v=None, stream=None):
     if k is None:
         k = torch.empty(shape, dtype=dtype, device=dev)
     if v is None:
-        v = torch.empty(shape, dtype=dtype, device=dev)
+        v = torch.empty_like(k, memory_format=torch.contiguous_format)
     m8._check(lib.llmint8_kv_gather(cache._ref, batch._ref, code, *_rows(k, dtype, *shape, dev, "k"),
                                     *_rows(v, dtype, *shape, dev, "v"), _stream(stream, dev)),
               "llmint8_kv_gather")
@@ -253,7 +253,7 @@ def llmint8_kv_attention(cache, batch, q, scale=None, causal=True, window=0, sin
     heads = q.shape[1] if q.dim() == 3 else -1
     qr = _rows(q, q.dtype, n, heads, cache.dim, dev, "q")
     if out is None:
-        out = torch.empty((n, heads, cache.dim), dtype=q.dtype, device=dev)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     orr = _rows(out, q.dtype, n, heads, cache.dim, dev, "out")
     if lse is not None:
         m8._need(lse, torch.float32, (n, heads), "lse")

@@ -1,5 +1,5 @@
 """The int8 key/value cache without a GPU: refusals of the C ABI, workspace sizes, the oracle against hand
-values, the device code's instructions, the host code under sanitizers."""
+values, the device code's instructions."""
 from __future__ import annotations
 
 import ctypes

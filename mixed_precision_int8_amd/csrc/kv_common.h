@@ -49,38 +49,35 @@ __device__ __forceinline__ KvSeq kv_seq_uniform(const KvBatch& s, int page_shift
   return q;
 }
 
-// The sequence that work item `item` belongs to, where sequence b owns the items
-// from (cu[b] * per >> shift) + b on. A sequence of n rows then has at least (n *
-// per >> shift) + 1 items: enough for the tiles of 2^shift that its n * per rows
-// fill, and one less at most than the pages of 2^shift that n tokens reach, with
-// no table of counts. Whole workgroup: the sequences are counted in parallel, one
-// round of loads for every kThreads of them, and the owner hands its numbers,
-// loaded in the same round, to the others (sh). Sets *index to the item's number
-// in the sequence and *count to the sequence's items; false where no sequence owns
-// the item (cu starts late, or falls).
+// The sequence that owns work item `item` (kv_items), found with no table of counts.
+// Whole workgroup: the sequences are counted in parallel, one round of loads for
+// every kThreads of them, and the owner hands its numbers, loaded in the same
+// round, to the others (sh). Sets *index to the item's number in the sequence and
+// *count to the sequence's items; false where no sequence owns the item (it is
+// past the last one's, or cu starts late or falls).
 template <int kThreads>
 __device__ __forceinline__ bool kv_find(const KvBatch& s, int page_shift, int item, int per, int shift,
                                         int (&sh)[5], KvSeq* out, int* index, int* count) {
   if (s.B == 1) {
     *out = kv_seq_uniform(s, page_shift, 0);
-    const int first = (int)(((int64_t)out->row0 * per) >> shift);
-    *index = item - first;
-    *count = (int)(((int64_t)(out->row0 + out->n) * per) >> shift) + 1 - first;
-    return first <= item;
+    const KvItems own = kv_items(0, out->row0, out->n, per, shift);
+    *index = kv_item_index(own, item);
+    *count = own.count;
+    return *index >= 0;
   }
   int b = -1;
   for (int b0 = 0; b0 < s.B; b0 += kThreads) {
     const int i = b0 + (int)threadIdx.x;
     const int lane = min(i, s.B - 1);
     const KvSeq q = kv_seq(s, page_shift, lane);
-    const int64_t at = (((int64_t)q.row0 * per) >> shift) + lane;
-    const int mine = __syncthreads_count(i < s.B && at <= item);
+    const KvItems own = kv_items(lane, q.row0, q.n, per, shift);
+    const int mine = __syncthreads_count(i < s.B && own.first <= item);
     if (mine > 0 && (int)threadIdx.x == mine - 1) {
       sh[0] = q.row0;
       sh[1] = q.n;
       sh[2] = q.len;
-      sh[3] = (int)at;
-      sh[4] = (int)((((int64_t)(q.row0 + q.n) * per) >> shift) + lane + 1 - at);
+      sh[3] = own.first;
+      sh[4] = own.count;
     }
     b += mine;
     if (mine < min(kThreads, s.B - b0)) break;
@@ -91,8 +88,9 @@ __device__ __forceinline__ bool kv_find(const KvBatch& s, int page_shift, int it
   out->row0 = uniform(sh[0]);
   out->n = uniform(sh[1]);
   out->len = uniform(sh[2]);
-  *index = item - uniform(sh[3]);
-  *count = uniform(sh[4]);
+  const KvItems own{uniform(sh[3]), uniform(sh[4])};
+  *index = kv_item_index(own, item);
+  *count = own.count;
   return *index >= 0;
 }
 

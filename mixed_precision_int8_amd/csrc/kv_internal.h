@@ -45,6 +45,32 @@ struct KvBatch {
   const int32_t* table;  // [B, width]
   int B, T, width;
 };
+// The work items of a launch: sequence b with rows [row0, row0 + n) owns `count` of
+// them from `first` on, enough for the tiles of 2^shift that its n * per rows fill,
+// and one less at most than the pages of 2^shift that n tokens reach. With rows
+// that follow each other the sequences' items do too; what a launch has beyond the
+// last sequence's (rows past cu[seqs]) belongs to none.
+struct KvItems {
+  int first, count;
+};
+__host__ __device__ inline KvItems kv_items(int b, int row0, int n, int per, int shift) {
+  KvItems i;
+  i.first = (int)(((int64_t)row0 * per) >> shift) + b;
+  i.count = (int)(((int64_t)(row0 + n) * per) >> shift) + b + 1 - i.first;
+  return i;
+}
+// An item's number in its sequence, -1 if it is not one of its own.
+__host__ __device__ inline int kv_item_index(const KvItems& i, int item) {
+  return item >= i.first && item - i.first < i.count ? item - i.first : -1;
+}
+// The pages of an item where per = 1 and a tile is a page: the sequence's last item
+// takes the page past the others' as well, if there is one.
+struct KvEntries {
+  int first, count;
+};
+__host__ __device__ inline KvEntries kv_item_entries(int pos0, int index, int count, int page_shift) {
+  return {((pos0 > 0 ? pos0 : 0) >> page_shift) + index, index + 1 == count ? 2 : 1};
+}
 // 16-bit rows [T, heads, dim]: strides in elements, channels dense
 struct KvRows {
   uint16_t* p;

@@ -403,12 +403,11 @@ __global__ __launch_bounds__(256, VEC ? 4 : 2) void kc_append(KvAppendArgs a, in
       }
     }
   };
-  // the sequence's last item takes the page past the others' as well, if there is one
-  const int entry = (max(pos0, 0) >> a.c.page_shift) + index;
-  write_page(entry);
-  if (index + 1 == count) {
+  const KvEntries own = kv_item_entries(pos0, index, count, a.c.page_shift);
+  write_page(own.first);
+  if (own.count > 1) {
     __syncthreads();
-    write_page(entry + 1);
+    write_page(own.first + 1);
   }
 }
 
@@ -492,9 +491,9 @@ __global__ __launch_bounds__(256) void kc_gather(KvCache c, KvBatch s, KvRows k,
       }
     }
   };
-  const int entry = (max(pos0, 0) >> c.page_shift) + index;
-  read_page(entry);
-  if (index + 1 == count) read_page(entry + 1);  // the last item takes the page past the others' as well
+  const KvEntries own = kv_item_entries(pos0, index, count, c.page_shift);
+  read_page(own.first);
+  if (own.count > 1) read_page(own.first + 1);
 }
 
 hipError_t launch_kv_gather(const KvCache& c, const KvBatch& s, const KvRows& k, const KvRows& v, bool bf16,

@@ -1,0 +1,76 @@
+// Host sweep of the index arithmetic that the key/value cache's kernels share with
+// it (mixed_precision_int8_amd/csrc/kv_internal.h). Built and run by
+// tests/test_kvcache_index.py; the argument names the check.
+#include <cstdio>
+#include <cstring>
+#include <random>
+#include <vector>
+
+#include "../mixed_precision_int8_amd/csrc/kv_internal.h"
+
+using namespace llmint8;
+
+static int failures = 0;
+#define EXPECT(c, ...)                          \
+  do {                                          \
+    if (!(c) && ++failures < 10) {              \
+      std::fprintf(stderr, "failed: %s: ", #c); \
+      std::fprintf(stderr, __VA_ARGS__);        \
+      std::fprintf(stderr, "\n");               \
+    }                                           \
+  } while (0)
+
+static std::mt19937 rng(7);
+static int draw(int lo, int hi) { return std::uniform_int_distribution<int>(lo, hi)(rng); }
+
+// Random batches of rising cu, some with rows past the last sequence's: every row
+// with a position is worked on by one item of the launch, no other row by any, both
+// as pages of tokens (append, gather) and as tiles of rows (attention).
+static void items() {
+  for (int round = 0; round < 4000; ++round) {
+    const int page_shift = draw(4, 7), B = draw(1, 9), per = draw(1, 9), shift = draw(4, 8);
+    std::vector<int> cu{0}, len;
+    for (int b = 0; b < B; ++b) {
+      const int kind = draw(0, 3), n = kind == 0 ? 0 : kind == 1 ? 1 : draw(1, kind == 2 ? 20 : 300);
+      cu.push_back(cu.back() + n);
+      len.push_back(draw(0, 9) == 0 ? draw(0, n) : n + draw(0, 300));  // now and then rows without a position
+    }
+    const int T = cu[B] + (draw(0, 1) ? 0 : draw(1, 300));
+    for (int tiles = 0; tiles < 2; ++tiles) {
+      const int p = tiles ? per : 1, s = tiles ? shift : page_shift;
+      std::vector<int> seen((size_t)T * p, 0);
+      const int launched = (int)(((int64_t)T * p) >> s) + B;
+      for (int item = 0; item < launched; ++item) {
+        int b = -1;  // the last sequence whose items begin no later, as kv_find counts it
+        while (b + 1 < B && kv_items(b + 1, cu[b + 1], cu[b + 2] - cu[b + 1], p, s).first <= item) ++b;
+        if (b < 0) continue;
+        const int n = cu[b + 1] - cu[b], pos0 = len[b] - n;
+        const KvItems own = kv_items(b, cu[b], n, p, s);
+        const int index = kv_item_index(own, item);
+        if (index < 0) continue;
+        if (tiles) {
+          for (int r = index << s; r < std::min((index + 1) << s, n * p); ++r) ++seen[(size_t)cu[b] * p + r];
+          continue;
+        }
+        const KvEntries e = kv_item_entries(pos0, index, own.count, s);
+        for (int i = e.first; i < e.first + e.count; ++i)
+          for (int at = std::max(pos0, i << s); at < std::min(len[b], (i + 1) << s); ++at) ++seen[cu[b] + at - pos0];
+      }
+      for (int b = 0; b <= B; ++b)
+        for (int r = cu[b]; r < (b < B ? cu[b + 1] : T); ++r)
+          for (int k = 0; k < p; ++k) {
+            const bool live = b < B && (tiles || len[b] - (cu[b + 1] - cu[b]) + r - cu[b] >= 0);
+            EXPECT(seen[(size_t)r * p + k] == (live ? 1 : 0), "%d times: row %d of %d (%d in the batch), page or tile 2^%d, per %d",
+                   seen[(size_t)r * p + k], r, T, cu[B], s, p);
+          }
+    }
+  }
+}
+
+int main(int, char** argv) {
+  const char* what = argv[1];
+  if (!std::strcmp(what, "items")) items();
+  else return 2;
+  if (!failures) std::printf("%s ok\n", what);
+  return failures ? 1 : 0;
+}

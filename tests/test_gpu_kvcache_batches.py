@@ -1,0 +1,59 @@
+"""Batches of the int8 key/value cache as a server forms them: calls with more rows than the sequences use,
+rows that are turned where they stand, mixed calls, other streams. Setup and bounds: test_gpu_kvcache."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+import oracle
+
+torch = pytest.importorskip("torch")
+import mixed_precision_int8_amd as m8  # noqa: E402
+from test_gpu_kvcache import TD, Setup, _say  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    m8.load_library()
+    yield
+    torch.cuda.synchronize()
+
+
+PADDED = [
+    # lens, counts, rows of the call, heads, q_heads, dim, page, rot, interleaved, dtype
+    ([100], [50], 128, 2, 4, 128, 64, 128, False, "f16"),             # tokens 50..99 reach two pages
+    ([77, 31, 500], [1, 1, 1], 64, 2, 8, 64, 16, 64, False, "bf16"),   # a step
+    ([77, 130, 500], [17, 17, 17], 300, 4, 4, 64, 16, 16, True, "f16"),  # drafts
+    ([300, 141, 90], [170, 0, 90], 512, 2, 6, 128, 32, 128, False, "bf16"),  # prompts
+    ([50, 40], [20, 3], 256, 2, 2, 48, 16, 22, True, "f16"),           # partners read one by one
+    ([70, 141], [30, 100], 131, 1, 2, 256, 128, 24, False, "bf16"),
+]
+
+
+@pytest.mark.parametrize("case", PADDED)
+def test_append_turns_q_once_where_it_stands_in_a_call_with_unused_rows(case):
+    lens, counts, rows, heads, q_heads, dim, page, rot, inter, dtype = case
+    _say(f"padded append {case}")
+    s = Setup(81, lens, counts, heads, dim, page)
+    used, s.rows = s.rows, rows
+    rope_np = oracle.rope_table(m8.rope_frequencies(rot)[0], max(lens) + 1)
+    rope = torch.from_numpy(rope_np).cuda()
+    k, kx = s.values(heads, dtype)
+    v, vx = s.values(heads, dtype)
+    q, qx = s.values(q_heads, dtype, wide=True)
+    want = torch.from_numpy(s.ref.append(s.cu, s.lens, s.table, kx, vx, qx, rope_np, inter)).to(TD[dtype])
+    want[used:] = q[used:].cpu()
+    m8.llmint8_kv_append(s.cache, s.batch(), k, v, q=q, rope=rope, interleaved=inter, q_out=q)
+    s.same_cache()
+    assert torch.equal(q.cpu(), want)
+    gk, gv = m8.llmint8_kv_gather(s.cache, s.batch(), TD[dtype], k=torch.full_like(k, 5.0), v=torch.full_like(v, 5.0))
+    for b, n in enumerate(lens):
+        kx, vx, _ = s.ref.tokens(s.table, b, n - counts[b], n)
+        at = slice(s.cu[b], s.cu[b + 1])
+        assert torch.equal(gk[at].cpu(), torch.from_numpy(kx).to(TD[dtype])), b
+        assert torch.equal(gv[at].cpu(), torch.from_numpy(vx).to(TD[dtype])), b
+    assert (gk[used:] == 5).all() and (gv[used:] == 5).all()

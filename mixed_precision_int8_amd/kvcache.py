@@ -352,12 +352,17 @@ class Int8SelfAttention:
         self.rope, self.interleaved, self.window, self.sinks = rope, interleaved, window, sinks
 
     def forward(self, X, batch):
-        """Y [rows, hidden] for the batch's new tokens X [rows, hidden], which join the cache."""
+        """Y [rows, hidden] for the batch's new tokens X [rows, hidden], which join the cache. Rows of X past
+        the batch's attend to nothing: their attention is zero."""
+        import torch
         c, nq = self.cache, self.q_heads
         qkv = self.qkv(X).view(X.shape[0], nq + 2 * c.heads, c.dim)
         q = llmint8_kv_append(c, batch, qkv[:, nq:nq + c.heads], qkv[:, nq + c.heads:], qkv[:, :nq],
                               self.rope, self.interleaved, q_out=qkv[:, :nq])
-        o = llmint8_kv_attention(c, batch, q, window=self.window, sinks=self.sinks)
+        # the attention writes the batch's rows only, and the second projection decides its outlier columns over
+        # all rows: what memory held in the others must not reach it
+        o = torch.zeros((X.shape[0], nq, c.dim), dtype=qkv.dtype, device=qkv.device)
+        llmint8_kv_attention(c, batch, q, window=self.window, sinks=self.sinks, out=o)
         return self.out(o.view(X.shape[0], nq * c.dim))
 
     __call__ = forward

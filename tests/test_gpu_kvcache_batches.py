@@ -57,3 +57,26 @@ def test_append_turns_q_once_where_it_stands_in_a_call_with_unused_rows(case):
         assert torch.equal(gk[at].cpu(), torch.from_numpy(kx).to(TD[dtype])), b
         assert torch.equal(gv[at].cpu(), torch.from_numpy(vx).to(TD[dtype])), b
     assert (gk[used:] == 5).all() and (gv[used:] == 5).all()
+
+
+@pytest.mark.parametrize("rows", [5, 40, 300])
+def test_layer_gives_the_batch_s_rows_the_same_whatever_memory_holds(rows):
+    """Unused rows of a call to Int8SelfAttention: the output projection decides its outlier columns over all
+    rows, so those of the attention must not be what memory held before."""
+    g = torch.Generator(device="cuda").manual_seed(7)
+    hidden, q_heads, heads, dim, used = 256, 8, 2, 32, 3
+    W = (torch.randn(((q_heads + 2 * heads) * dim, hidden), device="cuda", generator=g) / 16).half()
+    Wo = (torch.randn((hidden, q_heads * dim), device="cuda", generator=g) / 16).half()
+    X = torch.zeros((rows, hidden), device="cuda").half()
+    X[:used] = torch.randn((used, hidden), device="cuda", generator=g).half()
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    out = []
+    for poison in (0.0, 100.0, -3.0):
+        cache = m8.KVCache.empty(4, heads, dim, 16)
+        layer = m8.Int8SelfAttention(W, Wo, q_heads, cache)
+        held = [torch.full((rows, q_heads, dim), poison, device="cuda").half() for _ in range(40)]
+        del held
+        out.append(layer(X, m8.KVBatch(ints([0, 1, used]), ints([1, 2]), ints([[2], [0]]), rows)))
+    for y in out:
+        same = bool((y == out[0]).all())
+        assert same and bool((y[used:] == 0).all()) and bool((y[:used] != 0).any())

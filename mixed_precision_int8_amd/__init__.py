@@ -195,6 +195,24 @@ def _stream(stream, device):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _empty(shape, dtype, device, stream, fill=None):
+    """torch.empty (torch.full with ``fill``) for a call on ``stream`` (None: the current one). On another
+    stream than the current one the memory is of that stream's pool, so that no block that the current
+    stream may still be using is written there, and none that the call still uses goes back to the current
+    stream when the tensor is dropped; a result may be read on the current stream and dropped there."""
+    import torch
+    if stream is not None:
+        current = torch.cuda.current_stream(device)
+        if current.cuda_stream != stream.cuda_stream:
+            with torch.cuda.stream(stream):
+                t = _empty(shape, dtype, device, None, fill)
+            t.record_stream(current)
+            return t
+    if fill is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return torch.full(shape, fill, dtype=dtype, device=device)
+
+
 def _need(t, dtype, shape, name):
     import torch
     if not isinstance(t, torch.Tensor):
@@ -235,9 +253,9 @@ def llmint8_quantize_weight(W, Wq=None, sW=None, stream=None):
     N, K = W.shape
     _need(W, torch.float16, (N, K), "W")
     if Wq is None:
-        Wq = torch.empty((N, K), dtype=torch.int8, device=W.device)
+        Wq = _empty((N, K), torch.int8, W.device, stream)
     if sW is None:
-        sW = torch.empty((N,), dtype=torch.float32, device=W.device)
+        sW = _empty((N,), torch.float32, W.device, stream)
     _need(Wq, torch.int8, (N, K), "Wq")
     _need(sW, torch.float32, (N,), "sW")
     _check(lib.llmint8_quantize_weight(_ptr(W), N, K, _ptr(Wq), _ptr(sW), _stream(stream, W.device)),
@@ -262,9 +280,9 @@ def llmint8_quantize_weight_ex(W, Wq=None, sW=None, stream=None):
     code = _act_dtype(W.dtype)
     _need(W, W.dtype, (N, K), "W")
     if Wq is None:
-        Wq = torch.empty((N, K), dtype=torch.int8, device=W.device)
+        Wq = _empty((N, K), torch.int8, W.device, stream)
     if sW is None:
-        sW = torch.empty((N,), dtype=torch.float32, device=W.device)
+        sW = _empty((N,), torch.float32, W.device, stream)
     _need(Wq, torch.int8, (N, K), "Wq")
     _need(sW, torch.float32, (N,), "sW")
     _check(lib.llmint8_quantize_weight_ex(_ptr(W), code, N, K, _ptr(Wq), _ptr(sW),
@@ -273,14 +291,14 @@ def llmint8_quantize_weight_ex(W, Wq=None, sW=None, stream=None):
     return Wq, sW
 
 
-def _workspace(T, K, N, device, workspace, path=LLMINT8_PATH_AUTO):
+def _workspace(T, K, N, device, workspace, path=LLMINT8_PATH_AUTO, stream=None):
     """The caller's workspace, or a new one of the size the route needs (None when the
     route needs none: the fused decode kernel keeps everything in LDS)."""
     import torch
     if workspace is None:
         need = llmint8_workspace_bytes_path(T, K, N, path)
         if need > 0:
-            workspace = torch.empty((need,), dtype=torch.uint8, device=device)
+            workspace = _empty((need,), torch.uint8, device, stream)
     return workspace
 
 
@@ -288,7 +306,8 @@ def _ws_bytes(ws):
     return 0 if ws is None else ws.numel() * ws.element_size()
 
 
-def _linear_args(X, Wq, sW, threshold, Y, workspace, dtype=None, bias=None, path=LLMINT8_PATH_AUTO):
+def _linear_args(X, Wq, sW, threshold, Y, workspace, dtype=None, bias=None, path=LLMINT8_PATH_AUTO,
+                 stream=None):
     import torch
     T, K = X.shape
     N = Wq.shape[0]
@@ -299,9 +318,9 @@ def _linear_args(X, Wq, sW, threshold, Y, workspace, dtype=None, bias=None, path
     if bias is not None:
         _need(bias, dtype, (N,), "bias")
     if Y is None:
-        Y = torch.empty((T, N), dtype=dtype, device=X.device)
+        Y = _empty((T, N), dtype, X.device, stream)
     _need(Y, dtype, (T, N), "Y")
-    workspace = _workspace(T, K, N, X.device, workspace, path)
+    workspace = _workspace(T, K, N, X.device, workspace, path, stream)
     thr = float(threshold)
     if thr == math.inf:
         thr = math.inf
@@ -311,7 +330,7 @@ def _linear_args(X, Wq, sW, threshold, Y, workspace, dtype=None, bias=None, path
 def llmint8_linear(X, Wq, sW, threshold: float = 6.0, Y=None, workspace=None, stream=None):
     """Y fp16 [T, N] = LLM.int8() forward of X fp16 [T, K] with (Wq, sW)."""
     lib = load_library()
-    T, K, N, Y, ws, thr = _linear_args(X, Wq, sW, threshold, Y, workspace)
+    T, K, N, Y, ws, thr = _linear_args(X, Wq, sW, threshold, Y, workspace, stream=stream)
     _check(lib.llmint8_linear(_ptr(X), T, K, _ptr(Wq), _ptr(sW), N, thr, _ptr(Y), _ptr(ws),
                               _ws_bytes(ws), _stream(stream, X.device)),
            "llmint8_linear")
@@ -324,7 +343,7 @@ def llmint8_linear_ex(X, Wq, sW, threshold: float = 6.0, bias=None, Y=None, work
     bias [N] take the type of X) with (Wq, sW)."""
     lib = load_library()
     code = _act_dtype(X.dtype)
-    T, K, N, Y, ws, thr = _linear_args(X, Wq, sW, threshold, Y, workspace, X.dtype, bias)
+    T, K, N, Y, ws, thr = _linear_args(X, Wq, sW, threshold, Y, workspace, X.dtype, bias, stream=stream)
     _check(lib.llmint8_linear_ex(_ptr(X), code, T, K, _ptr(Wq), _ptr(sW), N, thr, _ptr(bias),
                                  _ptr(Y), _ptr(ws), _ws_bytes(ws),
                                  _stream(stream, X.device)),
@@ -347,7 +366,7 @@ def llmint8_linear_noalloc(X, Wq, sW, threshold: float = 6.0, bias=None, Y=None,
     if bias is not None:
         _need(bias, X.dtype, (N,), "bias")
     if Y is None:
-        Y = torch.empty((T, N), dtype=X.dtype, device=X.device)
+        Y = _empty((T, N), X.dtype, X.device, stream)
     _need(Y, X.dtype, (T, N), "Y")
     _check(lib.llmint8_linear_noalloc(_ptr(X), code, T, K, _ptr(Wq), _ptr(sW), N, float(threshold),
                                       _ptr(bias), _ptr(Y), _stream(stream, X.device)),
@@ -367,7 +386,7 @@ def llmint8_linear_timed_ex(X, Wq, sW, threshold, Y, workspace, events, bias=Non
     """
     lib = load_library()
     code = _act_dtype(X.dtype)
-    T, K, N, Y, ws, thr = _linear_args(X, Wq, sW, threshold, Y, workspace, X.dtype, bias, path)
+    T, K, N, Y, ws, thr = _linear_args(X, Wq, sW, threshold, Y, workspace, X.dtype, bias, path, stream=stream)
     handles = (_vp * len(events))(*[ctypes.c_void_p(e.cuda_event) for e in events])
     nk = ctypes.c_int(0)
     _check(lib.llmint8_linear_timed_ex(_ptr(X), code, T, K, _ptr(Wq), _ptr(sW), N, thr, _ptr(bias),
@@ -378,16 +397,16 @@ def llmint8_linear_timed_ex(X, Wq, sW, threshold, Y, workspace, events, bias=Non
     return nk.value
 
 
-def _debug_outputs(T, K, N, dev, want_C):
+def _debug_outputs(T, K, N, dev, want_C, stream=None):
     import torch
     KW = (K + 31) // 32
     return {
-        "bitmap": torch.zeros((KW,), dtype=torch.int32, device=dev),
-        "idx": torch.full((K,), -1, dtype=torch.int32, device=dev),
-        "count": torch.full((1,), -1, dtype=torch.int32, device=dev),
-        "Xq": torch.zeros((T, K), dtype=torch.int8, device=dev),
-        "aX": torch.zeros((T,), dtype=torch.float32, device=dev),
-        "C": torch.zeros((T, N), dtype=torch.int32, device=dev) if want_C else None,
+        "bitmap": _empty((KW,), torch.int32, dev, stream, 0),
+        "idx": _empty((K,), torch.int32, dev, stream, -1),
+        "count": _empty((1,), torch.int32, dev, stream, -1),
+        "Xq": _empty((T, K), torch.int8, dev, stream, 0),
+        "aX": _empty((T,), torch.float32, dev, stream, 0),
+        "C": _empty((T, N), torch.int32, dev, stream, 0) if want_C else None,
     }
 
 
@@ -397,9 +416,9 @@ def llmint8_linear_debug_ex(X, Wq, sW, threshold: float = 6.0, bias=None,
     """llmint8_linear_ex plus the intermediates of the same kernels: dict of tensors."""
     lib = load_library()
     code = _act_dtype(X.dtype)
-    T, K, N, Y, ws, thr = _linear_args(X, Wq, sW, threshold, Y, workspace, X.dtype, bias, path)
+    T, K, N, Y, ws, thr = _linear_args(X, Wq, sW, threshold, Y, workspace, X.dtype, bias, path, stream=stream)
     dev = X.device
-    out = _debug_outputs(T, K, N, dev, want_C)
+    out = _debug_outputs(T, K, N, dev, want_C, stream)
     _check(lib.llmint8_linear_debug_ex(_ptr(X), code, T, K, _ptr(Wq), _ptr(sW), N, thr, _ptr(bias),
                                        _ptr(Y), _ptr(ws), _ws_bytes(ws),
                                        _stream(stream, dev), int(path), _ptr(out["bitmap"]),
@@ -414,9 +433,9 @@ def llmint8_linear_debug(X, Wq, sW, threshold: float = 6.0, path: int = LLMINT8_
                          Y=None, workspace=None, stream=None, want_C: bool = True):
     """Forward plus the intermediates of the same kernels: dict of tensors."""
     lib = load_library()
-    T, K, N, Y, ws, thr = _linear_args(X, Wq, sW, threshold, Y, workspace, path=path)
+    T, K, N, Y, ws, thr = _linear_args(X, Wq, sW, threshold, Y, workspace, path=path, stream=stream)
     dev = X.device
-    out = _debug_outputs(T, K, N, dev, want_C)
+    out = _debug_outputs(T, K, N, dev, want_C, stream)
     _check(lib.llmint8_linear_debug(_ptr(X), T, K, _ptr(Wq), _ptr(sW), N, thr, _ptr(Y), _ptr(ws),
                                     _ws_bytes(ws), _stream(stream, dev), int(path),
                                     _ptr(out["bitmap"]), _ptr(out["idx"]), _ptr(out["count"]),
@@ -433,7 +452,7 @@ def llmint8_linear_timed(X, Wq, sW, threshold, Y, workspace, events, path=LLMINT
     Returns the number of kernels launched.
     """
     lib = load_library()
-    T, K, N, Y, ws, thr = _linear_args(X, Wq, sW, threshold, Y, workspace, path=path)
+    T, K, N, Y, ws, thr = _linear_args(X, Wq, sW, threshold, Y, workspace, path=path, stream=stream)
     handles = (_vp * len(events))(*[ctypes.c_void_p(e.cuda_event) for e in events])
     nk = ctypes.c_int(0)
     _check(lib.llmint8_linear_timed(_ptr(X), T, K, _ptr(Wq), _ptr(sW), N, thr, _ptr(Y), _ptr(ws),
@@ -455,7 +474,7 @@ def llmint8_dequantize_weight_t(Wq, sW, WdT=None, stream=None):
     _need(Wq, torch.int8, (N, K), "Wq")
     _need(sW, torch.float32, (N,), "sW")
     if WdT is None:
-        WdT = torch.empty((K, N), dtype=torch.float16, device=Wq.device)
+        WdT = _empty((K, N), torch.float16, Wq.device, stream)
     _need(WdT, torch.float16, (K, N), "WdT")
     _check(lib.llmint8_dequantize_weight_t(_ptr(Wq), _ptr(sW), N, K, _ptr(WdT),
                                            _stream(stream, Wq.device)),
@@ -463,7 +482,7 @@ def llmint8_dequantize_weight_t(Wq, sW, WdT=None, stream=None):
     return WdT
 
 
-def _backward_args(dY, Wq, sW, dX, workspace, dtype=None):
+def _backward_args(dY, Wq, sW, dX, workspace, dtype=None, stream=None):
     import torch
     T, N = dY.shape
     K = Wq.shape[1]
@@ -472,19 +491,19 @@ def _backward_args(dY, Wq, sW, dX, workspace, dtype=None):
     _need(Wq, torch.int8, (N, K), "Wq")
     _need(sW, torch.float32, (N,), "sW")
     if dX is None:
-        dX = torch.empty((T, K), dtype=dtype, device=dY.device)
+        dX = _empty((T, K), dtype, dY.device, stream)
     _need(dX, dtype, (T, K), "dX")
     if workspace is None:
         need = llmint8_backward_workspace_bytes(T, K, N)   # 0: the weight is dequantized on the fly
         if need > 0:
-            workspace = torch.empty((need,), dtype=torch.uint8, device=dY.device)
+            workspace = _empty((need,), torch.uint8, dY.device, stream)
     return T, K, N, dX, workspace
 
 
 def llmint8_linear_backward_input(dY, Wq, sW, dX=None, workspace=None, stream=None):
     """dX fp16 [T, K] = dY fp16 [T, N] . Wdeq, the input gradient of the frozen layer."""
     lib = load_library()
-    T, K, N, dX, ws = _backward_args(dY, Wq, sW, dX, workspace)
+    T, K, N, dX, ws = _backward_args(dY, Wq, sW, dX, workspace, stream=stream)
     _check(lib.llmint8_linear_backward_input(_ptr(dY), T, K, _ptr(Wq), _ptr(sW), N, _ptr(dX),
                                              _ptr(ws), _ws_bytes(ws),
                                              _stream(stream, dY.device)),
@@ -496,7 +515,7 @@ def llmint8_linear_backward_input_ex(dY, Wq, sW, dX=None, workspace=None, stream
     """dX [T, K] = dY [T, N] . Wdeq in the type of dY (fp16 or bf16)."""
     lib = load_library()
     code = _act_dtype(dY.dtype)
-    T, K, N, dX, ws = _backward_args(dY, Wq, sW, dX, workspace, dY.dtype)
+    T, K, N, dX, ws = _backward_args(dY, Wq, sW, dX, workspace, dY.dtype, stream)
     _check(lib.llmint8_linear_backward_input_ex(_ptr(dY), code, T, K, _ptr(Wq), _ptr(sW), N,
                                                 _ptr(dX), _ptr(ws), _ws_bytes(ws),
                                                 _stream(stream, dY.device)),
@@ -513,7 +532,7 @@ def llmint8_dequantize_weight_t_ex(Wq, sW, dtype=None, WdT=None, stream=None):
     _need(Wq, torch.int8, (N, K), "Wq")
     _need(sW, torch.float32, (N,), "sW")
     if WdT is None:
-        WdT = torch.empty((K, N), dtype=dtype, device=Wq.device)
+        WdT = _empty((K, N), dtype, Wq.device, stream)
     _need(WdT, dtype, (K, N), "WdT")
     _check(lib.llmint8_dequantize_weight_t_ex(_ptr(Wq), _ptr(sW), N, K, _ptr(WdT), _act_dtype(dtype),
                                               _stream(stream, Wq.device)),
@@ -524,7 +543,7 @@ def llmint8_dequantize_weight_t_ex(Wq, sW, dtype=None, WdT=None, stream=None):
 def llmint8_linear_backward_input_timed(dY, Wq, sW, events, dX=None, workspace=None, stream=None):
     """Input gradient recording ``events`` (3 created torch.cuda.Event) around its two kernels."""
     lib = load_library()
-    T, K, N, dX, ws = _backward_args(dY, Wq, sW, dX, workspace)
+    T, K, N, dX, ws = _backward_args(dY, Wq, sW, dX, workspace, stream=stream)
     handles = (_vp * len(events))(*[ctypes.c_void_p(e.cuda_event) for e in events])
     nk = ctypes.c_int(0)
     _check(lib.llmint8_linear_backward_input_timed(_ptr(dY), T, K, _ptr(Wq), _ptr(sW), N, _ptr(dX),
@@ -554,9 +573,9 @@ def llmint8_quantize_blockwise(x, block: int = 4096, q=None, absmax=None, stream
     n = x.numel()
     nb = -(-n // block)
     if q is None:
-        q = torch.empty((n,), dtype=torch.int8, device=x.device)
+        q = _empty((n,), torch.int8, x.device, stream)
     if absmax is None:
-        absmax = torch.empty((nb,), dtype=torch.float32, device=x.device)
+        absmax = _empty((nb,), torch.float32, x.device, stream)
     _need(q, torch.int8, (n,), "q")
     _need(absmax, torch.float32, (nb,), "absmax")
     _check(lib.llmint8_quantize_blockwise(_ptr(x), _codec_dtype(x.dtype), n, block, _ptr(q),
@@ -574,7 +593,7 @@ def llmint8_dequantize_blockwise(q, absmax, block: int = 4096, dtype=None, out=N
     _need(q, torch.int8, (n,), "q")
     _need(absmax, torch.float32, (nb,), "absmax")
     if out is None:
-        out = torch.empty((n,), dtype=dtype or torch.float16, device=q.device)
+        out = _empty((n,), dtype or torch.float16, q.device, stream)
     if not (out.is_cuda and out.is_contiguous() and out.numel() == n):
         raise ValueError("out: expected a contiguous CUDA tensor of n elements")
     _check(lib.llmint8_dequantize_blockwise(_ptr(q), _ptr(absmax), n, block, _ptr(out),
@@ -611,9 +630,9 @@ def llmint8_quantize_4bit(W, block: int = 64, quant_type="nf4", packed=None, abs
     n = W.numel()
     nb = -(-n // block)
     if packed is None:
-        packed = torch.empty((n // 2,), dtype=torch.uint8, device=W.device)
+        packed = _empty((n // 2,), torch.uint8, W.device, stream)
     if absmax is None:
-        absmax = torch.empty((nb,), dtype=torch.float32, device=W.device)
+        absmax = _empty((nb,), torch.float32, W.device, stream)
     _need(packed, torch.uint8, (n // 2,), "packed")
     _need(absmax, torch.float32, (nb,), "absmax")
     _check(lib.llmint8_quantize_4bit(_ptr(W), _act_dtype(W.dtype), n, block, _quant_type(quant_type),
@@ -632,7 +651,7 @@ def llmint8_dequantize_4bit(packed, absmax, block: int = 64, quant_type="nf4", d
     _need(packed, torch.uint8, (n // 2,), "packed")
     _need(absmax, torch.float32, (nb,), "absmax")
     if out is None:
-        out = torch.empty((n,), dtype=dtype or torch.float16, device=packed.device)
+        out = _empty((n,), dtype or torch.float16, packed.device, stream)
     if not (out.is_cuda and out.is_contiguous() and out.numel() == n):
         raise ValueError("out: expected a contiguous CUDA tensor of n elements")
     _check(lib.llmint8_dequantize_4bit(_ptr(packed), _ptr(absmax), n, block, _quant_type(quant_type),
@@ -654,7 +673,7 @@ def llmint8_linear_4bit(X, packed, absmax, N: int, block: int = 64, quant_type="
     if bias is not None:
         _need(bias, X.dtype, (N,), "bias")
     if Y is None:
-        Y = torch.empty((T, N), dtype=X.dtype, device=X.device)
+        Y = _empty((T, N), X.dtype, X.device, stream)
     _need(Y, X.dtype, (T, N), "Y")
     _check(lib.llmint8_linear_4bit(_ptr(X), _act_dtype(X.dtype), T, K, _ptr(packed), _ptr(absmax),
                                    block, _quant_type(quant_type), N, _ptr(bias), _ptr(Y),

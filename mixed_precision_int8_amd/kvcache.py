@@ -166,7 +166,7 @@ def llmint8_rope_table(freq, rows, magnitude=1.0, table=None, device="cuda", str
     lib = m8.load_library()
     n = len(freq)
     if table is None:
-        table = torch.empty((rows, 2 * n), dtype=torch.float32, device=device)
+        table = m8._empty((rows, 2 * n), torch.float32, device, stream)
     m8._need(table, torch.float32, (rows, 2 * n), "table")
     arr = (ctypes.c_double * max(n, 1))(*[float(x) for x in freq])
     m8._check(lib.llmint8_rope_table(arr, n, rows, float(magnitude), table.data_ptr(),
@@ -198,7 +198,7 @@ def llmint8_kv_append(cache, batch, k, v, q=None, rope=None, interleaved=False, 
         heads = q.shape[1] if q.dim() == 3 else -1
         qr = _rows(q, k.dtype, n, heads, cache.dim, dev, "q")
         if q_out is None:
-            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            q_out = m8._empty(q.shape, q.dtype, dev, stream)
         orr = _rows(q_out, k.dtype, n, heads, cache.dim, dev, "q_out")
     elif q_out is not None:
         raise ValueError("q_out without q")
@@ -225,9 +225,9 @@ def llmint8_kv_gather(cache, batch, dtype=None, k=None, v=None, stream=None):
     code = m8._act_dtype(dtype)
     shape, dev = (batch.rows, cache.heads, cache.dim), cache.device
     if k is None:
-        k = torch.empty(shape, dtype=dtype, device=dev)
+        k = m8._empty(shape, dtype, dev, stream)
     if v is None:
-        v = torch.empty_like(k, memory_format=torch.contiguous_format)
+        v = m8._empty(shape, dtype, dev, stream)
     m8._check(lib.llmint8_kv_gather(cache._ref, batch._ref, code, *_rows(k, dtype, *shape, dev, "k"),
                                     *_rows(v, dtype, *shape, dev, "v"), _stream(stream, dev)),
               "llmint8_kv_gather")
@@ -253,14 +253,14 @@ def llmint8_kv_attention(cache, batch, q, scale=None, causal=True, window=0, sin
     heads = q.shape[1] if q.dim() == 3 else -1
     qr = _rows(q, q.dtype, n, heads, cache.dim, dev, "q")
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = m8._empty(q.shape, q.dtype, dev, stream)
     orr = _rows(out, q.dtype, n, heads, cache.dim, dev, "out")
     if lse is not None:
         m8._need(lse, torch.float32, (n, heads), "lse")
     if workspace is None:
         need = lib.llmint8_kv_attention_workspace_bytes(cache._ref, batch._ref, heads, window, sinks)
         if need > 0:
-            workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+            workspace = m8._empty((need,), torch.uint8, dev, stream)
     m8._check(lib.llmint8_kv_attention(cache._ref, batch._ref, code, *qr, heads,
                                        1.0 / math.sqrt(cache.dim) if scale is None else float(scale),
                                        1 if causal else 0, window, sinks, *orr,

@@ -80,3 +80,31 @@ def test_layer_gives_the_batch_s_rows_the_same_whatever_memory_holds(rows):
     for y in out:
         same = bool((y == out[0]).all())
         assert same and bool((y[used:] == 0).all()) and bool((y[:used] != 0).any())
+
+
+def test_calls_on_another_stream_while_the_current_one_takes_memory():
+    """No workspace and no outputs given: what the calls take is not the current stream's to reuse."""
+    s = Setup(83, [9000, 700], [1, 3], 2, 128, 64)
+    q, _ = s.values(8, "f16")
+    k, _ = s.values(2, "f16")
+    b = s.batch(9000)
+    size = m8.llmint8_kv_attention_workspace_bytes(s.cache, b, 8)
+    assert size > 0
+    m8.llmint8_kv_append(s.cache, b, k, k)
+    want = m8.llmint8_kv_attention(s.cache, b, q)
+    W = torch.randn((256, 128), device="cuda").half()
+    Wq, sW = m8.llmint8_quantize_weight(W)
+    X = torch.randn((300, 128), device="cuda").half()
+    Y = m8.llmint8_linear(X, Wq, sW)
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)  # the calls below wait for this; what is taken here runs before them
+        got = m8.llmint8_kv_attention(s.cache, b, q, stream=side)
+        y = m8.llmint8_linear(X, Wq, sW, stream=side)
+        other = [torch.full((n,), 77, dtype=torch.uint8, device="cuda")
+                 for n in (size, size, size // 2, y.numel() * 2, got.numel() * 2, 1 << 20)]
+        side.synchronize()
+        assert torch.equal(got, want) and torch.equal(y, Y)
+        assert all(bool((t == 77).all()) for t in other)

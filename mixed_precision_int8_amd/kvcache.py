@@ -113,7 +113,12 @@ class KVBatch:
 
 
 def _rows(t, dtype, rows, heads, dim, device, name):
-    """(pointer, token stride, head stride) of 16-bit rows [rows, heads, dim] with dense channels."""
+    """(pointer, token stride, head stride) of 16-bit rows [rows, heads, dim] with dense channels. The calls
+    have no backward: a tensor that takes part in a graph would leave it without a word, so it is refused."""
+    import torch
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name}: requires a gradient, and the key/value cache has none to give (detach it, or "
+                         "call under torch.no_grad())")
     if t.dtype != dtype or t.shape != (rows, heads, dim) or t.device != device:
         raise ValueError(f"{name}: expected {dtype} {(rows, heads, dim)} on {device}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
@@ -338,7 +343,8 @@ class Int8SelfAttention:
     """Self-attention of a decoder layer on int8 weights and an int8 cache: q, k, v from one Int8Linear,
     rotated and written by ``llmint8_kv_append``, attended by ``llmint8_kv_attention``, and projected by a
     second Int8Linear. ``qkv_weight`` is [(q_heads + 2 heads) * dim, hidden], ``out_weight`` [hidden,
-    q_heads * dim]."""
+    q_heads * dim]. For serving: there is no backward through the cache, and X that requires a gradient is
+    refused (but under ``torch.no_grad()``)."""
 
     def __init__(self, qkv_weight, out_weight, q_heads, cache, rope=None, interleaved=False, window=0,
                  sinks=0, threshold=6.0):

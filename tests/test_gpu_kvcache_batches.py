@@ -108,3 +108,19 @@ def test_calls_on_another_stream_while_the_current_one_takes_memory():
         side.synchronize()
         assert torch.equal(got, want) and torch.equal(y, Y)
         assert all(bool((t == 77).all()) for t in other)
+
+
+def test_layer_refuses_input_that_requires_a_gradient():
+    hidden, q_heads, heads, dim = 64, 2, 1, 32
+    g = torch.Generator(device="cuda").manual_seed(9)
+    W, Wo, X = (torch.randn(n, device="cuda", generator=g).half() for n in
+                (((q_heads + 2 * heads) * dim, hidden), (hidden, q_heads * dim), (5, hidden)))
+    cache = m8.KVCache.empty(2, heads, dim, 16)
+    layer = m8.Int8SelfAttention(W, Wo, q_heads, cache)
+    seqs = m8.PagedSequences(cache)
+    batch = seqs.extend([seqs.add()], [5])
+    want = layer(X, batch)
+    with pytest.raises(ValueError, match="gradient"):
+        layer(X.requires_grad_(), batch)
+    with torch.no_grad():
+        assert torch.equal(layer(X, batch), want)

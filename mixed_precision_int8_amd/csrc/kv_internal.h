@@ -111,7 +111,18 @@ struct KvAttnArgs {
   float* part_ml;
   int* notes;
 };
-constexpr int kKvNoteShift = 8;  // a note: part << shift | row of the part, number of parts
+// A row's note for the join: slot of its first part << shift | its place in a run,
+// and how many parts there are; no parts if the two name none of the workspace (a
+// row that no run of this call holds has whatever the workspace held).
+constexpr int kKvNoteShift = 8;
+struct KvNote {
+  int slot, place, parts;
+};
+__host__ __device__ inline KvNote kv_note(int where, int parts, int run, int max_parts) {
+  const KvNote n{where >> kKvNoteShift, where & ((1 << kKvNoteShift) - 1), parts};
+  const bool there = where >= 0 && n.place < run && n.slot < max_parts && parts >= 1 && parts <= max_parts - n.slot;
+  return there ? n : KvNote{0, 0, 0};
+}
 int kv_attention_run(const KvBatch& s, int heads, int q_heads);  // rows of a run: 16 or 32
 int kv_attention_extra(const KvBatch& s, int heads, int q_heads, int dim, int64_t max_span, int num_cus,
                        int* slots);

@@ -658,8 +658,8 @@ __global__ __launch_bounds__(256) void kv_join(KvAttnArgs a) {
   // read beside cu, not after it
   v2i note = *reinterpret_cast<const v2i*>(a.notes + min(row, (int64_t)a.s.T * a.q_heads - 1) * 2);
   if (!in) note = v2i{-1, 0};
-  const int slot = note[0] >> kKvNoteShift, nn = note[0] & ((1 << kKvNoteShift) - 1);
-  const int parts = note[0] < 0 || note[1] < 0 || note[1] > a.max_parts - slot ? 0 : note[1];
+  const KvNote of = kv_note(note[0], note[1], a.run, a.max_parts);
+  const int slot = of.slot, nn = of.place, parts = of.parts;
   if (ROWS == 1 && parts == 0) return;
   const int64_t qrow = t;
   const int qh = (int)(row - (int64_t)t * a.q_heads);

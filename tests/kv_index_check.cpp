@@ -67,9 +67,30 @@ static void items() {
   }
 }
 
+// Any two numbers that a row's note may hold: what is read of the workspace for it
+// is within the parts' rows.
+static void notes() {
+  const int runs[] = {16, 32, 128, 256}, sizes[] = {1, 2, 3, 64, 1536, 1 << 22};
+  for (int run : runs)
+    for (int max_parts : sizes)
+      for (int round = 0; round < 200000; ++round) {
+        const int kind = draw(0, 2);
+        const int where = kind == 0 ? (int)rng() : kind == 1 ? draw(-3, 600) : (max_parts + draw(-2, 2)) << kKvNoteShift | draw(0, 255);
+        const int parts = draw(0, 1) ? (int)rng() : draw(-2, max_parts + 2);
+        const KvNote n = kv_note(where, parts, run, max_parts);
+        EXPECT(n.parts >= 0 && n.slot >= 0 && n.place >= 0, "note %d %d", where, parts);
+        const int64_t last = ((int64_t)n.slot + n.parts - 1) * run + n.place;
+        EXPECT(n.parts == 0 || last < (int64_t)max_parts * run, "note %d %d of %d parts of %d rows", where, parts, max_parts, run);
+        const int64_t first = where >> kKvNoteShift, row = where & 255;
+        if (where >= 0 && row < run && parts >= 1 && first + parts <= max_parts)
+          EXPECT(n.slot == first && n.place == row && n.parts == parts, "note %d %d", where, parts);
+      }
+}
+
 int main(int, char** argv) {
   const char* what = argv[1];
   if (!std::strcmp(what, "items")) items();
+  else if (!std::strcmp(what, "notes")) notes();
   else return 2;
   if (!failures) std::printf("%s ok\n", what);
   return failures ? 1 : 0;

@@ -124,3 +124,30 @@ def test_layer_refuses_input_that_requires_a_gradient():
         layer(X.requires_grad_(), batch)
     with torch.no_grad():
         assert torch.equal(layer(X, batch), want)
+
+
+@pytest.mark.parametrize("lens,counts,q_heads,cu", [
+    ([6000, 5000, 4000], [236, 2, 2], 4, [0, 236, 4, 240]),    # kv_prompt in parts: tokens 128..131 are nobody's
+    ([6000, 5000, 4000], [4, 4, 4], 4, [0, 12, 0, 12]),        # kv_step in parts
+])
+def test_the_join_takes_no_row_of_a_run_that_there_is_not(lens, counts, q_heads, cu):
+    """cu that falls leaves rows that no run holds, whose notes are what the workspace held: here places past
+    the end of a run, or parts past the last one. Such rows are left alone, and so is what lies around."""
+    s = Setup(85, lens, counts, 2, 64, 16)
+    q, _ = s.values(q_heads, "bf16")
+    b = s.batch(max(lens), cu)
+    size = m8.llmint8_kv_attention_workspace_bytes(s.cache, b, q_heads)
+    assert size > 0
+    notes = s.rows * q_heads
+    for place, parts in ((255, 1), (0x7fffff00, 1), (0, 2 ** 31 - 1), (-1, 5), (0, 0), (2 ** 31 - 1, 2 ** 31 - 1)):
+        print(f"[case] {cu} note {place} {parts}", flush=True)
+        space = torch.full((size // 4 + 2048,), 7, dtype=torch.int32, device="cuda")
+        ws = space[1024:1024 + size // 4]
+        ws[-2 * notes:] = torch.tensor([place, parts] * notes, dtype=torch.int32, device="cuda")
+        out = torch.full((s.rows, q_heads, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+        m8.llmint8_kv_attention(s.cache, b, q, out=out, workspace=ws)
+        torch.cuda.synchronize()
+        assert (space[:1024] == 7).all() and (space[1024 + size // 4:] == 7).all()
+        assert out.isfinite().all()
+        if counts[0] == 236:
+            assert (out[128:132] == 3.0).all()

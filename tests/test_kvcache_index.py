@@ -31,3 +31,8 @@ def check(tmp_path_factory):
 def test_every_row_of_a_batch_is_worked_on_once(check):
     """Also where the call has rows past the last sequence's."""
     check("items")
+
+
+def test_a_note_of_any_content_names_rows_of_the_workspace(check):
+    """A row that no run holds (cu that falls) has a note of whatever the workspace held."""
+    check("notes")

@@ -20,23 +20,8 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
 // the larger of two, NaN if one of them is (fmaxf takes the other)
 __device__ __forceinline__ float max_or_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 
-// Tokens of sequence b in this call: rows [row0, row0 + n), positions
-// [len - n, len). Every number is cut to what the buffers hold, so that no
-// content of cu, len or table makes a kernel leave them: cu to [0, T], n to
-// >= 0, len to [0, width * page].
-struct KvSeq {
-  int b, row0, n, len;
-};
-
 __device__ __forceinline__ KvSeq kv_seq(const KvBatch& s, int page_shift, int b) {
-  KvSeq q;
-  const int c0 = min(max(s.cu[b], 0), s.T), c1 = min(max(s.cu[b + 1], 0), s.T);
-  q.b = b;
-  q.row0 = c0;
-  q.n = max(c1 - c0, 0);
-  const int64_t room = (int64_t)s.width << page_shift;
-  q.len = (int)min((int64_t)max(s.len[b], 0), room);
-  return q;
+  return kv_seq_of(b, s.cu[b], s.cu[b + 1], s.len[b], s.T, (int64_t)s.width << page_shift);
 }
 
 // kv_seq of a sequence that all lanes ask for
@@ -46,6 +31,7 @@ __device__ __forceinline__ KvSeq kv_seq_uniform(const KvBatch& s, int page_shift
   q.row0 = uniform(q.row0);
   q.n = uniform(q.n);
   q.len = uniform(q.len);
+  q.pos0 = uniform(q.pos0);
   return q;
 }
 
@@ -57,7 +43,7 @@ __device__ __forceinline__ KvSeq kv_seq_uniform(const KvBatch& s, int page_shift
 // past the last one's, or cu starts late or falls).
 template <int kThreads>
 __device__ __forceinline__ bool kv_find(const KvBatch& s, int page_shift, int item, int per, int shift,
-                                        int (&sh)[5], KvSeq* out, int* index, int* count) {
+                                        int (&sh)[6], KvSeq* out, int* index, int* count) {
   if (s.B == 1) {
     *out = kv_seq_uniform(s, page_shift, 0);
     const KvItems own = kv_items(0, out->row0, out->n, per, shift);
@@ -78,6 +64,7 @@ __device__ __forceinline__ bool kv_find(const KvBatch& s, int page_shift, int it
       sh[2] = q.len;
       sh[3] = own.first;
       sh[4] = own.count;
+      sh[5] = q.pos0;
     }
     b += mine;
     if (mine < min(kThreads, s.B - b0)) break;
@@ -88,20 +75,25 @@ __device__ __forceinline__ bool kv_find(const KvBatch& s, int page_shift, int it
   out->row0 = uniform(sh[0]);
   out->n = uniform(sh[1]);
   out->len = uniform(sh[2]);
+  out->pos0 = uniform(sh[5]);
   const KvItems own{uniform(sh[3]), uniform(sh[4])};
   *index = kv_item_index(own, item);
   *count = own.count;
   return *index >= 0;
 }
 
-// Page that the table names for the tokens of an entry; may be any number. Tokens
-// past an entry's end of the table are past the sequence's end as well.
+// Page that the table names for the tokens of an entry; may be any number. Past the
+// table's end, where a tile may reach but no token is, the last one's.
 __device__ __forceinline__ int kv_entry(const KvBatch& s, int b, int entry) {
   return s.table[(int64_t)b * s.width + min(entry, s.width - 1)];
 }
 // The page itself, or -1 where there is none of that number.
 __device__ __forceinline__ int kv_page(int number, int64_t pages) {
   return (uint32_t)number < (uint64_t)pages ? number : -1;
+}
+// The page of an entry that may be past the table's end, where there is none.
+__device__ __forceinline__ int kv_entry_page(const KvBatch& s, int b, int entry, int64_t pages) {
+  return entry < s.width ? kv_page(kv_entry(s, b, entry), pages) : -1;
 }
 
 }  // namespace llmint8

@@ -11,8 +11,8 @@ namespace llmint8 {
 int abi_hip_status(hipError_t e);
 int abi_cu_count();
 
-// The kernels index tokens, rows and work items in 32 bits
-// (an item's first token is below len + rows + 2 seqs page < 2^31)
+// The kernels index tokens, rows and work items in 32 bits (a launch has fewer than
+// rows + seqs items; positions are below len)
 constexpr int64_t kKvMax = int64_t(1) << 29;
 constexpr int64_t kKvMaxQHeads = 65536;
 constexpr int64_t kKvMaxQRows = int64_t(1) << 30;  // rows times query heads of an attention call
@@ -45,6 +45,39 @@ struct KvBatch {
   const int32_t* table;  // [B, width]
   int B, T, width;
 };
+// Tokens of sequence b in this call: rows [row0, row0 + n), positions from pos0 on
+// (below 0: rows without one), of a sequence that has tokens [0, len) in pages that
+// the table has entries for. Every number is cut to what the buffers hold, so that
+// no content of cu, len or table makes a kernel leave them: cu to [0, T], n to >= 0,
+// len to [0, width * page]. Positions are those of the whole length: a token past
+// the table has no page, and the ones before it keep their places.
+struct KvSeq {
+  int b, row0, n, len, pos0;
+};
+__host__ __device__ inline KvSeq kv_seq_of(int b, int cu0, int cu1, int length, int T, int64_t room) {
+  KvSeq q;
+  cu0 = cu0 < 0 ? 0 : cu0 > T ? T : cu0;
+  cu1 = cu1 < 0 ? 0 : cu1 > T ? T : cu1;
+  length = length < 0 ? 0 : length;
+  q.b = b;
+  q.row0 = cu0;
+  q.n = cu1 > cu0 ? cu1 - cu0 : 0;
+  q.len = length < room ? length : (int)room;
+  q.pos0 = length - q.n;
+  return q;
+}
+// The tokens of a sequence's rows that are on page `entry` of its table: positions
+// [t0, t1), slot 0 at base; none if t0 >= t1. There may be no such entry.
+struct KvOnPage {
+  int base, t0, t1;
+};
+__host__ __device__ inline KvOnPage kv_on_page(const KvSeq& q, int entry, int page_shift) {
+  const int64_t base = (int64_t)entry << page_shift, next = base + (1 << page_shift);
+  const int end = q.pos0 + q.n;
+  if (base >= end) return {0, 0, 0};  // below, base < 2^31
+  return {(int)base, q.pos0 > base ? q.pos0 : (int)base, next < end ? (int)next : end};
+}
+
 // The work items of a launch: sequence b with rows [row0, row0 + n) owns `count` of
 // them from `first` on, enough for the tiles of 2^shift that its n * per rows fill,
 // and one less at most than the pages of 2^shift that n tokens reach. With rows

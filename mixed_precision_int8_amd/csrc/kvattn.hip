@@ -107,7 +107,7 @@ __device__ __forceinline__ SeqWork seq_work(const KvAttnArgs& a, const KvSeq& s)
   SeqWork w;
   const int G = a.q_heads / a.c.heads;
   w.runs = (int)(((int64_t)s.n * G + 16 * RT - 1) / (16 * RT));
-  w.span = visible_span(s.len, s.len - s.n, s.len - 1, a.causal, a.window, a.sinks);
+  w.span = visible_span(s.len, s.pos0, s.pos0 + s.n - 1, a.causal, a.window, a.sinks);
   w.tiles = max(w.span.count(), 1);  // rows that see nothing are written too
   return w;
 }
@@ -212,6 +212,7 @@ __device__ __forceinline__ bool find_part(const KvAttnArgs& a, int w, int64_t (&
       found[4] = in;
       found[5] = parts;
       found[6] = (int)(y + cut) + in;
+      found[7] = q.pos0;
     }
     before += all_x;
     cut += all_y;
@@ -222,6 +223,7 @@ __device__ __forceinline__ bool find_part(const KvAttnArgs& a, int w, int64_t (&
   seq->row0 = uniform(found[1]);
   seq->n = uniform(found[2]);
   seq->len = uniform(found[3]);
+  seq->pos0 = uniform(found[7]);
   p->parts = uniform(found[5]);
   p->slot = uniform(found[6]);
   const int in = uniform(found[4]), run = in / p->parts;
@@ -264,7 +266,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void kv_step(KvAttnArgs a) 
   __shared__ float sh_ml[NT][4][16][2];
   __shared__ v4i sh_q[NT > 1 ? NT * NK * 2 * 64 : 1];
   __shared__ float sh_unit[NT][16];
-  __shared__ int sh_seq[5];
+  __shared__ int sh_seq[6];
   __shared__ int sh_found[8];
   __shared__ int64_t sh_sums[8];
   const int D = FULL ? DP : a.c.dim;
@@ -306,10 +308,10 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void kv_step(KvAttnArgs a) 
   };
   auto row_of = [&](int t) {
     const int r = min(row_first + 16 * (six + t) + nn, rows - 1), tok = r / G;
-    return Row{sq.row0 + tok, h * G + (r - tok * G), sq.len - sq.n + tok};
+    return Row{sq.row0 + tok, h * G + (r - tok * G), sq.pos0 + tok};
   };
-  const int pos_lo = sq.len - sq.n + row_first / G;  // of the run
-  const int pos_hi = sq.len - sq.n + min(row_first + 16 * RT - 1, rows - 1) / G;
+  const int pos_lo = sq.pos0 + row_first / G;  // of the run
+  const int pos_hi = sq.pos0 + min(row_first + 16 * RT - 1, rows - 1) / G;
   const Span span = CUT ? seq_work<RT>(a, sq).span
                         : visible_span(sq.len, pos_lo, pos_hi, a.causal, a.window, a.sinks);
   int i0 = 0, i1 = span.count();

@@ -181,18 +181,18 @@ __host__ __device__ constexpr int q_heads_of(int dim) { return NT == 64 ? 256 / 
 template <bool BF16, int NT, bool VEC>
 __global__ __launch_bounds__(256, VEC ? 4 : 2) void kc_append(KvAppendArgs a, int across) {
   __shared__ float red[4];
-  __shared__ int sh_seq[5];
+  __shared__ int sh_seq[6];
   const int P = 1 << a.c.page_shift, D = a.c.dim, H = a.c.heads;
   const int block = (int)(blockIdx.x % across);
   int index, count;
   KvSeq q;
   if (!kv_find<256>(a.s, a.c.page_shift, blockIdx.x / across, 1, a.c.page_shift, sh_seq, &q, &index, &count)) return;
-  const int pos0 = q.len - q.n;                               // position of row0 (< 0: those rows are dropped)
+  const int pos0 = q.pos0;
   auto write_page = [&](int entry) {
-    const int base = entry << a.c.page_shift;                   // position of slot 0
-    const int t0 = max(pos0, base), t1 = min(q.len, base + P);  // positions written
-    if (q.n == 0 || t0 >= t1) return;
-    const int n = t1 - t0, s0 = t0 - base;
+    const KvOnPage on = kv_on_page(q, entry, a.c.page_shift);
+    const int t0 = on.t0, t1 = on.t1;
+    if (t0 >= t1) return;
+    const int n = t1 - t0, s0 = t0 - on.base;
     const Rope<VEC> rope{a.rope, a.rope_rows, a.rot, a.interleaved};
     const int units = D >> 4;
     constexpr int kPer = 256 / NT;
@@ -236,7 +236,7 @@ __global__ __launch_bounds__(256, VEC ? 4 : 2) void kc_append(KvAppendArgs a, in
     if (y >= 2 * H) return;  // whole wavefronts, and no barrier follows where they are parts of a workgroup
     const bool isv = y >= H;
     const int h = isv ? y - H : y;
-    const int page = kv_page(kv_entry(a.s, q.b, entry), a.c.pages);
+    const int page = kv_entry_page(a.s, q.b, entry, a.c.pages);
     if (page < 0) return;
     const KvRows src = isv ? a.v : a.k;
     const int64_t ph = (int64_t)page * H + h;
@@ -438,19 +438,19 @@ hipError_t launch_kv_append(const KvAppendArgs& a, bool bf16, hipStream_t stream
 // codes one after the other: 5.2 us for one page, 18.8 for 256 pages of 51 MB.
 template <bool BF16>
 __global__ __launch_bounds__(256) void kc_gather(KvCache c, KvBatch s, KvRows k, KvRows v, int per, int across) {
-  __shared__ int sh_seq[5];
+  __shared__ int sh_seq[6];
   const int P = 1 << c.page_shift, D = c.dim, H = c.heads, tid = threadIdx.x;
   const int block = (int)(blockIdx.x % across);
   int index, count;
   KvSeq q;
   if (!kv_find<256>(s, c.page_shift, blockIdx.x / across, 1, c.page_shift, sh_seq, &q, &index, &count)) return;
-  const int pos0 = q.len - q.n;
+  const int pos0 = q.pos0;
   auto read_page = [&](int entry) {
-    const int base = entry << c.page_shift;
-    const int t0 = max(pos0, base), t1 = min(q.len, base + P);
-    if (q.n == 0 || t0 >= t1) return;
-    const int page = kv_page(kv_entry(s, q.b, entry), c.pages);
-    const int cpr = D >> 3, n = t1 - t0, s0 = t0 - base;
+    const KvOnPage on = kv_on_page(q, entry, c.page_shift);
+    const int t0 = on.t0, t1 = on.t1;
+    if (t0 >= t1) return;
+    const int page = kv_entry_page(s, q.b, entry, c.pages);
+    const int cpr = D >> 3, n = t1 - t0, s0 = t0 - on.base;
     const int64_t row = q.row0 + (t0 - pos0);
     const int step = 256 / cpr, r0 = tid / cpr, c0 = (tid - r0 * cpr) * 8;  // a thread's row of a step, and channels
     if (r0 >= step) return;

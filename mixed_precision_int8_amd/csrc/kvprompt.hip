@@ -90,7 +90,7 @@ __global__ __launch_bounds__(64 * W, DP <= 128 ? 2 : 1) void kv_prompt(KvAttnArg
   constexpr int kKPitch = 2 * DP + 16, kVPitch = 2 * 64 + 16;
   constexpr int kKBytes = 64 * kKPitch, kVBytes = DP * kVPitch;
   __shared__ __attribute__((aligned(16))) char smem_k[2 * kKBytes], smem_v[2 * kVBytes];
-  __shared__ int sh_seq[5];
+  __shared__ int sh_seq[6];
   const int D = FULL ? DP : a.c.dim;
   const int shift = a.c.page_shift, P = 1 << shift, H = a.c.heads, G = a.q_heads / H;
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
@@ -106,10 +106,10 @@ __global__ __launch_bounds__(64 * W, DP <= 128 ? 2 : 1) void kv_prompt(KvAttnArg
   const int b = sq.b;
   const int r = (int)min(row0 + wave * 32 + nn, rows - 1);
   const int tok = r / G, qh = h * G + (r - tok * G);
-  const int pos = sq.len - sq.n + tok;
+  const int pos = sq.pos0 + tok;
   const int64_t qrow = sq.row0 + tok;
-  const int pos_lo = sq.len - sq.n + (int)row0 / G;
-  const int pos_hi = sq.len - sq.n + (int)(min(row0 + kRows, rows) - 1) / G;
+  const int pos_lo = sq.pos0 + (int)row0 / G;
+  const int pos_hi = sq.pos0 + (int)(min(row0 + kRows, rows) - 1) / G;
 
   // tiles that any of the rows sees
   const int end = a.causal ? min(sq.len, pos_hi + 1) : sq.len;

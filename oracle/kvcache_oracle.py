@@ -68,10 +68,9 @@ class KVOracle:
     def append(self, cu, length, table, k, v, q=None, rope=None, interleaved=False):
         """k, v [rows, heads, dim], q [rows, q_heads, dim]; returns q rotated (float32, not rounded)."""
         q_out = None if q is None else np.array(q)
-        room = table.shape[1] * self.page
         for b in range(len(length)):
-            n, L = int(cu[b + 1] - cu[b]), min(int(length[b]), room)
-            first = L - n
+            n = int(cu[b + 1] - cu[b])
+            first = int(length[b]) - n
             todo = {}
             for i in range(n):
                 pos, row = first + i, int(cu[b]) + i
@@ -120,14 +119,15 @@ class KVOracle:
         dlogit = np.zeros((rows, hq))
         room = table.shape[1] * self.page
         for b in range(len(length)):
-            n, L = int(cu[b + 1] - cu[b]), min(int(length[b]), room)
+            n, whole = int(cu[b + 1] - cu[b]), int(length[b])
+            L = min(whole, room)  # tokens past the table have no page
             if n == 0:
                 continue
             k, v, there = self.tokens(table, b, 0, L)
             k, v = k.astype(np.float64), v.astype(np.float64)
             j = np.arange(L)
             for i in range(n):
-                pos, row = L - n + i, int(cu[b]) + i
+                pos, row = whole - n + i, int(cu[b]) + i
                 see = there.copy()
                 if causal:
                     see &= j <= pos

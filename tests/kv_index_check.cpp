@@ -1,6 +1,8 @@
 // Host sweep of the index arithmetic that the key/value cache's kernels share with
 // it (mixed_precision_int8_amd/csrc/kv_internal.h). Built and run by
 // tests/test_kvcache_index.py; the argument names the check.
+#include <algorithm>
+#include <cstdint>
 #include <cstdio>
 #include <cstring>
 #include <random>
@@ -67,6 +69,44 @@ static void items() {
   }
 }
 
+// Lengths past the table, up to the largest: a row keeps its position, tokens that
+// the table has no entry for are on entries past it, and nothing is out of range.
+static void positions() {
+  for (int round = 0; round < 200000; ++round) {
+    const int page_shift = draw(4, 7), width = draw(1, 40), T = draw(1, 500), P = 1 << page_shift;
+    const int64_t room = (int64_t)width << page_shift;
+    const int hostile[] = {-5, 0, T, T + 9, INT32_MAX, INT32_MIN};
+    const int kind = draw(0, 9);
+    const int cu0 = kind == 0 ? hostile[draw(0, 5)] : draw(0, T), cu1 = kind < 2 ? hostile[draw(0, 5)] : draw(cu0 < 0 || cu0 > T ? 0 : cu0, T);
+    const int length = draw(0, 3) ? draw(0, (int)room + 300) : draw(0, 1) ? draw(INT32_MAX - 300, INT32_MAX) : draw(-9, 9);
+    const KvSeq q = kv_seq_of(3, cu0, cu1, length, T, room);
+    EXPECT(q.row0 >= 0 && q.n >= 0 && q.row0 + q.n <= T, "cu %d %d of %d", cu0, cu1, T);
+    EXPECT(q.len == std::max<int64_t>(0, std::min<int64_t>(length, room)), "len %d, room %ld", length, (long)room);
+    const KvItems own = kv_items(3, q.row0, q.n, 1, page_shift);
+    std::vector<int> seen(q.n, 0);
+    for (int item = own.first; item < own.first + own.count; ++item) {
+      const KvEntries e = kv_item_entries(q.pos0, kv_item_index(own, item), own.count, page_shift);
+      for (int entry = e.first; entry < e.first + e.count; ++entry) {
+        const KvOnPage on = kv_on_page(q, entry, page_shift);
+        if (on.t0 >= on.t1) continue;
+        EXPECT(on.t0 >= on.base && on.t1 - 1 - on.base < P && on.base == entry * (int64_t)P, "entry %d", entry);
+        for (int64_t at = on.t0; at < on.t1; ++at) {
+          const int64_t row = at - q.pos0;
+          EXPECT(row >= 0 && row < q.n, "position %ld of %d", (long)at, length);
+          if (row < 0 || row >= q.n) continue;
+          ++seen[row];
+          // row i is token len - n + i, on entry (len - n + i) / P
+          EXPECT(at == std::max(length, 0) - (int64_t)q.n + row && at / P == entry, "position %ld of %d", (long)at, length);
+        }
+      }
+    }
+    for (int i = 0; i < q.n; ++i) {
+      const bool live = std::max(length, 0) - (int64_t)q.n + i >= 0;
+      EXPECT(seen[i] == (live ? 1 : 0), "row %d of %d, length %d", i, q.n, length);
+    }
+  }
+}
+
 // Any two numbers that a row's note may hold: what is read of the workspace for it
 // is within the parts' rows.
 static void notes() {
@@ -91,6 +131,7 @@ int main(int, char** argv) {
   const char* what = argv[1];
   if (!std::strcmp(what, "items")) items();
   else if (!std::strcmp(what, "notes")) notes();
+  else if (!std::strcmp(what, "positions")) positions();
   else return 2;
   if (!failures) std::printf("%s ok\n", what);
   return failures ? 1 : 0;

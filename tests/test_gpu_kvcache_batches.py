@@ -9,7 +9,7 @@ import oracle
 
 torch = pytest.importorskip("torch")
 import mixed_precision_int8_amd as m8  # noqa: E402
-from test_gpu_kvcache import TD, Setup, _say  # noqa: E402
+from test_gpu_kvcache import TD, Setup, _say, check_attention  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -151,3 +151,42 @@ def test_the_join_takes_no_row_of_a_run_that_there_is_not(lens, counts, q_heads,
         assert out.isfinite().all()
         if counts[0] == 236:
             assert (out[128:132] == 3.0).all()
+
+
+PAST = [
+    # table entries, lens, counts, heads, q_heads, dim, page, dtype
+    (2, [33, 20], [1, 3], 2, 4, 64, 16, "f16"),          # one token past 32
+    (3, [60, 48, 400], [30, 4, 2], 2, 2, 128, 16, "bf16"),
+    (1, [100, 70], [80, 70], 1, 4, 64, 64, "f16"),
+    (40, [700, 640], [90, 200], 1, 2, 64, 16, "bf16"),   # kv_prompt
+    (300, [5000, 4790, 6000], [4, 4, 4], 1, 2, 64, 16, "f16"),  # in parts
+]
+
+
+@pytest.mark.parametrize("case", PAST)
+def test_tokens_past_the_table(case):
+    """Lengths that the table has no entries for: tokens there are written nowhere, read as zeros and are not
+    seen; all others keep their places."""
+    width, lens, counts, heads, q_heads, dim, page, dtype = case
+    _say(f"past the table {case}")
+    s = Setup(87, [min(n, width * page) for n in lens], counts, heads, dim, page, width=width)
+    s.lens = list(lens)
+    rope_np = oracle.rope_table(m8.rope_frequencies(dim)[0], max(lens))
+    rope = torch.from_numpy(rope_np).cuda()
+    k, kx = s.values(heads, dtype)
+    v, vx = s.values(heads, dtype)
+    q, qx = s.values(q_heads, dtype)
+    qr = m8.llmint8_kv_append(s.cache, s.batch(), k, v, q=q, rope=rope)
+    want = torch.from_numpy(s.ref.append(s.cu, s.lens, s.table, kx, vx, qx, rope_np)).to(TD[dtype])
+    s.same_cache()
+    assert torch.equal(qr.cpu(), want)
+    gk, gv = m8.llmint8_kv_gather(s.cache, s.batch(), TD[dtype])
+    for b, n in enumerate(lens):
+        kx, vx, there = s.ref.tokens(s.table, b, n - counts[b], n)
+        at = slice(s.cu[b], s.cu[b + 1])
+        assert torch.equal(gk[at].cpu(), torch.from_numpy(kx).to(TD[dtype])), b
+        assert torch.equal(gv[at].cpu(), torch.from_numpy(vx).to(TD[dtype])), b
+        assert there.tolist() == [j < width * page for j in range(n - counts[b], n)]
+    q = (qr, want.float().numpy())
+    check_attention(s, q_heads, dtype, q=q, hints=(0, max(lens)))
+    check_attention(s, q_heads, dtype, q=q, hints=(0, max(lens)), window=40, sinks=2)

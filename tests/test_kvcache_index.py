@@ -36,3 +36,8 @@ def test_every_row_of_a_batch_is_worked_on_once(check):
 def test_a_note_of_any_content_names_rows_of_the_workspace(check):
     """A row that no run holds (cu that falls) has a note of whatever the workspace held."""
     check("notes")
+
+
+def test_rows_keep_their_positions_whatever_the_length(check):
+    """Tokens past the end of the table have no page; the rows before them stay where they are."""
+    check("positions")

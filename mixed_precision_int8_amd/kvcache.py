@@ -112,11 +112,15 @@ class KVBatch:
     table = property(lambda self: self._t[2])
 
 
+def _grad_enabled():
+    import torch
+    return torch.is_grad_enabled()
+
+
 def _rows(t, dtype, rows, heads, dim, device, name):
     """(pointer, token stride, head stride) of 16-bit rows [rows, heads, dim] with dense channels. The calls
     have no backward: a tensor that takes part in a graph would leave it without a word, so it is refused."""
-    import torch
-    if t.requires_grad and torch.is_grad_enabled():
+    if t.requires_grad and _grad_enabled():
         raise ValueError(f"{name}: requires a gradient, and the key/value cache has none to give (detach it, or "
                          "call under torch.no_grad())")
     if t.dtype != dtype or t.shape != (rows, heads, dim) or t.device != device:
@@ -203,7 +207,8 @@ def llmint8_kv_append(cache, batch, k, v, q=None, rope=None, interleaved=False, 
         heads = q.shape[1] if q.dim() == 3 else -1
         qr = _rows(q, k.dtype, n, heads, cache.dim, dev, "q")
         if q_out is None:
-            q_out = m8._empty(q.shape, q.dtype, dev, stream)
+            q_out = (torch.empty_like(q, memory_format=torch.contiguous_format) if stream is None
+                     else m8._empty(q.shape, q.dtype, dev, stream))
         orr = _rows(q_out, k.dtype, n, heads, cache.dim, dev, "q_out")
     elif q_out is not None:
         raise ValueError("q_out without q")
@@ -230,9 +235,10 @@ def llmint8_kv_gather(cache, batch, dtype=None, k=None, v=None, stream=None):
     code = m8._act_dtype(dtype)
     shape, dev = (batch.rows, cache.heads, cache.dim), cache.device
     if k is None:
-        k = m8._empty(shape, dtype, dev, stream)
+        k = torch.empty(shape, dtype=dtype, device=dev) if stream is None else m8._empty(shape, dtype, dev, stream)
     if v is None:
-        v = m8._empty(shape, dtype, dev, stream)
+        v = (torch.empty_like(k, memory_format=torch.contiguous_format) if stream is None
+             else m8._empty(shape, dtype, dev, stream))
     m8._check(lib.llmint8_kv_gather(cache._ref, batch._ref, code, *_rows(k, dtype, *shape, dev, "k"),
                                     *_rows(v, dtype, *shape, dev, "v"), _stream(stream, dev)),
               "llmint8_kv_gather")
@@ -258,7 +264,8 @@ def llmint8_kv_attention(cache, batch, q, scale=None, causal=True, window=0, sin
     heads = q.shape[1] if q.dim() == 3 else -1
     qr = _rows(q, q.dtype, n, heads, cache.dim, dev, "q")
     if out is None:
-        out = m8._empty(q.shape, q.dtype, dev, stream)
+        out = (torch.empty_like(q, memory_format=torch.contiguous_format) if stream is None
+               else m8._empty(q.shape, q.dtype, dev, stream))
     orr = _rows(out, q.dtype, n, heads, cache.dim, dev, "out")
     if lse is not None:
         m8._need(lse, torch.float32, (n, heads), "lse")

@@ -83,11 +83,12 @@ class KVBatch:
     """The sequences of a call: ``cu`` int32 [seqs + 1] (rows cu[b]..cu[b+1]-1 are the last tokens of
     sequence b), ``length`` int32 [seqs] (tokens in the cache, these rows included), ``table`` int32
     [seqs, width] (pages). The contents may change between calls; ``rows`` is the number of rows of the
-    call's tensors, ``max_len`` about the largest length (it sizes the work; any value is correct)."""
+    call's tensors, ``max_len`` about the largest length (it sizes the work; any value is correct).
+    ``positions``, where the host knows it: the rows' positions are below it (``PagedSequences`` sets it)."""
 
-    __slots__ = ("_t", "_c", "_ref", "seqs", "rows", "device")
+    __slots__ = ("_t", "_c", "_ref", "seqs", "rows", "device", "positions")
 
-    def __init__(self, cu, length, table, rows, max_len=0):
+    def __init__(self, cu, length, table, rows, max_len=0, positions=None):
         import torch
         m8 = _m8()
         self.seqs = length.shape[0] if length.dim() == 1 else -1
@@ -102,6 +103,7 @@ class KVBatch:
         if self.rows < 0 or max_len < 0:
             raise ValueError("rows and max_len: expected >= 0")
         self.device = cu.device
+        self.positions = positions
         self._t = (cu, length, table)
         self._c = _Batch(cu.data_ptr(), length.data_ptr(), table.data_ptr(), self.seqs, self.rows,
                          table.shape[1], int(max_len))
@@ -192,7 +194,8 @@ def _same_device(cache, batch):
 def llmint8_kv_append(cache, batch, k, v, q=None, rope=None, interleaved=False, q_out=None, stream=None):
     """Write k, v [rows, heads, dim] (fp16 or bf16) to the cache, k rotated by ``rope`` (fp32 [positions,
     rot], from ``llmint8_rope_table``) on the way. ``q`` [rows, q_heads, dim], if given, is rotated into
-    ``q_out`` (new by default; may be ``q``), which is returned."""
+    ``q_out`` (new by default; may be ``q``), which is returned. Positions that ``rope`` has no row for are
+    refused where the batch knows its ``positions``; otherwise they take its last row."""
     import torch
     m8 = _m8()
     lib = m8.load_library()
@@ -218,6 +221,8 @@ def llmint8_kv_append(cache, batch, k, v, q=None, rope=None, interleaved=False, 
             raise ValueError(f"rope: expected contiguous fp32 [positions, rot] on {dev}, got {rope.dtype} "
                              f"{tuple(rope.shape)} on {rope.device}")
         table_rows, rot = rope.shape
+        if batch.positions is not None and batch.positions > table_rows:
+            raise ValueError(f"rope: {table_rows} positions, and the batch's rows reach {batch.positions}")
         table = rope.data_ptr()
     m8._check(lib.llmint8_kv_append(cache._ref, batch._ref, code, *kr, *vr, *qr, *orr, heads, table,
                                     table_rows, rot, 1 if interleaved else 0, _stream(stream, dev)),
@@ -343,7 +348,8 @@ class PagedSequences:
         flat = torch.tensor(cu + lens + [p for t in table for p in t], dtype=torch.int32).to(self.cache.device)
         b = len(seqs)
         parts = [flat[:b + 1].clone(), flat[b + 1:2 * b + 1].clone(), flat[2 * b + 1:].clone()]
-        return KVBatch(parts[0], parts[1], parts[2].view(b, width), cu[-1], max_len=max(lens, default=0))
+        return KVBatch(parts[0], parts[1], parts[2].view(b, width), cu[-1], max_len=max(lens, default=0),
+                       positions=max((n for n, m in zip(lens, counts) if m > 0), default=0))
 
 
 class Int8SelfAttention:

@@ -40,3 +40,19 @@ def test_tensors_that_require_a_gradient_are_refused(setup):
         with torch.no_grad():
             call(g)
         call(g.detach())
+
+
+def test_positions_that_the_rope_table_has_no_row_for_are_refused(setup):
+    c, _, _ = setup
+    seqs = m8.PagedSequences(c)
+    a, b = seqs.add(), seqs.add()
+    x = torch.zeros((18, 2, 32), dtype=torch.float16)
+    rope = torch.zeros((17, 32), dtype=torch.float32)
+    m8.llmint8_kv_append(c, seqs.extend([a], [17]), x[:17], x[:17], rope=rope)
+    with pytest.raises(ValueError, match="17 positions.*18"):
+        m8.llmint8_kv_append(c, seqs.extend([a, b], [1, 2]), x[:3], x[:3], rope=rope)
+    m8.llmint8_kv_append(c, seqs.extend([a, b], [0, 2]), x[:2], x[:2], rope=rope)  # only b has rows
+    m8.llmint8_kv_append(c, seqs.extend([a], [1]), x[:1], x[:1])                    # nothing is rotated
+    t = seqs.whole([a])
+    m8.llmint8_kv_append(c, m8.KVBatch(t.cu, t.length, t.table, 19), torch.zeros((19, 2, 32)).half(),
+                         torch.zeros((19, 2, 32)).half(), rope=rope)               # the host does not know

@@ -72,10 +72,10 @@ struct KvOnPage {
   int base, t0, t1;
 };
 __host__ __device__ inline KvOnPage kv_on_page(const KvSeq& q, int entry, int page_shift) {
-  const int64_t base = (int64_t)entry << page_shift, next = base + (1 << page_shift);
   const int end = q.pos0 + q.n;
-  if (base >= end) return {0, 0, 0};  // below, base < 2^31
-  return {(int)base, q.pos0 > base ? q.pos0 : (int)base, next < end ? (int)next : end};
+  if (entry > (end - 1) >> page_shift) return {0, 0, 0};  // where base could leave 32 bits
+  const int base = entry << page_shift, left = end - base;
+  return {base, q.pos0 > base ? q.pos0 : base, base + (left < 1 << page_shift ? left : 1 << page_shift)};
 }
 
 // The work items of a launch: sequence b with rows [row0, row0 + n) owns `count` of

@@ -501,7 +501,20 @@ LLMINT8_API llmint8_status llmint8_kv_gather(const llmint8_kv_cache* cache, cons
  * and gets o = sum_j softmax(scale q . k)_j v_j, rounded once, and (lse not
  * NULL, fp32 [rows, q_heads]) log sum_j exp(scale q . k_j). A row that sees
  * nothing gets zeros and -inf. Any mix of single tokens and longer runs is one
- * call. Sums and statistics are fp32 or exact integers.
+ * call.
+ *   Precision: logits, statistics and sums are fp32 or exact integers; exp, log
+ * and reciprocals are the hardware's. Narrower are q and the softmax weights, by
+ * the kernel that the call takes (rows * q_heads / heads, to a sequence on
+ * average):
+ *   up to 32   8-bit products: q is held to 2^-16 of the largest channel of its row
+ *              and head (a channel far below the largest has fewer bits than it
+ *              came with); a weight times V's scale to 2^-16 of the largest one of
+ *              its 64 tokens
+ *   more       16-bit products: fp16 q exactly, bf16 q to 2^-38 of its largest
+ *              channel; a weight to 2^-11 of itself, or 2^-33 of the row's largest
+ * The magnitudes aV of the pages that a row sees may differ by 2^100, zero counting
+ * as 2^-64 (any fp16 values do not reach that): past it the share of the smaller
+ * ones in the softmax is lost.
  *   q_heads    a multiple of heads; rows * q_heads <= 2^30
  *   scale      finite (usually 1 / sqrt(dim))
  *   workspace  llmint8_kv_attention_workspace_bytes(...) bytes, 256-byte

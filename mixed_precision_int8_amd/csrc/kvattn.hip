@@ -11,10 +11,16 @@
 //   S^T = K . q^T   A = 16 tokens x 64 channels of codes, as loaded; B = q, held
 //                   as 16-bit integers in two int8 planes (q = qi * max|q| /
 //                   32639, qi = 256 hi + lo): the error of a channel is 2^-16 of
-//                   the row's largest, below the inputs' own rounding, and the
-//                   sums are exact (dim * 127 * 32639 < 2^31).
+//                   the row's largest. That is below the inputs' own rounding for
+//                   channels down to 2^-5 of the largest in fp16 and 2^-8 in bf16;
+//                   smaller ones keep fewer bits than they had. Over 128 channels
+//                   of like keys that changes a logit by about what the rounding
+//                   of the largest one did; a third plane would keep them, at
+//                   half the first product again.
+//                   The sums are exact (dim * 127 * 32639 < 2^31).
 //   O^T = V^T . P^T A = 16 channels x 64 tokens of codes, as loaded; B = the
-//                   weights exp2(u - tile max) as 16-bit integers in two planes.
+//                   weights exp2(u - tile max) as 16-bit integers in two planes
+//                   (half a step is 2^-16 of the tile's largest).
 // The tokens of a tile are assigned to the rows of S^T so that the weights a lane
 // gets out of the first product (token 16 g + 4 t + i of query row n, lane 16 g +
 // n) are the operand it needs for the second one: nothing moves between lanes.

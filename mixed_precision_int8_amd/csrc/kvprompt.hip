@@ -8,7 +8,8 @@
 // on v_mfma_f32_32x32x16_f16.
 //   S^T = K . q^T   A = 32 tokens x 16 channels from LDS, B = q in registers, fp16
 //                   (bf16 rows times a power of two that brings the largest
-//                   channel to 2^13: exact but for channels under 2^-37 of it)
+//                   channel to 2^13: exact but for channels under 2^-30 of it,
+//                   whose last bits are below fp16's 2^-24)
 //   O^T = V^T . P^T A = 32 channels x 16 tokens from LDS, B = the weights as fp16
 // Tokens are assigned to the rows of S^T so that a lane's weights are, in order,
 // its operand of the second product (bits 2 and 3 of the row swapped). Scales

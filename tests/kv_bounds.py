@@ -9,7 +9,7 @@ to first order and (exp and the sum's own change) second; their weights are inte
 their 64 tokens, V's scale (a per code) among them:
   S = sum over tiles (max_j p_j a_j) / 65278 sum_j |code_j|
 The 16-bit products round each weight by 2^-11, those under 2^-14 to 2^-25 of 2^-8 of the row's largest: F = 2^-11 A
-+ 2^-31 sum_j |code_j| max_j p_j a_j (q is exact, or to 2^-30 of its largest channel).
++ 2^-31 sum_j |code_j| max_j p_j a_j (q is exact, or to 2^-38 of its largest channel).
 E, in units of 2^-24 and twice (the weight and the sum): a logit's scale and sum, eight roundings of |s| + |log2 a|;
 its products' sum in fp32, a rounding of sum_c |q_c k_c| for every 16 channels and five more; exponentials,
 logarithms, reciprocals of the hardware and the join, 24; the sums over a row's tokens, one for every 16 of them and
@@ -108,6 +108,7 @@ class Rows:
         size = np.where(see, np.abs(s), 0).max(1, keepdims=True) + np.abs(np.log2(a)).max()
         whole = np.where(see, abs(scale) * (np.abs(q) @ np.abs(k).T), 0).max(1, keepdims=True)
         E = 2.0 ** -24 * (8 * size + (k.shape[1] / 16 + 5) * whole + 24 + 5 * len(tiles))
+        self.exact_q_tol = u * np.abs(self.o) + F + 2 * E * A + 2.0 ** -25
         self.tol = u * np.abs(self.o) + np.maximum(Q + S, F) + 2 * E * A + 2.0 ** -25
         self.lse_tol = (h * abs(scale) * np.abs(p @ k).sum(1, keepdims=True) + 1.5 * d * d + 2 * E)[:, 0] + 2.0 ** -23 * np.abs(self.lse)
 

@@ -500,8 +500,9 @@ LLMINT8_API llmint8_status llmint8_kv_gather(const llmint8_kv_cache* cache, cons
  *   of these only j > p - window or j < sinks
  * and gets o = sum_j softmax(scale q . k)_j v_j, rounded once, and (lse not
  * NULL, fp32 [rows, q_heads]) log sum_j exp(scale q . k_j). A row that sees
- * nothing gets zeros and -inf. Any mix of single tokens and longer runs is one
- * call.
+ * nothing gets zeros and -inf. Any mix of single tokens and longer runs may be
+ * one call; the kernel is chosen for all of it, so that prompts beside many single
+ * tokens are faster in a call of their own.
  *   Precision: logits, statistics and sums are fp32 or exact integers; exp, log
  * and reciprocals are the hardware's. Narrower are q and the softmax weights, by
  * the kernel that the call takes (rows * q_heads / heads, to a sequence on

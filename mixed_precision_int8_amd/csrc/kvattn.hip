@@ -727,7 +727,10 @@ int kv_attention_run(const KvBatch& s, int heads, int q_heads) {
   return per <= 16 ? 16 : 32;
 }
 
-// Whether a call's sequences have rows enough, on average, for kv_prompt: more than
+// Whether a call's sequences have rows enough, on average, for kv_prompt (one
+// kernel for all of a call: a prompt of 512 tokens with 64 single ones of 500-8000
+// takes 253 us in one call, 115 and 19 in two; with a prompt of 400 131, 115 and
+// 16): more than
 // the 32 of a run of kv_step, which would read the codes again for the next ones.
 // Measured, 16 sequences of 1000-6000 tokens (us, kv_step / kv_prompt): 20 rows
 // 40 / 56, 32 rows 40 / 57, 80 rows (3000-6000) 127 / 79; 64 of 500-4000 with 64
@@ -750,7 +753,10 @@ static int64_t runs_at_most(const KvBatch& s, int heads, int q_heads) {
 // there the join costs more than the cut gains. Measured, us uncut / cut: one
 // sequence of 2000 tokens 19 / 24; 16 of 2000-3000 29 / 28 and of 2000-4000 36 /
 // 29; 24 of 2000-4000 37 / 42; 64 of 1000-2000 41 / 56. *slots: workgroups that
-// run at once, three, two or one to a CU by the registers of the head size.
+// are taken to run at once, three, two or one to a CU: what the registers of the
+// head size's largest forms leave room for. One sixteen of whole heads of 64 or 96
+// would leave room for four and three; what the rule would make of that is not
+// measured.
 int kv_attention_extra(const KvBatch& s, int heads, int q_heads, int dim, int64_t max_span, int num_cus, int* slots) {
   *slots = num_cus * (dim <= 64 ? 3 : dim <= 128 ? 2 : 1);
   const int64_t runs = runs_about(s, heads, q_heads);

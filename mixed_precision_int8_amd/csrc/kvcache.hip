@@ -166,15 +166,17 @@ __device__ __forceinline__ void transpose8x4(const uint32_t w[8], uint32_t lo[4]
 //
 // HBM-bound for prompts (NT 256): every input is read once, as what a thread holds
 // of a page stays in registers between the maximum and the codes, and the angles
-// of a token once for four heads of q. 9800 tokens of 32 and 8 heads of 128 take 42
-// us, 160 MB at 3.8 TB/s. A step writes few tokens (NT 64): there the time is that
+// of a token once for four heads of q. 7495 tokens of 32 and 8 heads of 128 take 42
+// us, 169 MB at 4.0 TB/s. A step writes few tokens (NT 64): there the time is that
 // of the loads that wait for each other (one token 4.4 us, one of each of 256
 // sequences 9.9 us), and a wavefront takes a head, a thread one unit of q. Measured
 // with the gather of the open pages (us, NT 64 / 256): 256 sequences of one token
 // 26 / 44; 64 of four 18 / 21, of six 19 / 21, of eight 23 / 21, of 32 46 / 27.
 //
 // VEC: Rope's. Partners and angles that are read one by one take registers that
-// the vectors of the other form need, so the two are kept apart.
+// the vectors of the other form need, so the two are kept apart. The form without
+// is slow (the same tokens with 24 of 128 channels turned 192 us, with all turned
+// 35, both from the caches; 150 scalars spilled); head sizes in use have vectors.
 template <int NT, bool VEC>
 __host__ __device__ constexpr int q_heads_of(int dim) { return NT == 64 ? 256 / (dim >> 4) : VEC ? 4 : 1; }
 

@@ -24,10 +24,14 @@
 // tile.
 //
 // Bound by the SIMDs' issue of vector and matrix instructions together (55% and
-// 40-45% of the time on long prompts; the softmax and the conversion are what the
-// first are): one prompt of 16384 tokens of 32 heads of 128 runs at 1040 TFLOP/s,
-// prompts of 2000-4096 behind 5000 at 880-920 (their last tiles are masked and the
-// last workgroups alone), where a large product of the library runs at 1530.
+// 40-45% of the time on long prompts; the softmax, the conversion and about a dozen
+// of 49 spilled scalars read back to a tile are what the first are) and by LDS: a
+// tile's products read it once for every wavefront, 160 KB with the stores, 1280
+// cycles of a CU at 128 bytes a cycle where its matrix instructions take 1024, and
+// the stores' lanes, 16 bytes at a stride of 32, conflict. One prompt of 16384 tokens of 32 heads of 128 runs at 1040 TFLOP/s,
+// prompts of 2000-4096 behind 5000 at 880-920 (their last tiles are masked, the last
+// workgroups alone, and the rows that start first are the last sequence's, not the
+// longest of the call), where a large product of the library runs at 1530.
 #include <algorithm>
 #include <type_traits>
 

@@ -190,3 +190,44 @@ def test_tokens_past_the_table(case):
     q = (qr, want.float().numpy())
     check_attention(s, q_heads, dtype, q=q, hints=(0, max(lens)))
     check_attention(s, q_heads, dtype, q=q, hints=(0, max(lens)), window=40, sinks=2)
+
+
+def test_layer_in_a_captured_graph_with_a_fixed_number_of_rows():
+    """As a server replays it: eight rows to a call, of which each step uses some, over growing sequences. Every
+    replay against eager calls on a cache of their own."""
+    g = torch.Generator(device="cuda").manual_seed(11)
+    hidden, q_heads, heads, dim, rows, page = 256, 8, 2, 32, 8, 16
+    W = (torch.randn(((q_heads + 2 * heads) * dim, hidden), device="cuda", generator=g) / 16).half()
+    Wo = (torch.randn((hidden, q_heads * dim), device="cuda", generator=g) / 16).half()
+    f, mag = m8.rope_frequencies(dim)
+    rope = m8.llmint8_rope_table(f, 100, mag)
+    X = torch.zeros((rows, hidden), device="cuda").half()
+    table = torch.tensor([[5, 1, 7], [0, 4, 2], [3, 6, 8]], dtype=torch.int32, device="cuda")
+    cu = torch.zeros((4,), dtype=torch.int32, device="cuda")
+    lens = torch.zeros((3,), dtype=torch.int32, device="cuda")
+    batch = m8.KVBatch(cu, lens, table, rows)
+    mine, theirs = ([m8.Int8SelfAttention(W, Wo, q_heads, m8.KVCache.empty(9, heads, dim, page), rope=rope)][0] for _ in range(2))
+    mine(X, batch)  # what a first call sets up
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        Y = mine(X, batch)
+    held = [0, 0, 0]
+    for counts in ([5, 2, 1], [1, 1, 1], [1, 0, 1], [3, 4, 0], [1, 1, 1], [0, 0, 0], [2, 1, 5], [1, 1, 1]):
+        held = [h + n for h, n in zip(held, counts)]
+        cu.copy_(torch.tensor([0, *np.cumsum(counts)], dtype=torch.int32))
+        lens.copy_(torch.tensor(held, dtype=torch.int32))
+        X.copy_(torch.randn((rows, hidden), device="cuda", generator=g))
+        graph.replay()
+        got = Y.clone()
+        want = theirs(X, batch)
+        torch.cuda.synchronize()
+        used = sum(counts)
+        assert torch.equal(got, want), counts
+        assert (got[used:] == 0).all() and (used == 0 or bool((got[:used] != 0).any()))
+    for a, b in zip(mine.cache._t[:2], theirs.cache._t[:2]):
+        for s, n in enumerate(held):
+            for e in range(0, n, page):
+                p = int(table[s, e // page])
+                part = (lambda t: t[p, :, :n - e]) if a.shape[2] == page else (lambda t: t[p, :, :, :n - e])
+                assert torch.equal(part(a), part(b))

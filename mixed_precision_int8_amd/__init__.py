@@ -299,7 +299,16 @@ def _workspace(T, K, N, device, workspace, path=LLMINT8_PATH_AUTO, stream=None):
         need = llmint8_workspace_bytes_path(T, K, N, path)
         if need > 0:
             workspace = _empty((need,), torch.uint8, device, stream)
+    else:
+        _need_workspace(workspace, device)
     return workspace
+
+
+def _need_workspace(ws, device):
+    """Kernels take a workspace by its address and bytes: those have to be all of it, on the call's device."""
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"workspace: expected contiguous on {device}, got {ws.dtype} {tuple(ws.shape)} with strides "
+                         f"{ws.stride()} on {ws.device}")
 
 
 def _ws_bytes(ws):
@@ -497,6 +506,8 @@ def _backward_args(dY, Wq, sW, dX, workspace, dtype=None, stream=None):
         need = llmint8_backward_workspace_bytes(T, K, N)   # 0: the weight is dequantized on the fly
         if need > 0:
             workspace = _empty((need,), torch.uint8, dY.device, stream)
+    else:
+        _need_workspace(workspace, dY.device)
     return T, K, N, dX, workspace
 
 

@@ -274,10 +274,14 @@ def llmint8_kv_attention(cache, batch, q, scale=None, causal=True, window=0, sin
     orr = _rows(out, q.dtype, n, heads, cache.dim, dev, "out")
     if lse is not None:
         m8._need(lse, torch.float32, (n, heads), "lse")
+        if lse.device != dev:
+            raise ValueError(f"lse: expected on {dev}, got {lse.device}")
     if workspace is None:
         need = lib.llmint8_kv_attention_workspace_bytes(cache._ref, batch._ref, heads, window, sinks)
         if need > 0:
             workspace = m8._empty((need,), torch.uint8, dev, stream)
+    else:
+        m8._need_workspace(workspace, dev)
     m8._check(lib.llmint8_kv_attention(cache._ref, batch._ref, code, *qr, heads,
                                        1.0 / math.sqrt(cache.dim) if scale is None else float(scale),
                                        1 if causal else 0, window, sinks, *orr,

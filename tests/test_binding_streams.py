@@ -111,3 +111,32 @@ def test_memory_of_a_call_on_the_current_stream(watch, name):
     for stream in (None, current):
         CALLS[name](args, stream)
     assert made and not used and all(stream is current for stream, _ in made)
+
+
+WITH_WORKSPACE = {
+    "linear": lambda a, w: m8.llmint8_linear(a["X"], a["Wq"], a["sW"], workspace=w),
+    "linear_ex": lambda a, w: m8.llmint8_linear_ex(a["X"], a["Wq"], a["sW"], workspace=w),
+    "linear_debug": lambda a, w: m8.llmint8_linear_debug(a["X"], a["Wq"], a["sW"], workspace=w),
+    "linear_timed": lambda a, w: m8.llmint8_linear_timed(a["X"], a["Wq"], a["sW"], 6.0, None, w, []),
+    "backward": lambda a, w: m8.llmint8_linear_backward_input(a["dY"], a["Wq"], a["sW"], workspace=w),
+    "backward_ex": lambda a, w: m8.llmint8_linear_backward_input_ex(a["dY"], a["Wq"], a["sW"], workspace=w),
+    "kv_attention": lambda a, w: m8.llmint8_kv_attention(*_kv(a), a["k"], workspace=w),
+}
+
+
+@pytest.mark.parametrize("name", WITH_WORKSPACE)
+def test_workspaces_that_are_not_the_call_s_memory_are_refused(watch, name):
+    """Of another device, or with holes: the kernels would work in memory that is not the tensor's."""
+    args = watch[-1]
+    call = WITH_WORKSPACE[name]
+    call(args, torch.zeros((4096,), dtype=torch.uint8))
+    for bad in (torch.zeros((4096,), dtype=torch.uint8, device="meta"), torch.zeros((8192,), dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            call(args, bad)
+
+
+def test_lse_of_another_device_is_refused(watch):
+    a = watch[-1]
+    m8.llmint8_kv_attention(*_kv(a), a["k"], lse=torch.zeros((4, 2)))
+    with pytest.raises(ValueError, match="lse"):
+        m8.llmint8_kv_attention(*_kv(a), a["k"], lse=torch.zeros((4, 2), device="meta"))

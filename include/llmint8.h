@@ -418,11 +418,11 @@ LLMINT8_API int llmint8_gemm_tile(int64_t T, int64_t N);
  * len[b] - n_b .. len[b] - 1; token j is in page table[b][j / page], slot
  * j % page. cu rises from 0 to at most rows; any n_b may be 0. The three arrays
  * are device memory and the host never reads them. The kernels stay inside the
- * buffers whatever they hold (where cu falls, rows may get any value): rows at
- * negative positions (n_b > len[b]) and rows past cu[seqs] are left alone by
- * append and gather, a page id outside [0, pages) or an entry past width is a
- * page that does not exist (append writes nothing there, gather gives zeros,
- * attention does not see it).
+ * buffers whatever they hold (where cu falls, rows may get any value). Rows past
+ * cu[seqs] are left alone by all calls, rows at negative positions (n_b > len[b])
+ * by append and gather (in attention they see nothing). A page id outside
+ * [0, pages) or an entry past width is a page that does not exist: append writes
+ * nothing there, gather gives zeros, attention does not see it.
  *
  * Limits (LLMINT8_ERR_UNSUPPORTED): page 16, 32, 64 or 128; dim a multiple of 16
  * up to 256; heads <= 4096; rows, width * page and 2 seqs page <= 2^29. Device

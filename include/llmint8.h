@@ -531,6 +531,144 @@ LLMINT8_API llmint8_status llmint8_kv_attention(const llmint8_kv_cache* cache, c
                                                 int64_t out_head, float* lse, void* workspace,
                                                 size_t workspace_bytes, void* stream);
 
+/*
+ * Training through a layer on int8 weights: what stands between its linears, with
+ * gradients. Nothing here touches the int8 weights; llmint8_linear_backward_input
+ * carries the gradient through those.
+ *
+ * Attention over packed sequences: the rows of a call are whole sequences one after
+ * the other, and every token of a sequence is a row of q, k and v. Rows cu[b] ..
+ * cu[b+1]-1 are sequence b; cu rises from 0 to at most rows and is device memory that
+ * the host never reads. Whatever it holds, the kernels stay inside the buffers (where
+ * it falls, rows may get any value). Rows past cu[seqs] are left as they were, in all
+ * outputs. A row at position p of its sequence sees the tokens j of it with
+ *   causal == 0: all;  causal != 0: j <= p, and with window > 0 of these only
+ *   j > p - window or j < sinks
+ * as in llmint8_kv_attention. Query head i belongs to key/value head i / (q_heads /
+ * heads).
+ *   out = sum_j P_j v_j, P = softmax(scale q . k); lse = log sum_j exp(scale q . k_j)
+ *   delta = sum_c dout out; dv = P^T dout; dS = P (dout . v - delta);
+ *   dq = scale dS k; dk = scale dS^T q, dk and dv summed over a group's query heads
+ * Each output is rounded once. Logits, statistics, sums and delta are fp32; exp, log
+ * and reciprocals are the hardware's. P and dS are rounded to the 16-bit type for the
+ * products that sum over them: to 2^-8 (bf16) or 2^-11 (fp16) of each, in fp16 but for
+ * weights under 2^-29 of one and dS under 2^-30 of the largest of its row (dq) or
+ * token (dk). Results do not depend on what else runs: the same call gives the same
+ * bits. A NaN or infinity reaches the rows that see its token (its gradients: the
+ * tokens that its row sees) and no others.
+ *   q, out, dout, dq  [rows, q_heads, dim]; k, v, dk, dv [rows, heads, dim]: 16 bits,
+ *              dense channels, token and head strides in elements (multiples of 8, token
+ *              strides up to 2^23), 16-byte aligned; may be slices of larger tensors.
+ *              Outputs overlap neither inputs nor each other.
+ *   lse        fp32 [rows, q_heads], dense, or NULL in the forward call
+ *   dim        a multiple of 8 up to 256; q_heads a multiple of heads
+ *   scale      finite
+ *   workspace  llmint8_attention_backward_workspace_bytes(...) bytes, 256-byte aligned,
+ *              contents on entry do not matter
+ * seqs = 0 or rows = 0 is a no-op.
+ */
+typedef struct {
+  const int32_t* cu; /* [seqs + 1] */
+  int64_t seqs, rows;
+  int64_t q_heads, heads, dim;
+  float scale;
+  int causal;
+  int64_t window, sinks;
+} llmint8_attention_shape;
+
+/* 16-bit rows: address, token stride and head stride in elements. */
+typedef struct {
+  void* data;
+  int64_t token, head;
+} llmint8_rows;
+
+LLMINT8_API llmint8_status llmint8_attention(const llmint8_attention_shape* shape, int dtype,
+                                             const llmint8_rows* q, const llmint8_rows* k,
+                                             const llmint8_rows* v, const llmint8_rows* out, float* lse,
+                                             void* stream);
+LLMINT8_API size_t llmint8_attention_backward_workspace_bytes(const llmint8_attention_shape* shape);
+LLMINT8_API llmint8_status llmint8_attention_backward(
+    const llmint8_attention_shape* shape, int dtype, const llmint8_rows* q, const llmint8_rows* k,
+    const llmint8_rows* v, const llmint8_rows* out, const float* lse, const llmint8_rows* dout,
+    const llmint8_rows* dq, const llmint8_rows* dk, const llmint8_rows* dv, void* workspace,
+    size_t workspace_bytes, void* stream);
+
+/*
+ * Rotary positions with one or more axes (time, height, width): the first `rot`
+ * channels of every head turn, pair i by row pos[row][axis[i]] of the table from
+ * llmint8_rope_table (pairs and rounding as in llmint8_kv_append); the others are
+ * copied. inverse != 0 turns back, which is the gradient of the call without.
+ *   x, y    [rows, heads, dim] in dtype (strides in elements, 2-byte aligned); y may be
+ *           x (same strides) and must not overlap it otherwise. x2, y2 with heads2 are a
+ *           second tensor of the same rows (the keys), or NULL with heads2 = 0
+ *   pos     device int32 [rows, axes]; positions outside the table take its nearest row
+ *   axis    HOST uint8 [rot / 2], read before the call returns, each below axes (1 to 8)
+ *   rot     even, up to dim and 256; dim even, up to 65536
+ */
+LLMINT8_API llmint8_status llmint8_rope(int dtype, const llmint8_rows* x, const llmint8_rows* y,
+                                        int64_t heads, const llmint8_rows* x2, const llmint8_rows* y2,
+                                        int64_t heads2, int64_t rows, int64_t dim, const int32_t* pos,
+                                        int64_t axes, const uint8_t* axis, const float* table,
+                                        int64_t table_rows, int64_t rot, int interleaved, int inverse,
+                                        void* stream);
+
+/*
+ * Layer norm: xh = (x - mean) / sqrt(mean((x - mean)^2) + eps), y = xh w + b over the K
+ * channels of a row; backward with g = dy w
+ *   dx = (g - mean(g) - xh mean(g xh)) / sqrt(var + eps), dw = sum dy xh, db = sum dy.
+ * Statistics and sums are fp32, every output is rounded once; sums over rows are taken
+ * in an order that the sizes alone decide.
+ *   x, y, dy, dx  [rows, K] in dtype F16, BF16 or F32, dense channels, row strides in
+ *                 elements; aligned to their elements. dx overlaps neither x nor dy; y may
+ *                 be x.
+ *   w, b, dw, db  [K] in w_dtype: dtype, or F32; w and b may be NULL (1 and 0), dw and db
+ *                 as well where they are not wanted
+ *   stats         fp32 [rows, 2] (mean and 1 / sqrt(var + eps)), or NULL in the forward
+ *   eps           > 0, finite; K up to 65536
+ *   workspace     llmint8_layer_norm_workspace_bytes(rows, K) bytes, 256-byte aligned; NULL
+ *                 where neither dw nor db is wanted
+ * rows = 0 writes zeros to dw and db.
+ */
+LLMINT8_API llmint8_status llmint8_layer_norm(const void* x, int64_t x_row, int dtype, int64_t rows,
+                                              int64_t K, const void* w, const void* b, int w_dtype,
+                                              float eps, void* y, int64_t y_row, float* stats,
+                                              void* stream);
+LLMINT8_API size_t llmint8_layer_norm_workspace_bytes(int64_t rows, int64_t K);
+LLMINT8_API llmint8_status llmint8_layer_norm_backward(const void* dy, int64_t dy_row, const void* x,
+                                                       int64_t x_row, int dtype, int64_t rows, int64_t K,
+                                                       const void* w, int w_dtype, const float* stats,
+                                                       void* dx, int64_t dx_row, void* dw, void* db,
+                                                       void* workspace, size_t workspace_bytes,
+                                                       void* stream);
+
+/*
+ * The norm over many gradients, and clipping by it.
+ *   norm = fl32(scale sqrt(sum over all g^2)), squares and sums in 64 bits, in an order
+ *          that the sizes alone decide; scale is 1 / loss scale, or 1
+ *   out  = r(fl32(g f)), f = fl32(scale min(1, max_norm / (norm + 1e-6))) in 64 bits
+ * With several GPUs each takes the norm of its own, the squares are added, and every GPU
+ * clips by the root. A norm that is NaN makes every value NaN (but for max_norm infinity).
+ *   grads     HOST array of `count` tensors, read before the call returns: data (device,
+ *             aligned to its elements), n values of dtype F16, BF16 or F32; out (clip
+ *             only): data itself or a tensor that overlaps none, of out_dtype: dtype or F32
+ *   norm      device fp32; written by llmint8_grad_norm, read by llmint8_grad_clip
+ *   max_norm  > 0 (infinity: scaled only, whatever the norm); scale > 0, finite
+ *   workspace llmint8_grad_norm_workspace_bytes(grads, count) bytes, 256-byte aligned
+ */
+typedef struct {
+  const void* data;
+  void* out;
+  int64_t n;
+  int dtype, out_dtype;
+} llmint8_grad;
+
+LLMINT8_API size_t llmint8_grad_norm_workspace_bytes(const llmint8_grad* grads, int64_t count);
+LLMINT8_API llmint8_status llmint8_grad_norm(const llmint8_grad* grads, int64_t count, double scale,
+                                             float* norm, void* workspace, size_t workspace_bytes,
+                                             void* stream);
+LLMINT8_API llmint8_status llmint8_grad_clip(const llmint8_grad* grads, int64_t count, const float* norm,
+                                             double max_norm, double scale, void* stream);
+
 /* Largest T the fused GEMV route accepts for this K (0 if none). */
 LLMINT8_API int llmint8_gemv_max_rows(int64_t K);
 

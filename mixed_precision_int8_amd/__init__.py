@@ -29,6 +29,10 @@ __all__ = [
     "KVCache", "KVBatch", "llmint8_rope_table", "rope_frequencies", "llmint8_kv_append",
     "llmint8_kv_gather", "llmint8_kv_attention", "llmint8_kv_attention_workspace_bytes",
     "PagedSequences", "Int8SelfAttention",
+    "PackedRows", "llmint8_attention", "llmint8_attention_backward",
+    "llmint8_attention_backward_workspace_bytes", "rope_axes", "llmint8_rope", "llmint8_layer_norm",
+    "llmint8_layer_norm_backward", "llmint8_layer_norm_workspace_bytes", "GradientSet", "llmint8_grad_norm",
+    "llmint8_grad_clip", "packed_attention", "rotary", "layer_norm", "LayerNorm", "clip_grad_norm",
 ]
 
 LLMINT8_PATH_AUTO = 0
@@ -56,6 +60,9 @@ EXPORTED_SYMBOLS = (
     "llmint8_gemm_tile", "llmint8_linear_noalloc", "llmint8_noalloc_scratch_bytes",
     "llmint8_rope_table", "llmint8_kv_append", "llmint8_kv_gather",
     "llmint8_kv_attention_workspace_bytes", "llmint8_kv_attention",
+    "llmint8_attention", "llmint8_attention_backward_workspace_bytes", "llmint8_attention_backward",
+    "llmint8_rope", "llmint8_layer_norm", "llmint8_layer_norm_workspace_bytes", "llmint8_layer_norm_backward",
+    "llmint8_grad_norm_workspace_bytes", "llmint8_grad_norm", "llmint8_grad_clip",
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -161,6 +168,7 @@ def load_library():
     lib.llmint8_kv_attention.argtypes = [_vp, _vp, ctypes.c_int, *rows, _i64, ctypes.c_float, ctypes.c_int,
                                          _i64, _i64, *rows, _vp, _vp, ctypes.c_size_t, _vp]
     lib.llmint8_kv_attention.restype = ctypes.c_int
+    _training.bind(lib)
     lib.llmint8_gemv_max_rows.argtypes = [_i64]
     lib.llmint8_gemv_max_rows.restype = ctypes.c_int
     lib.llmint8_status_string.argtypes = [ctypes.c_int]
@@ -837,3 +845,8 @@ class Int8Linear:
 from .kvcache import (  # noqa: E402 - the submodule uses the loader above
     Int8SelfAttention, KVBatch, KVCache, PagedSequences, llmint8_kv_append, llmint8_kv_attention,
     llmint8_kv_attention_workspace_bytes, llmint8_kv_gather, llmint8_rope_table, rope_frequencies)
+from . import training as _training  # noqa: E402
+from .training import (  # noqa: E402
+    GradientSet, LayerNorm, PackedRows, clip_grad_norm, layer_norm, llmint8_attention, llmint8_attention_backward,
+    llmint8_attention_backward_workspace_bytes, llmint8_grad_clip, llmint8_grad_norm, llmint8_layer_norm,
+    llmint8_layer_norm_backward, llmint8_layer_norm_workspace_bytes, llmint8_rope, packed_attention, rope_axes, rotary)

@@ -1,0 +1,192 @@
+// Attention over packed sequences on gfx950, forward: o = softmax(scale q k^T) v of
+// each sequence's rows over its own tokens, with grouped heads, causal masks,
+// sliding windows and sinks, or none.
+//
+// A workgroup takes 128 rows of a sequence and key/value head (tokens times the
+// group's query heads, so that a tile of k and v serves all of them), 32 to a
+// wavefront, and goes over the tokens in tiles of 64, the next one on its way to
+// the other half of LDS while one is computed:
+//   S^T = K . q^T    A = 32 tokens x 16 channels from LDS, B = q in registers
+//   O^T = V^T . P^T  A = 32 channels x 16 tokens from LDS, transposed by the read,
+//                    B = the weights, in the lane that computed them
+// Softmax over the tiles with a running maximum m, left where it is until a tile
+// exceeds it by 2^7: w = exp2(u - m + 8) is at most 2^15, so that in fp16 weights
+// down to 2^-32 of the largest count. Statistics and sums are fp32, a weight is
+// rounded to the inputs' type (2^-11 or 2^-8 of itself at most) for the product.
+#include <type_traits>
+
+#include "attn_common.h"
+
+namespace llmint8 {
+
+template <int DP, bool BF16>
+__global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_attention(AttnArgs a) {
+  using Tile = AttnTile<DP>;
+  constexpr int W = 4, kRows = 32 * W, NQ = Tile::NQ, ND = Tile::ND;
+  __shared__ __attribute__((aligned(1024))) char smem[4 * Tile::kBytes];  // k, v; two stages
+  __shared__ int sh[4];
+  const int D = a.dim, H = a.heads, G = a.q_heads / H;
+  const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
+  const int hf = lane >> 5, nn = lane & 31;
+  // the last rows of a sequence see the most: they start first
+  const int h = (int)(blockIdx.x % H), item = (int)((gridDim.x - 1 - blockIdx.x) / H);
+  AttnSeq sq;
+  int run;
+  if (!attn_find<64 * W>(a, item, G, 7, sh, &sq, &run)) return;
+  const int64_t rows = (int64_t)sq.n * G, row0 = (int64_t)run * kRows;
+  if (row0 >= rows) return;
+  const int r = (int)min(row0 + wave * 32 + nn, rows - 1);
+  const int pos = r / G, qh = h * G + (r - pos * G);
+  const int64_t qrow = (int64_t)sq.row0 + pos;
+  const int pos_lo = (int)row0 / G, pos_hi = (int)(min(row0 + kRows, rows) - 1) / G;
+
+  // tiles that any of the rows sees
+  const int end = a.causal ? pos_hi + 1 : sq.n;
+  const int hi = (end + 63) >> 6;
+  const int lo = a.window > 0 ? min(max(pos_lo - a.window + 1, 0) >> 6, hi) : 0;
+  const int sink = a.window > 0 ? min((int)(((int64_t)a.sinks + 63) >> 6), lo) : 0;
+  const int tiles = sink + hi - lo;
+  auto base_of = [&](int i) { return (i < sink ? i : lo + i - sink) << 6; };
+
+  const AttnCopy<DP, W> ck(a.k.token, D), cv(a.v.token, D);
+  const uint16_t* kp = a.k.p + (int64_t)sq.row0 * a.k.token + (int64_t)h * a.k.head;
+  const uint16_t* vp = a.v.p + (int64_t)sq.row0 * a.v.token + (int64_t)h * a.v.head;
+  auto copy = [&](int i, auto stage) {
+    ck.issue(kp, a.k.token, base_of(i), sq.n, smem + stage * 2 * Tile::kBytes);
+    cv.issue(vp, a.v.token, base_of(i), sq.n, smem + (stage * 2 + 1) * Tile::kBytes);
+  };
+  constexpr std::integral_constant<int, 0> kEven;
+  constexpr std::integral_constant<int, 1> kOdd;
+  copy(0, kEven);
+
+  uint4 q[NQ];
+  {
+    const uint16_t* qp = a.q.p + qrow * a.q.token + (int64_t)qh * a.q.head;
+    const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
+#pragma unroll
+    for (int ks = 0; ks < NQ; ++ks) {
+      const int c0 = ks * 16 + hf * 8;
+      q[ks] = make_uint4(0, 0, 0, 0);
+      if (c0 < D) {
+        q[ks] = *reinterpret_cast<const uint4*>(qp + c0);
+        q[ks] = make_uint4(q[ks].x ^ flip, q[ks].y ^ flip, q[ks].z ^ flip, q[ks].w ^ flip);
+      }
+    }
+  }
+  // u = s f; never zero, so that a masked logit stays -infinity
+  const float f = fmaxf(fabsf(a.scale) * 1.44269504088896341f, 1e-37f);
+
+  v16f_t acc[ND];
+#pragma unroll
+  for (int d = 0; d < ND; ++d) acc[d] = attn_zero();
+  float m_run = kAttnNegInf, l_run = 0.0f;  // l_run: of this lane's tokens
+  const int all_end = a.causal ? min(pos_lo, sq.n - 1) : sq.n - 1;
+  const int all_begin = a.window > 0 ? pos_hi - a.window + 1 : 0;
+  const AttnRead<DP> rd;
+  const AttnSees sees(a, pos, sq.n);
+
+  auto tile = [&](int i, auto here, auto there) {
+    attn_wait_copies();
+    __syncthreads();
+    if (i + 1 < tiles) copy(i + 1, there);
+    const char* tk = smem + here * 2 * Tile::kBytes;
+    const char* tv = tk + Tile::kBytes;
+    v16f_t s[2];
+#pragma unroll
+    for (int st = 0; st < NQ; ++st)
+#pragma unroll
+      for (int sb = 0; sb < 2; ++sb)
+        s[sb] = Act16<BF16>::mma32(rd.rows(tk, sb, st), q[st], st == 0 ? attn_zero() : s[sb]);
+    const int base = base_of(i);
+    const bool masked = base + 63 > all_end || base < all_begin;
+    // a lane's values 8 k .. 8 k + 7 are tokens 16 k + 8 hf .. of the tile
+    if (masked) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (!sees(base + 16 * k + 8 * hf + j)) s[k >> 1][(k & 1) * 8 + j] = kAttnNegInf;
+    }
+    float mt = kAttnNegInf;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) mt = fmaxf(mt, fmaxf(s[0][j], s[1][j]));
+    mt = attn_pair_max(mt) * f;
+    // a row that has outgrown its maximum: what was summed moves to the new one (its own row
+    // decides, so that results do not depend on the rows beside it)
+    if (__any(mt > m_run + 7.0f)) {
+      const float m_new = mt > m_run + 7.0f ? mt : m_run;
+      const float alpha = m_run == kAttnNegInf ? 0.0f : __builtin_amdgcn_exp2f(m_run - m_new);
+      m_run = m_new;
+      l_run *= alpha;
+#pragma unroll
+      for (int d = 0; d < ND; ++d) acc[d] *= alpha;
+    }
+    const float off = m_run == kAttnNegInf ? 0.0f : 8.0f - m_run;
+    uint4 p[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        w[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k >> 1][(k & 1) * 8 + j], f, off));
+        l_run += w[j];
+      }
+      p[k] = make_uint4(Act16<BF16>::pack2(w[0], w[1]), Act16<BF16>::pack2(w[2], w[3]),
+                        Act16<BF16>::pack2(w[4], w[5]), Act16<BF16>::pack2(w[6], w[7]));
+    }
+    if (masked) {
+      uint32_t odd = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+          acc[d] = Act16<BF16>::mma32(attn_finite<BF16>(rd.channels(tv, d, k), &odd), p[k], acc[d]);
+      if (__builtin_expect(__any(odd != 0), 0))
+        attn_others<DP, BF16>(acc, tv, [&](int t) { return sees(base + t); });
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int d = 0; d < ND; ++d) acc[d] = Act16<BF16>::mma32(rd.channels(tv, d, k), p[k], acc[d]);
+    }
+  };
+  for (int i = 0; i < tiles; i += 2) {
+    tile(i, kEven, kOdd);
+    if (i + 1 < tiles) tile(i + 1, kOdd, kEven);
+  }
+
+  l_run = attn_pair_sum(l_run);
+  if (row0 + wave * 32 + nn >= rows) return;
+  const float inv = l_run == 0.0f ? 0.0f : 1.0f / l_run;
+  uint16_t* op = a.o.p + qrow * a.o.token + (int64_t)qh * a.o.head;
+#pragma unroll
+  for (int d = 0; d < ND; ++d)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int c = d * 32 + 8 * k + 4 * hf;
+      if (c >= D) continue;
+      *reinterpret_cast<uint2*>(op + c) =
+          make_uint2(Act16<BF16>::pack2(acc[d][4 * k] * inv, acc[d][4 * k + 1] * inv),
+                     Act16<BF16>::pack2(acc[d][4 * k + 2] * inv, acc[d][4 * k + 3] * inv));
+    }
+  if (a.lse && hf == 0)
+    a.lse[qrow * a.q_heads + qh] = l_run == 0.0f ? kAttnNegInf : (m_run - 8.0f + log2f(l_run)) * 0.693147180559945309f;
+}
+
+template <int DP, bool BF16>
+static hipError_t launch_fwd(const AttnArgs& a, hipStream_t stream) {
+  const int64_t items = ((int64_t)a.T * (a.q_heads / a.heads) >> 7) + a.B;
+  const int64_t blocks = items * a.heads;
+  if (blocks > INT32_MAX) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL((ka_attention<DP, BF16>), dim3((unsigned)blocks), dim3(256), 0, stream, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_attention(const AttnArgs& a, bool bf16, hipStream_t stream) {
+  if (a.dim <= 64) return bf16 ? launch_fwd<64, true>(a, stream) : launch_fwd<64, false>(a, stream);
+  if (a.dim <= 96) return bf16 ? launch_fwd<96, true>(a, stream) : launch_fwd<96, false>(a, stream);
+  if (a.dim <= 128) return bf16 ? launch_fwd<128, true>(a, stream) : launch_fwd<128, false>(a, stream);
+  return bf16 ? launch_fwd<256, true>(a, stream) : launch_fwd<256, false>(a, stream);
+}
+
+}  // namespace llmint8

@@ -1,0 +1,49 @@
+// The packed attention's part of internal.h: limits, what the kernels take,
+// launchers. A call's rows are sequences one after the other; every token of a
+// sequence is a row of q, k and v.
+#pragma once
+
+#include "kv_internal.h"
+
+namespace llmint8 {
+
+// Rows and (row, head) pairs are counted in 32 bits; a tile of 64 rows has to lie
+// within a buffer window of 2^31 bytes, so strides are limited as well.
+constexpr int64_t kAttnMaxStride = int64_t(1) << 23;
+inline int admit_attention(int64_t seqs, int64_t rows, int64_t q_heads, int64_t heads, int64_t dim) {
+  if (seqs < 0 || rows < 0 || q_heads <= 0 || heads <= 0 || dim <= 0) return LLMINT8_ERR_INVALID_ARG;
+  if (q_heads % heads != 0) return LLMINT8_ERR_INVALID_ARG;
+  if (dim % 8 != 0 || dim > 256 || heads > 4096 || q_heads > 65536) return LLMINT8_ERR_UNSUPPORTED;
+  if (rows > kKvMax || seqs > (int64_t(1) << 24)) return LLMINT8_ERR_UNSUPPORTED;
+  // workgroups of a launch: ((rows * group) / 128 + seqs) * heads
+  if (rows * q_heads > kKvMaxQRows || (rows * q_heads / 128 + (seqs + 1) * heads) >= kTwo31)
+    return LLMINT8_ERR_UNSUPPORTED;
+  return LLMINT8_OK;
+}
+
+struct AttnArgs {
+  const int32_t* cu;  // [B + 1]
+  int B, T;
+  KvRows q, k, v, o;
+  float* lse;  // [T, q_heads] or null
+  float scale;
+  int q_heads, heads, dim, causal, window, sinks;
+  // backward
+  KvRows d_o, dq, dk, dv;
+  float* stat;  // [2][q_heads][T]: a row's lse in powers of two, and sum do o
+};
+
+// Rows [row0, row0 + n) of sequence b, cut to the call's rows whatever cu holds.
+struct AttnSeq {
+  int row0, n;
+};
+__host__ __device__ inline AttnSeq attn_seq_of(int cu0, int cu1, int T) {
+  cu0 = cu0 < 0 ? 0 : cu0 > T ? T : cu0;
+  cu1 = cu1 < 0 ? 0 : cu1 > T ? T : cu1;
+  return AttnSeq{cu0, cu1 > cu0 ? cu1 - cu0 : 0};
+}
+
+hipError_t launch_attention(const AttnArgs& a, bool bf16, hipStream_t stream);
+hipError_t launch_attention_backward(const AttnArgs& a, bool bf16, hipStream_t stream);
+
+}  // namespace llmint8

@@ -1,0 +1,72 @@
+// Layer norm, rotary positions with axes, and the gradients' norm: what their
+// kernels take, and the launchers.
+#pragma once
+
+#include "attn_internal.h"
+
+namespace llmint8 {
+
+// Element types of these operators, as the ABI numbers them.
+enum : int { kF16 = 0, kF32 = 1, kBF16 = 2 };
+
+constexpr int64_t kNormMaxWidth = 65536;
+struct NormArgs {
+  const void* x;
+  const void* w;  // [K] or null
+  const void* b;  // [K] or null
+  void* y;
+  float* stats;  // [rows, 2]: mean, 1 / sqrt(var + eps); forward: or null
+  int64_t rows, x_row, y_row;
+  int K;
+  float eps;
+  // backward: y is dx
+  const void* dy;
+  int64_t dy_row;
+  void* dw;  // or null
+  void* db;  // or null
+  float* parts;  // [groups][2][K]
+  int groups;
+};
+// Workgroups of the backward pass, each of which leaves one row of partial sums.
+int norm_groups(int64_t rows, int64_t K, int num_cus);
+hipError_t launch_norm(const NormArgs& a, int type, int w_type, hipStream_t stream);
+hipError_t launch_norm_backward(const NormArgs& a, int type, int w_type, hipStream_t stream);
+hipError_t launch_norm_join(const NormArgs& a, int w_type, hipStream_t stream);  // dw and db from the groups' sums
+
+constexpr int kRopeMaxAxes = 8;
+struct RopeArgs {
+  KvRows x[2], y[2];  // second: heads[1] = 0 if there is none
+  int heads[2];
+  const int32_t* pos;  // [rows, axes]
+  const float* table;  // [table_rows, rot]
+  int64_t rows;
+  int axes, table_rows, dim, rot, interleaved, copy;  // copy: the channels that do not turn are copied
+  float sign;                                         // of the angles
+  uint8_t axis[kRopeMaxPairs];
+};
+hipError_t launch_rope(const RopeArgs& a, bool bf16, int num_cus, hipStream_t stream);
+
+// Gradients: `kGradBatch` tensors to a launch, as its arguments. A workgroup takes
+// `chunk` values of one; tensor t's workgroups begin at `start`. One entry is 32 bytes
+// for all that is read of a tensor: beside an array of bytes indexed by the tensor the
+// compiler has split 8 t into t and 7 t for a scalar load of an address, and scalar
+// loads drop the lowest two bits of each.
+constexpr int kGradBatch = 120;
+struct GradItem {
+  const void* p;
+  void* out;
+  int64_t n;
+  int start;
+  int types;  // type | out_type << 8
+};
+struct GradBatch {
+  GradItem item[kGradBatch];
+  int count, chunk;
+  int blocks;  // of all the items
+};
+static_assert(sizeof(GradItem) == 32 && sizeof(GradBatch) + 32 <= 4096, "a launch's arguments");
+hipError_t launch_grad_squares(const GradBatch& g, double* parts, hipStream_t stream);
+hipError_t launch_grad_norm(const double* parts, int64_t n, double scale, float* norm, hipStream_t stream);
+hipError_t launch_grad_scale(const GradBatch& g, const float* norm, double max_norm, double scale, hipStream_t stream);
+
+}  // namespace llmint8

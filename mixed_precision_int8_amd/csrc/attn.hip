@@ -51,13 +51,11 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_attention(AttnArgs 
   const AttnCopy<DP, W> ck(a.k.token, D), cv(a.v.token, D);
   const uint16_t* kp = a.k.p + (int64_t)sq.row0 * a.k.token + (int64_t)h * a.k.head;
   const uint16_t* vp = a.v.p + (int64_t)sq.row0 * a.v.token + (int64_t)h * a.v.head;
-  auto copy = [&](int i, auto stage) {
+  auto copy = [&](int i, int stage) {
     ck.issue(kp, a.k.token, base_of(i), sq.n, smem + stage * 2 * Tile::kBytes);
     cv.issue(vp, a.v.token, base_of(i), sq.n, smem + (stage * 2 + 1) * Tile::kBytes);
   };
-  constexpr std::integral_constant<int, 0> kEven;
-  constexpr std::integral_constant<int, 1> kOdd;
-  copy(0, kEven);
+  copy(0, 0);
 
   uint4 q[NQ];
   {
@@ -82,23 +80,37 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_attention(AttnArgs 
   float m_run = kAttnNegInf, l_run = 0.0f;  // l_run: of this lane's tokens
   const int all_end = a.causal ? min(pos_lo, sq.n - 1) : sq.n - 1;
   const int all_begin = a.window > 0 ? pos_hi - a.window + 1 : 0;
-  const AttnRead<DP> rd;
+  AttnRead<DP> rd(smem);
   const AttnSees sees(a, pos, sq.n);
 
-  auto tile = [&](int i, auto here, auto there) {
+  for (int i = 0; i < tiles; ++i) {
+    const int stage = i & 1, base = base_of(i);
+    const bool masked = base + 63 > all_end || base < all_begin;
     attn_wait_copies();
     __syncthreads();
-    if (i + 1 < tiles) copy(i + 1, there);
-    const char* tk = smem + here * 2 * Tile::kBytes;
-    const char* tv = tk + Tile::kBytes;
+    bool odd = false;
+    if (masked) odd = attn_finite<DP, BF16, W>(smem + (stage * 2 + 1) * Tile::kBytes);
+    if (i + 1 < tiles) copy(i + 1, stage ^ 1);
+
+    // operands are read two steps ahead of their products
+    uint4 x[3][2];
+#pragma unroll
+    for (int st = 0; st < 2; ++st)
+#pragma unroll
+      for (int sb = 0; sb < 2; ++sb) x[st][sb] = rd.rows(0, sb, st);
     v16f_t s[2];
 #pragma unroll
-    for (int st = 0; st < NQ; ++st)
+    for (int st = 0; st < NQ; ++st) {
 #pragma unroll
-      for (int sb = 0; sb < 2; ++sb)
-        s[sb] = Act16<BF16>::mma32(rd.rows(tk, sb, st), q[st], st == 0 ? attn_zero() : s[sb]);
-    const int base = base_of(i);
-    const bool masked = base + 63 > all_end || base < all_begin;
+      for (int sb = 0; sb < 2; ++sb) {
+        if (st + 2 < NQ) x[(st + 2) % 3][sb] = rd.rows(0, sb, st + 2);
+        s[sb] = Act16<BF16>::mma32(x[st % 3][sb], q[st], st == 0 ? attn_zero() : s[sb]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    uint4 y[2][ND];
+#pragma unroll
+    for (int d = 0; d < ND; ++d) y[0][d] = rd.channels(1, d, 0);
     // a lane's values 8 k .. 8 k + 7 are tokens 16 k + 8 hf .. of the tile
     if (masked) {
 #pragma unroll
@@ -107,9 +119,9 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_attention(AttnArgs 
         for (int j = 0; j < 8; ++j)
           if (!sees(base + 16 * k + 8 * hf + j)) s[k >> 1][(k & 1) * 8 + j] = kAttnNegInf;
     }
-    float mt = kAttnNegInf;
+    float mt = s[0][0];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) mt = fmaxf(mt, fmaxf(s[0][j], s[1][j]));
+    for (int j = 0; j < 16; ++j) mt = attn_max(mt, s[0][j], s[1][j]);
     mt = attn_pair_max(mt) * f;
     // a row that has outgrown its maximum: what was summed moves to the new one (its own row
     // decides, so that results do not depend on the rows beside it)
@@ -122,37 +134,27 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_attention(AttnArgs 
       for (int d = 0; d < ND; ++d) acc[d] *= alpha;
     }
     const float off = m_run == kAttnNegInf ? 0.0f : 8.0f - m_run;
-    uint4 p[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
+      if (k < 3) {
+#pragma unroll
+        for (int d = 0; d < ND; ++d) y[(k + 1) & 1][d] = rd.channels(1, d, k + 1);
+      }
       float w[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         w[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k >> 1][(k & 1) * 8 + j], f, off));
         l_run += w[j];
       }
-      p[k] = make_uint4(Act16<BF16>::pack2(w[0], w[1]), Act16<BF16>::pack2(w[2], w[3]),
-                        Act16<BF16>::pack2(w[4], w[5]), Act16<BF16>::pack2(w[6], w[7]));
+      const uint4 p = make_uint4(Act16<BF16>::pack2(w[0], w[1]), Act16<BF16>::pack2(w[2], w[3]),
+                                 Act16<BF16>::pack2(w[4], w[5]), Act16<BF16>::pack2(w[6], w[7]));
+#pragma unroll
+      for (int d = 0; d < ND; ++d) acc[d] = Act16<BF16>::mma32(y[k & 1][d], p, acc[d]);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    if (masked) {
-      uint32_t odd = 0;
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-#pragma unroll
-        for (int d = 0; d < ND; ++d)
-          acc[d] = Act16<BF16>::mma32(attn_finite<BF16>(rd.channels(tv, d, k), &odd), p[k], acc[d]);
-      if (__builtin_expect(__any(odd != 0), 0))
-        attn_others<DP, BF16>(acc, tv, [&](int t) { return sees(base + t); });
-    } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-#pragma unroll
-        for (int d = 0; d < ND; ++d) acc[d] = Act16<BF16>::mma32(rd.channels(tv, d, k), p[k], acc[d]);
-    }
-  };
-  for (int i = 0; i < tiles; i += 2) {
-    tile(i, kEven, kOdd);
-    if (i + 1 < tiles) tile(i + 1, kOdd, kEven);
+    if (__builtin_expect(odd, 0))
+      attn_others<DP, BF16>(acc, vp, a.v.token, base, sq.n, D, [&](int t) { return sees(base + t); });
+    rd.next(stage ? -2 * Tile::kBytes : 2 * Tile::kBytes);
   }
 
   l_run = attn_pair_sum(l_run);

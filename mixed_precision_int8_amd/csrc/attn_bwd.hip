@@ -25,9 +25,12 @@ namespace {
 template <bool BF16, int ND>
 struct Reach {
   float g = BF16 ? 1.0f : 8.507059173023462e37f;  // 2^126
-  // `top`: the largest |dS| of this lane's part of the column
-  __device__ __forceinline__ void fit(float top, v16f_t (&acc)[ND]) {
+  // t: this lane's part of the column
+  __device__ __forceinline__ void fit(const v16f_t& t, v16f_t (&acc)[ND]) {
     if constexpr (!BF16) {
+      float top = 0.0f;
+#pragma unroll
+      for (int x = 0; x < 16; ++x) top = fmaxf(top, fabsf(t[x]));
       top = attn_pair_max(top);
       if (__any(top * g > 32768.0f)) {
         if (top * g > 32768.0f) {
@@ -43,8 +46,13 @@ struct Reach {
   }
 };
 
-constexpr std::integral_constant<int, 0> kEven;
-constexpr std::integral_constant<int, 1> kOdd;
+// values 8 k .. 8 k + 7 as an operand
+template <bool BF16>
+__device__ __forceinline__ uint4 attn_pack(const v16f_t& t, int k) {
+  using A = Act16<BF16>;
+  return make_uint4(A::pack2(t[8 * k], t[8 * k + 1]), A::pack2(t[8 * k + 2], t[8 * k + 3]),
+                    A::pack2(t[8 * k + 4], t[8 * k + 5]), A::pack2(t[8 * k + 6], t[8 * k + 7]));
+}
 
 }  // namespace
 
@@ -79,11 +87,11 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_dq(AttnArgs a) {
   const AttnCopy<DP, W> ck(a.k.token, D), cv(a.v.token, D);
   const uint16_t* kp = a.k.p + (int64_t)sq.row0 * a.k.token + (int64_t)h * a.k.head;
   const uint16_t* vp = a.v.p + (int64_t)sq.row0 * a.v.token + (int64_t)h * a.v.head;
-  auto copy = [&](int i, auto stage) {
+  auto copy = [&](int i, int stage) {
     ck.issue(kp, a.k.token, base_of(i), sq.n, smem + stage * 2 * Tile::kBytes);
     cv.issue(vp, a.v.token, base_of(i), sq.n, smem + (stage * 2 + 1) * Tile::kBytes);
   };
-  copy(0, kEven);
+  copy(0, 0);
 
   uint4 q[NQ], g[NQ];
   float delta = 0.0f;
@@ -126,25 +134,24 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_dq(AttnArgs a) {
   Reach<BF16, ND> reach;
   const int all_end = a.causal ? min(pos_lo, sq.n - 1) : sq.n - 1;
   const int all_begin = a.window > 0 ? pos_hi - a.window + 1 : 0;
-  const AttnRead<DP> rd;
+  AttnRead<DP> rd(smem);
   const AttnSees sees(a, pos, sq.n);
 
-  auto tile = [&](int i, auto here, auto there) {
+  for (int i = 0; i < tiles; ++i) {
+    const int stage = i & 1, base = base_of(i);
+    const bool masked = base + 63 > all_end || base < all_begin;
     attn_wait_copies();
     __syncthreads();
-    if (i + 1 < tiles) copy(i + 1, there);
-    const char* tk = smem + here * 2 * Tile::kBytes;
-    const char* tv = tk + Tile::kBytes;
-    const int base = base_of(i);
-    const bool masked = base + 63 > all_end || base < all_begin;
-    uint32_t odd = 0;
+    bool odd = false;
+    if (masked) odd = attn_finite<DP, BF16, W>(smem + stage * 2 * Tile::kBytes);
+    if (i + 1 < tiles) copy(i + 1, stage ^ 1);
 #pragma unroll
     for (int sb = 0; sb < 2; ++sb) {
-      v16f_t s = attn_zero(), t = attn_zero();
+      v16f_t s = attn_rows_product<DP, BF16>(rd, 0, sb, q);
+      v16f_t t = attn_rows_product<DP, BF16>(rd, 1, sb, g);
+      uint4 y[2][ND];
 #pragma unroll
-      for (int st = 0; st < NQ; ++st) s = Act16<BF16>::mma32(rd.rows(tk, sb, st), q[st], s);
-#pragma unroll
-      for (int st = 0; st < NQ; ++st) t = Act16<BF16>::mma32(rd.rows(tv, sb, st), g[st], t);
+      for (int d = 0; d < ND; ++d) y[0][d] = rd.channels(0, d, 2 * sb);
 #pragma unroll
       for (int x = 0; x < 16; ++x) t[x] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x], f, -lse2)) * (t[x] - delta);
       if (masked) {
@@ -153,30 +160,24 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_dq(AttnArgs a) {
           if (!sees(base + 32 * sb + 16 * (x >> 3) + 8 * hf + (x & 7))) t[x] = 0.0f;
       }
       if constexpr (!BF16) {
-        float top = 0.0f;
-#pragma unroll
-        for (int x = 0; x < 16; ++x) top = fmaxf(top, fabsf(t[x]));
-        reach.fit(top, acc);
+        reach.fit(t, acc);
         t *= reach.g;
       }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const uint4 p = make_uint4(Act16<BF16>::pack2(t[8 * k], t[8 * k + 1]), Act16<BF16>::pack2(t[8 * k + 2], t[8 * k + 3]),
-                                   Act16<BF16>::pack2(t[8 * k + 4], t[8 * k + 5]), Act16<BF16>::pack2(t[8 * k + 6], t[8 * k + 7]));
+        if (k == 0) {
 #pragma unroll
-        for (int d = 0; d < ND; ++d) {
-          uint4 x = rd.channels(tk, d, 2 * sb + k);
-          if (masked) x = attn_finite<BF16>(x, &odd);
-          acc[d] = Act16<BF16>::mma32(x, p, acc[d]);
+          for (int d = 0; d < ND; ++d) y[1][d] = rd.channels(0, d, 2 * sb + 1);
         }
+        const uint4 p = attn_pack<BF16>(t, k);
+#pragma unroll
+        for (int d = 0; d < ND; ++d) acc[d] = Act16<BF16>::mma32(y[k][d], p, acc[d]);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
-    if (__builtin_expect(masked && __any(odd != 0), 0))
-      attn_others<DP, BF16>(acc, tk, [&](int t) { return sees(base + t); });
-  };
-  for (int i = 0; i < tiles; i += 2) {
-    tile(i, kEven, kOdd);
-    if (i + 1 < tiles) tile(i + 1, kOdd, kEven);
+    if (__builtin_expect(odd, 0))
+      attn_others<DP, BF16>(acc, kp, a.k.token, base, sq.n, D, [&](int t) { return sees(base + t); });
+    rd.next(stage ? -2 * Tile::kBytes : 2 * Tile::kBytes);
   }
 
   if (!mine) return;
@@ -225,7 +226,7 @@ __global__ __launch_bounds__(256, 1) void ka_dkv(AttnArgs a) {
   const uint16_t* qp = a.q.p + (int64_t)sq.row0 * a.q.token + (int64_t)h * G * a.q.head;
   const uint16_t* gp = a.d_o.p + (int64_t)sq.row0 * a.d_o.token + (int64_t)h * G * a.d_o.head;
   const float* sp = a.stat + (int64_t)h * G * a.T + sq.row0;
-  auto copy = [&](int head, int base, auto stage) {
+  auto copy = [&](int head, int base, int stage) {
     cq.issue(qp + (int64_t)head * a.q.head, a.q.token, base, sq.n, smem + stage * 2 * Tile::kBytes);
     cg.issue(gp + (int64_t)head * a.d_o.head, a.d_o.token, base, sq.n, smem + (stage * 2 + 1) * Tile::kBytes);
     if (wave < 2) {
@@ -234,11 +235,11 @@ __global__ __launch_bounds__(256, 1) void ka_dkv(AttnArgs a) {
     }
   };
   int head = 0, at = lo;  // the tile that is copied next
-  auto next = [&](auto stage) {
+  auto next = [&](int stage) {
     copy(head, at << 6, stage);
     if (++at == lo + per) at = lo, ++head;
   };
-  next(kEven);
+  next(0);
 
   uint4 kr[NQ], vr[NQ];
   {
@@ -263,7 +264,7 @@ __global__ __launch_bounds__(256, 1) void ka_dkv(AttnArgs a) {
 #pragma unroll
   for (int d = 0; d < ND; ++d) ak[d] = av[d] = attn_zero();
   Reach<BF16, ND> reach;
-  const AttnRead<DP> rd;
+  AttnRead<DP> rd(smem);
   // this lane's token is seen by rows i in [j, until) of a causal sequence, all of another
   const int from = a.causal ? col : 0;
   const int until = a.window > 0 && col >= a.sinks ? (int)min((int64_t)sq.n, (int64_t)col + a.window) : sq.n;
@@ -271,27 +272,22 @@ __global__ __launch_bounds__(256, 1) void ka_dkv(AttnArgs a) {
   const int all_from = a.causal ? j_hi : 0;
   const int all_until = a.window > 0 && j_hi >= a.sinks ? max(j0, (int)min((int64_t)a.sinks, (int64_t)j_hi)) + a.window : INT32_MAX;
 
-  int i_at = lo;
-  auto tile = [&](int i, auto here, auto there) {
+  for (int i = 0, i_at = lo, i_head = 0; i < tiles; ++i) {
+    const int stage = i & 1, base = i_at << 6;
+    const bool masked = base < all_from || base + 64 > all_until;
     attn_wait_copies();
     __syncthreads();
-    if (i + 1 < tiles) next(there);
-    const char* tq = smem + here * 2 * Tile::kBytes;
-    const char* tg = tq + Tile::kBytes;
-    const float* st_l = sh_stat + here * 128;
-    const int base = i_at << 6;
-    if (++i_at == lo + per) i_at = lo;
-    const bool masked = base < all_from || base + 64 > all_until;
-    uint32_t odd = 0;
+    bool odd = false;
+    if (masked) {
+      if constexpr (DK) odd = attn_finite<DP, BF16, W>(smem + stage * 2 * Tile::kBytes);
+      if constexpr (DV) odd |= attn_finite<DP, BF16, W>(smem + (stage * 2 + 1) * Tile::kBytes);
+    }
+    if (i + 1 < tiles) next(stage ^ 1);
+    const float* st_l = sh_stat + stage * 128;
 #pragma unroll
     for (int sb = 0; sb < 2; ++sb) {
-      v16f_t s = attn_zero(), t = attn_zero();
-#pragma unroll
-      for (int st = 0; st < NQ; ++st) s = Act16<BF16>::mma32(rd.rows(tq, sb, st), kr[st], s);
-      if constexpr (DK) {
-#pragma unroll
-        for (int st = 0; st < NQ; ++st) t = Act16<BF16>::mma32(rd.rows(tg, sb, st), vr[st], t);
-      }
+      v16f_t s = attn_rows_product<DP, BF16>(rd, 0, sb, kr), t = attn_zero();
+      if constexpr (DK) t = attn_rows_product<DP, BF16>(rd, 1, sb, vr);
 #pragma unroll
       for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -315,45 +311,32 @@ __global__ __launch_bounds__(256, 1) void ka_dkv(AttnArgs a) {
         }
       }
       if constexpr (DK && !BF16) {
-        float top = 0.0f;
-#pragma unroll
-        for (int x = 0; x < 16; ++x) top = fmaxf(top, fabsf(t[x]));
-        reach.fit(top, ak);
+        reach.fit(t, ak);
         t *= reach.g;
       }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         if constexpr (DV) {
-          const uint4 p = make_uint4(Act16<BF16>::pack2(s[8 * k], s[8 * k + 1]), Act16<BF16>::pack2(s[8 * k + 2], s[8 * k + 3]),
-                                     Act16<BF16>::pack2(s[8 * k + 4], s[8 * k + 5]), Act16<BF16>::pack2(s[8 * k + 6], s[8 * k + 7]));
+          const uint4 p = attn_pack<BF16>(s, k);
 #pragma unroll
-          for (int d = 0; d < ND; ++d) {
-            uint4 x = rd.channels(tg, d, 2 * sb + k);
-            if (masked) x = attn_finite<BF16>(x, &odd);
-            av[d] = Act16<BF16>::mma32(x, p, av[d]);
-          }
+          for (int d = 0; d < ND; ++d) av[d] = Act16<BF16>::mma32(rd.channels(1, d, 2 * sb + k), p, av[d]);
         }
         if constexpr (DK) {
-          const uint4 p = make_uint4(Act16<BF16>::pack2(t[8 * k], t[8 * k + 1]), Act16<BF16>::pack2(t[8 * k + 2], t[8 * k + 3]),
-                                     Act16<BF16>::pack2(t[8 * k + 4], t[8 * k + 5]), Act16<BF16>::pack2(t[8 * k + 6], t[8 * k + 7]));
+          const uint4 p = attn_pack<BF16>(t, k);
 #pragma unroll
-          for (int d = 0; d < ND; ++d) {
-            uint4 x = rd.channels(tq, d, 2 * sb + k);
-            if (masked) x = attn_finite<BF16>(x, &odd);
-            ak[d] = Act16<BF16>::mma32(x, p, ak[d]);
-          }
+          for (int d = 0; d < ND; ++d) ak[d] = Act16<BF16>::mma32(rd.channels(0, d, 2 * sb + k), p, ak[d]);
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
-    if (__builtin_expect(masked && __any(odd != 0), 0)) {
+    if (__builtin_expect(odd, 0)) {
       auto see = [&](int t) { return (base + t >= from) & (base + t < until); };
-      if constexpr (DV) attn_others<DP, BF16>(av, tg, see);
-      if constexpr (DK) attn_others<DP, BF16>(ak, tq, see);
+      if constexpr (DV)
+        attn_others<DP, BF16>(av, gp + (int64_t)i_head * a.d_o.head, a.d_o.token, base, sq.n, D, see);
+      if constexpr (DK) attn_others<DP, BF16>(ak, qp + (int64_t)i_head * a.q.head, a.q.token, base, sq.n, D, see);
     }
-  };
-  for (int i = 0; i < tiles; i += 2) {
-    tile(i, kEven, kOdd);
-    if (i + 1 < tiles) tile(i + 1, kOdd, kEven);
+    if (++i_at == lo + per) i_at = lo, ++i_head;
+    rd.next(stage ? -2 * Tile::kBytes : 2 * Tile::kBytes);
   }
 
   if (col >= sq.n) return;

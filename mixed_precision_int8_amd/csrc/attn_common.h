@@ -12,9 +12,14 @@
 // so that a lane's 16 results are rows 8 hf .. 8 hf + 7 of each sixteen: as they
 // stand, operand B of the next product, which sums over these rows.
 //
-// 16-byte chunks of a row are stored at chunk ^ swizzle(row): 16 rows' reads at one
-// chunk fall on all 64 banks, and so do the four rows x 32 bytes that a
-// transposing read takes for 16 lanes.
+// Rows of 16 are laid out so that the 16-byte reads of 16 rows at one chunk fall on all 64
+// banks, and so do the four rows x 32 bytes that a transposing read takes for 16 lanes:
+// chunks are stored at chunk ^ 2 (row % 4) and every four rows begin 16, 128 or 144 bytes
+// later (rows of 128 bytes: chunk ^ 2 (row / 2 % 4), 16 bytes later every eight rows). The
+// exclusive or touches three bits of a chunk's number, so that four addresses to a lane
+// serve all "rows" operands and two all "channels" operands: the rest of an address is a
+// constant of the instruction. (With the usual one over all bits each step had an address
+// of its own; the 128-channel kernels spilled 90 registers.)
 #pragma once
 
 #include "attn_internal.h"
@@ -28,12 +33,17 @@ template <int DP>
 struct AttnTile {
   static constexpr int kPitch = DP <= 64 ? 128 : DP <= 128 ? 256 : 512;  // bytes of a row
   static constexpr int kChunks = kPitch / 16;
-  static constexpr int kBytes = 64 * kPitch;
+  static constexpr bool kNarrow = kPitch == 128;
+  static constexpr int kSixteen = 16 * kPitch + (kNarrow ? 32 : 256);  // bytes of 16 rows
+  static constexpr int kBytes = 4 * kSixteen;
   static constexpr int NQ = DP / 16;  // 16-channel steps
   static constexpr int ND = DP / 32;  // 32-channel blocks
-  static __device__ __forceinline__ int swizzle(int row) {
-    if constexpr (kPitch == 128) return ((row >> 1) & 3) << 1 | ((row >> 3) & 1);
-    return (row & 7) << 1 | ((row >> 3) & 1);
+  static __device__ __forceinline__ constexpr int swizzle(int row) {
+    return kNarrow ? ((row >> 1) & 3) << 1 : (row & 3) << 1;
+  }
+  static __device__ __forceinline__ constexpr int at(int row) {
+    const int pad = kNarrow ? (row >> 3 & 1) * 16 : (row >> 2 & 1) * 16 + (row >> 3 & 1) * 128;
+    return (row >> 4) * kSixteen + (row & 15) * kPitch + pad;
   }
 };
 
@@ -47,63 +57,66 @@ __device__ __forceinline__ void attn_copy4(__amdgpu_buffer_rsrc_t r, float* to, 
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 4, off, 0, 0, 0);
 }
 
-// A matrix of rows in memory: the window that starts at a row, and the offsets at
-// which this thread's copies of a tile stand in it.
+// A matrix of rows in memory: the offset at which this thread's copies of a tile begin.
 template <int DP, int W>
 struct AttnCopy {
   using Tile = AttnTile<DP>;
-  static constexpr int kIssues = Tile::kBytes / 1024 / W;  // of 1 KB to a wavefront and tile
-  uint32_t off[kIssues];
+  static constexpr int kIssues = 64 * Tile::kPitch / 1024 / W;  // of 1 KB to a wavefront and tile
+  static constexpr int kRows = 1024 / Tile::kPitch;             // of an issue
+  static_assert(kRows * W % 4 == 0, "the rows of a thread's issues have one swizzle");
+  uint32_t off, step;
   __device__ __forceinline__ AttnCopy(int64_t token, int dim) {
     const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
-#pragma unroll
-    for (int i = 0; i < kIssues; ++i) {
-      const int at = (i * W + wave) * 64 + lane;
-      const int row = at / Tile::kChunks, chunk = at % Tile::kChunks ^ Tile::swizzle(row);
-      off[i] = chunk * 8 < dim ? (uint32_t)(row * (int)token * 2 + chunk * 16) : kOobOffset;
-    }
+    const int row = wave * kRows + lane / Tile::kChunks, chunk = lane % Tile::kChunks ^ Tile::swizzle(row);
+    off = chunk * 8 < dim ? (uint32_t)(row * (int)token * 2 + chunk * 16) : kOobOffset;
+    step = (uint32_t)(kRows * W * (int)token * 2);
   }
-  // rows [first, first + 64) of `rows` (an address and its row count) into LDS at `to`
+  // rows [first, first + 64) of the n at p into LDS at `to`; those from n on are zeros
   __device__ __forceinline__ void issue(const uint16_t* p, int64_t token, int first, int n, char* to) const {
     const int wave = uniform((int)threadIdx.x >> 6);
     const int left = min(n - first, 64);
     const __amdgpu_buffer_rsrc_t r = make_rsrc(p + (int64_t)first * token, (uint32_t)(max(left, 0) * (int)token * 2));
 #pragma unroll
-    for (int i = 0; i < kIssues; ++i)
-      attn_copy16(r, to + (i * W + wave) * 1024, off[i]);
+    for (int i = 0; i < kIssues; ++i) attn_copy16(r, to + Tile::at((i * W + wave) * kRows), off + i * step);
   }
 };
 
 __device__ __forceinline__ void attn_wait_copies() { __builtin_amdgcn_s_waitcnt(0x0f70); }  // vmcnt(0)
 
-// Operands from a tile.
+// Operands from tiles: `tile` is the place of one among the tiles of a workgroup, a
+// constant; the addresses move between its stages (`next`).
 template <int DP>
 struct AttnRead {
   using Tile = AttnTile<DP>;
-  int row_at, row_x, tr_at, tr_x;
-  __device__ __forceinline__ AttnRead() {
+  const char* row[4];
+  const char* tr[2];
+  __device__ __forceinline__ explicit AttnRead(const char* smem) {
     const int lane = threadIdx.x & 63, hf = lane >> 5, nn = lane & 31;
-    const int row = (nn & 0x13) | (nn & 4) << 1 | (nn & 8) >> 1;
-    row_at = row * Tile::kPitch;
-    row_x = (hf ^ Tile::swizzle(row)) * 16;
+    const int r = (nn & 0x13) | (nn & 4) << 1 | (nn & 8) >> 1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) row[i] = smem + Tile::at(r) + ((2 * i + hf) ^ Tile::swizzle(r)) * 16;
     const int i = lane & 15, t = 8 * hf + (i >> 2), c = 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);
-    tr_at = t * Tile::kPitch + 8 * (i & 1);
-    tr_x = (c ^ Tile::swizzle(t)) * 16;
+#pragma unroll
+    for (int d = 0; d < 2; ++d) tr[d] = smem + Tile::at(t) + ((4 * d + c) ^ Tile::swizzle(t)) * 16 + 8 * (i & 1);
+  }
+  __device__ __forceinline__ void next(int by) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) row[i] += by;
+    tr[0] += by;
+    tr[1] += by;
   }
   // rows [32 block, +32) x channels [16 step, +16)
-  __device__ __forceinline__ uint4 rows(const char* tile, int block, int step) const {
-    return *reinterpret_cast<const uint4*>(tile + row_at + (row_x ^ step * 32) + block * 32 * Tile::kPitch);
+  __device__ __forceinline__ uint4 rows(int tile, int block, int step) const {
+    return *reinterpret_cast<const uint4*>(row[step & 3] + (tile * Tile::kBytes + (step >> 2) * 128 + block * 2 * Tile::kSixteen));
   }
   // channels [32 block, +32) x rows [16 step, +16)
-  __device__ __forceinline__ uint4 channels(const char* tile, int block, int step) const {
+  __device__ __forceinline__ uint4 channels(int tile, int block, int step) const {
     typedef short v4s __attribute__((ext_vector_type(4)));
     typedef __attribute__((address_space(3))) v4s* lds_v4s;
-    // four rows on, bit 2 of the row is the swizzle's bit 3 (2 where a row has eight chunks)
-    constexpr int kNext = Tile::kPitch == 128 ? 64 : 128;
-    const int x = tr_x ^ block * 64;
-    const char* p = tile + tr_at + step * 16 * Tile::kPitch;
-    const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(p + x));
-    const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(p + 4 * Tile::kPitch + (x ^ kNext)));
+    const int at = tile * Tile::kBytes + (block >> 1) * 128 + step * Tile::kSixteen;
+    // four rows on, the exclusive or of narrow rows has its bit 2 turned
+    const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(tr[block & 1] + at));
+    const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(tr[(block ^ (int)Tile::kNarrow) & 1] + at + Tile::at(4)));
     const uint2 a = __builtin_bit_cast(uint2, lo), b = __builtin_bit_cast(uint2, hi);
     return make_uint4(a.x, a.y, b.x, b.y);
   }
@@ -175,35 +188,51 @@ struct AttnSees {
   __device__ __forceinline__ bool operator()(int j) const { return (j <= last) & ((j > from) | (j < sinks)); }
 };
 
+// The largest of three, NaN if one of them is (one instruction; fmaxf costs two more, as it
+// takes the other one and quiets its operands first).
+__device__ __forceinline__ float attn_max(float a, float b, float c) {
+  return __builtin_elementwise_maximum(__builtin_elementwise_maximum(a, b), c);
+}
+
 // A product whose weights are exactly zero where a column does not see a row must not
 // take that row's values that are not finite (0 times them is NaN). Where a tile has
-// masked rows its operands pass attn_finite, which zeroes such values and notes that
-// there were any; attn_others then adds them to the sums of the columns that see them.
-template <bool BF16>
-__device__ __forceinline__ uint4 attn_finite(const uint4& x, uint32_t* odd) {
-  constexpr uint32_t kUp = BF16 ? 0x00800080u : 0x04000400u;  // carries an exponent of ones into bit 15
-  uint32_t v[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t bad = ((v[j] & 0x7fff7fffu) + kUp) & 0x80008000u;
-    *odd |= bad;
-    v[j] &= ~((bad >> 15) * 0xffffu);
-  }
-  return make_uint4(v[0], v[1], v[2], v[3]);
-}
-// Rows of the tile go by `see(row)`: whether this lane's column sees that row of the 64.
-template <int DP, bool BF16, class See>
-__device__ __forceinline__ void attn_others(v16f_t (&acc)[DP / 32], const char* tile, See&& see) {
+// masked rows the workgroup zeroes such values in LDS first; if there were any (the
+// result), attn_others adds them, from memory, to the sums of the columns that see them.
+template <int DP, bool BF16, int W>
+__device__ __forceinline__ bool attn_finite(char* tile) {
   using Tile = AttnTile<DP>;
+  constexpr uint32_t kUp = BF16 ? 0x00800080u : 0x04000400u;  // carries an exponent of ones into bit 15
+  uint32_t odd = 0;
+#pragma unroll
+  for (int i = 0; i < 64 * Tile::kChunks / (64 * W); ++i) {
+    const int u = i * 64 * W + (int)threadIdx.x;
+    uint4* at = reinterpret_cast<uint4*>(tile + Tile::at(u / Tile::kChunks) + u % Tile::kChunks * 16);
+    const uint4 x = *at;
+    uint32_t v[4] = {x.x, x.y, x.z, x.w}, any = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t bad = ((v[j] & 0x7fff7fffu) + kUp) & 0x80008000u;
+      any |= bad;
+      v[j] &= ~((bad >> 15) * 0xffffu);
+    }
+    if (any) *at = make_uint4(v[0], v[1], v[2], v[3]);
+    odd |= any;
+  }
+  return __syncthreads_or(odd != 0);
+}
+// Rows [first, first + 64) of the n at p; `see(row)`: whether this lane's column sees that
+// row of the 64.
+template <int DP, bool BF16, class See>
+__device__ __forceinline__ void attn_others(v16f_t (&acc)[DP / 32], const uint16_t* p, int64_t token, int first, int n,
+                                            int dim, See&& see) {
   constexpr uint32_t kInf = BF16 ? 0x7f80u : 0x7c00u;
-  const int lane = threadIdx.x & 63, hf = lane >> 5;
+  const int lane = threadIdx.x & 63, hf = lane >> 5, rows = min(n - first, 64);
 #pragma unroll 1
-  for (int t = 0; t < 64; ++t) {
+  for (int t = 0; t < rows; ++t) {
     const bool sees = see(t);
 #pragma unroll 1
-    for (int c0 = 0; c0 < Tile::kPitch / 2; c0 += 64) {
-      const int at = (c0 + lane) >> 3;
-      const uint16_t v = *reinterpret_cast<const uint16_t*>(tile + t * Tile::kPitch + ((at ^ Tile::swizzle(t)) * 16) + (lane & 7) * 2);
+    for (int c0 = 0; c0 < dim; c0 += 64) {
+      const uint32_t v = c0 + lane < dim ? p[(int64_t)(first + t) * token + c0 + lane] : 0u;
       uint64_t left = __ballot((v & kInf) == kInf);
       while (left) {
         const int from = __builtin_ctzll(left);
@@ -218,6 +247,23 @@ __device__ __forceinline__ void attn_others(v16f_t (&acc)[DP / 32], const char* 
       }
     }
   }
+}
+
+// s += the tile's rows [32 block, +32) times b, operands read two steps ahead
+template <int DP, bool BF16>
+__device__ __forceinline__ v16f_t attn_rows_product(const AttnRead<DP>& rd, int tile, int block, const uint4 (&b)[DP / 16]) {
+  constexpr int NQ = DP / 16, kAhead = 2;
+  uint4 x[kAhead + 1];
+#pragma unroll
+  for (int st = 0; st < kAhead; ++st) x[st] = rd.rows(tile, block, st);
+  v16f_t s;
+#pragma unroll
+  for (int st = 0; st < NQ; ++st) {
+    if (st + kAhead < NQ) x[(st + kAhead) % (kAhead + 1)] = rd.rows(tile, block, st + kAhead);
+    s = Act16<BF16>::mma32(x[st % (kAhead + 1)], b[st], st == 0 ? attn_zero() : s);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  return s;
 }
 
 }  // namespace llmint8

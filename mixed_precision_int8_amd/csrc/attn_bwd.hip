@@ -46,14 +46,6 @@ struct Reach {
   }
 };
 
-// values 8 k .. 8 k + 7 as an operand
-template <bool BF16>
-__device__ __forceinline__ uint4 attn_pack(const v16f_t& t, int k) {
-  using A = Act16<BF16>;
-  return make_uint4(A::pack2(t[8 * k], t[8 * k + 1]), A::pack2(t[8 * k + 2], t[8 * k + 3]),
-                    A::pack2(t[8 * k + 4], t[8 * k + 5]), A::pack2(t[8 * k + 6], t[8 * k + 7]));
-}
-
 }  // namespace
 
 template <int DP, bool BF16>
@@ -124,7 +116,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_dq(AttnArgs a) {
   const bool mine = row0 + wave * 32 + nn < rows;
   if (mine && hf == 0) {
     float* st = a.stat + (int64_t)qh * a.T + qrow;
-    st[0] = lse2;
+    st[0] = (BF16 ? 0.0f : 15.0f) - lse2;
     st[(int64_t)a.q_heads * a.T] = delta;
   }
 
@@ -195,26 +187,34 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_dq(AttnArgs a) {
     }
 }
 
-// DV, DK: which of the two it forms (heads of more than 128 channels take a launch for
-// each, as the registers hold one).
-template <int DP, bool BF16, bool DV, bool DK>
-__global__ __launch_bounds__(256, 1) void ka_dkv(AttnArgs a) {
+// Two wavefronts share 32 tokens: one forms S and P and sums dV, the other do V^T and dS
+// (from the first one's P, through LDS) and sums dK, eight wavefronts to a workgroup. A
+// wavefront's vector instructions wait for its matrix instructions here (measured: four of
+// 32x32x16 and 16 multiply-adds take what each takes alone, together, from one wavefront;
+// the longer of the two from two), so that two to a SIMD are what overlaps them, and one
+// wavefront with both sums needs 450 registers and runs alone (1355 us where this takes
+// 840: 15000 tokens of 32/8 heads of 128).
+template <int DP, bool BF16>
+__global__ __launch_bounds__(DP <= 128 ? 512 : 256, DP <= 128 ? 2 : 1) void ka_dkv(AttnArgs a) {
   using Tile = AttnTile<DP>;
-  constexpr int W = 4, kCols = 32 * W, NQ = Tile::NQ, ND = Tile::ND;
-  __shared__ __attribute__((aligned(1024))) char smem[4 * Tile::kBytes];  // q, do; two stages
-  __shared__ __attribute__((aligned(256))) float sh_stat[4 * 64];         // lse, delta; two stages
+  constexpr int kPairs = DP <= 128 ? 4 : 2, W = 2 * kPairs, kCols = 32 * kPairs, NQ = Tile::NQ, ND = Tile::ND;
+  constexpr int kStages = DP <= 128 ? 3 : 2, kStage = 2 * Tile::kBytes;
+  __shared__ __attribute__((aligned(1024))) char smem[kStages * kStage];             // q, do
+  __shared__ __attribute__((aligned(256))) float sh_stat[2 * kStages * 64];          // lse, delta
+  __shared__ __attribute__((aligned(1024))) v4f sh_p[2 * kPairs * 4 * 64];           // P, two steps
   __shared__ int sh[4];
   const int D = a.dim, H = a.heads, G = a.q_heads / H;
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
-  const int hf = lane >> 5, nn = lane & 31;
+  const int hf = lane >> 5, nn = lane & 31, pair = wave % kPairs;
+  const bool second = wave >= kPairs;
   // the first tokens of a sequence are seen by the most: they start first
   const int h = (int)(blockIdx.x % H), item = (int)(blockIdx.x / H);
   AttnSeq sq;
   int run;
-  if (!attn_find<64 * W>(a, item, 1, 7, sh, &sq, &run)) return;
+  if (!attn_find<64 * W>(a, item, 1, kPairs == 4 ? 7 : 6, sh, &sq, &run)) return;
   const int j0 = run * kCols;
   if (j0 >= sq.n) return;
-  const int col = j0 + wave * 32 + nn, j = min(col, sq.n - 1), j_hi = min(j0 + kCols, sq.n) - 1;
+  const int col = j0 + pair * 32 + nn, j = min(col, sq.n - 1), j_hi = min(j0 + kCols, sq.n) - 1;
 
   // rows that see any of the tokens
   const int first = a.causal ? j0 : 0;
@@ -226,153 +226,174 @@ __global__ __launch_bounds__(256, 1) void ka_dkv(AttnArgs a) {
   const uint16_t* qp = a.q.p + (int64_t)sq.row0 * a.q.token + (int64_t)h * G * a.q.head;
   const uint16_t* gp = a.d_o.p + (int64_t)sq.row0 * a.d_o.token + (int64_t)h * G * a.d_o.head;
   const float* sp = a.stat + (int64_t)h * G * a.T + sq.row0;
-  auto copy = [&](int head, int base, int stage) {
-    cq.issue(qp + (int64_t)head * a.q.head, a.q.token, base, sq.n, smem + stage * 2 * Tile::kBytes);
-    cg.issue(gp + (int64_t)head * a.d_o.head, a.d_o.token, base, sq.n, smem + (stage * 2 + 1) * Tile::kBytes);
+  int c_head = 0, c_at = lo, c_stage = 0;  // the tile that is copied next
+  auto copy = [&]() {
+    const int base = c_at << 6;
+    char* to = smem + c_stage * kStage;
+    cq.issue(qp + (int64_t)c_head * a.q.head, a.q.token, base, sq.n, to);
+    cg.issue(gp + (int64_t)c_head * a.d_o.head, a.d_o.token, base, sq.n, to + Tile::kBytes);
     if (wave < 2) {
-      const float* p = sp + (int64_t)head * a.T + base + (wave ? (int64_t)a.q_heads * a.T : 0);
-      attn_copy4(make_rsrc(p, (uint32_t)min(sq.n - base, 64) * 4), sh_stat + (stage * 2 + wave) * 64, (uint32_t)lane * 4);
+      const float* p = sp + (int64_t)c_head * a.T + base + (wave ? (int64_t)a.q_heads * a.T : 0);
+      attn_copy4(make_rsrc(p, (uint32_t)min(sq.n - base, 64) * 4), sh_stat + (c_stage * 2 + wave) * 64, (uint32_t)lane * 4);
     }
+    if (++c_at == lo + per) c_at = lo, ++c_head;
+    if (++c_stage == kStages) c_stage = 0;
   };
-  int head = 0, at = lo;  // the tile that is copied next
-  auto next = [&](int stage) {
-    copy(head, at << 6, stage);
-    if (++at == lo + per) at = lo, ++head;
-  };
-  next(0);
+  copy();
 
-  uint4 kr[NQ], vr[NQ];
+  uint4 kv[NQ];  // k of this lane's token, v in the second wavefront
   {
-    const uint16_t* kp = a.k.p + ((int64_t)sq.row0 + j) * a.k.token + (int64_t)h * a.k.head;
-    const uint16_t* vp = a.v.p + ((int64_t)sq.row0 + j) * a.v.token + (int64_t)h * a.v.head;
-    const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
+    const KvRows& r = second ? a.v : a.k;
+    const uint16_t* p = r.p + ((int64_t)sq.row0 + j) * r.token + (int64_t)h * r.head;
+    const uint32_t flip = !second && a.scale < 0.0f ? 0x80008000u : 0u;
 #pragma unroll
     for (int ks = 0; ks < NQ; ++ks) {
       const int c0 = ks * 16 + hf * 8;
-      kr[ks] = vr[ks] = make_uint4(0, 0, 0, 0);
+      kv[ks] = make_uint4(0, 0, 0, 0);
       if (c0 < D) {
-        kr[ks] = *reinterpret_cast<const uint4*>(kp + c0);
-        kr[ks] = make_uint4(kr[ks].x ^ flip, kr[ks].y ^ flip, kr[ks].z ^ flip, kr[ks].w ^ flip);
-        if constexpr (DK) vr[ks] = *reinterpret_cast<const uint4*>(vp + c0);
+        kv[ks] = *reinterpret_cast<const uint4*>(p + c0);
+        kv[ks] = make_uint4(kv[ks].x ^ flip, kv[ks].y ^ flip, kv[ks].z ^ flip, kv[ks].w ^ flip);
       }
     }
   }
   const float f = fabsf(a.scale) * 1.44269504088896341f;
-  constexpr float kUp = BF16 ? 0.0f : 15.0f;
 
-  v16f_t ak[ND], av[ND];
+  v16f_t acc[ND];  // dV, dK in the second wavefront
 #pragma unroll
-  for (int d = 0; d < ND; ++d) ak[d] = av[d] = attn_zero();
+  for (int d = 0; d < ND; ++d) acc[d] = attn_zero();
   Reach<BF16, ND> reach;
-  AttnRead<DP> rd(smem);
   // this lane's token is seen by rows i in [j, until) of a causal sequence, all of another
   const int from = a.causal ? col : 0;
   const int until = a.window > 0 && col >= a.sinks ? (int)min((int64_t)sq.n, (int64_t)col + a.window) : sq.n;
   // tiles that begin from here on and end before there are seen whole by all columns
   const int all_from = a.causal ? j_hi : 0;
   const int all_until = a.window > 0 && j_hi >= a.sinks ? max(j0, (int)min((int64_t)a.sinks, (int64_t)j_hi)) + a.window : INT32_MAX;
+  // once a tile's copies are there for all: the values that no masked product may meet
+  auto clean = [&](int stage, int base, bool* masked) {
+    *masked = base < all_from || base + 64 > all_until;
+    if (!*masked) return false;
+    const bool q_odd = attn_finite<DP, BF16, W>(smem + stage * kStage);
+    return attn_finite<DP, BF16, W>(smem + stage * kStage + Tile::kBytes) || q_odd;
+  };
 
-  for (int i = 0, i_at = lo, i_head = 0; i < tiles; ++i) {
-    const int stage = i & 1, base = i_at << 6;
-    const bool masked = base < all_from || base + 64 > all_until;
-    attn_wait_copies();
-    __syncthreads();
-    bool odd = false;
-    if (masked) {
-      if constexpr (DK) odd = attn_finite<DP, BF16, W>(smem + stage * 2 * Tile::kBytes);
-      if constexpr (DV) odd |= attn_finite<DP, BF16, W>(smem + (stage * 2 + 1) * Tile::kBytes);
-    }
-    if (i + 1 < tiles) next(stage ^ 1);
-    const float* st_l = sh_stat + stage * 128;
+  // the first wavefront's products are q's rows and do's channels, the second's the others
+  AttnRead<DP> rd(smem);
+  rd.next_rows(second ? Tile::kBytes : 0);
+  rd.next_channels(second ? 0 : Tile::kBytes);
+  v4f* const p_mine = sh_p + pair * 256 + lane;
+  const float* const st_mine = sh_stat + (second ? 64 : 0) + 8 * hf;
+  attn_wait_copies();
+  __syncthreads();
+  int base = lo << 6, i_at = lo, i_head = 0, stage = 0;
+  bool masked;
+  bool odd = clean(0, base, &masked);
+  if (kStages > 2 && tiles > 1) copy();
+  // Operands are read a phase ahead: a step's channels during the products of its rows,
+  // the next step's rows during those of its channels.
+  static_assert(NQ == 2 * ND, "a step has as many products of rows as of channels");
+  uint4 xr[NQ], xc[NQ];
+#pragma unroll
+  for (int k = 0; k < NQ; ++k) xr[k] = rd.rows(0, 0, k);
+  for (int i = 0; i < tiles; ++i) {
+    int next_at = i_at + 1, next_head = i_head, next_stage = stage + 1;
+    if (next_at == lo + per) next_at = lo, ++next_head;
+    if (next_stage == kStages) next_stage = 0;
+    bool next_masked = false, next_odd = false;
 #pragma unroll
     for (int sb = 0; sb < 2; ++sb) {
-      v16f_t s = attn_rows_product<DP, BF16>(rd, 0, sb, kr), t = attn_zero();
-      if constexpr (DK) t = attn_rows_product<DP, BF16>(rd, 1, sb, vr);
+      v4f l[4];
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
+      for (int e = 0; e < 4; ++e)
+        l[e] = *reinterpret_cast<const v4f*>(st_mine + stage * 128 + 32 * sb + 16 * (e >> 1) + 4 * (e & 1));
+      v16f_t s;
 #pragma unroll
-        for (int e = 0; e < 8; e += 4) {
-          const int row = 32 * sb + 16 * k + 8 * hf + e;
-          const v4f l = *reinterpret_cast<const v4f*>(st_l + row);
-          v4f dl;
-          if constexpr (DK) dl = *reinterpret_cast<const v4f*>(st_l + 64 + row);
+      for (int k = 0; k < NQ; ++k) {
+        xc[k] = rd.channels(0, k % ND, 2 * sb + k / ND);
+        s = Act16<BF16>::mma32(xr[k], kv[k], k == 0 ? attn_zero() : s);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      auto mask = [&](v16f_t& x) {
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int y = 8 * k + e + x;
-            s[y] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[y], f, kUp - l[x]));
-            if constexpr (DK) t[y] = s[y] * (t[y] - dl[x]);
-          }
+        for (int z = 0; z < 16; ++z) {
+          const int row = base + 32 * sb + 16 * (z >> 3) + 8 * hf + (z & 7);
+          if (!((row >= from) & (row < until))) x[z] = 0.0f;
         }
-      if (masked) {
+      };
+      v4f* p = p_mine + sb * kPairs * 256;
+      if (!second) {
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
-          const int row = base + 32 * sb + 16 * (x >> 3) + 8 * hf + (x & 7);
-          if (!((row >= from) & (row < until))) s[x] = t[x] = 0.0f;
+        for (int z = 0; z < 16; ++z) s[z] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[z], f, l[z >> 2][z & 3]));
+        if (masked) mask(s);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[e * 64] = v4f{s[4 * e], s[4 * e + 1], s[4 * e + 2], s[4 * e + 3]};
+      }
+      if (sb == 1) attn_wait_copies();  // the next tile's
+      __syncthreads();
+      if (sb == 1) {
+        rd.next_rows((next_stage - stage) * kStage);
+        if (i + 1 < tiles) next_odd = clean(next_stage, next_at << 6, &next_masked);
+        if (kStages > 2 && i + 2 < tiles) copy();
+      } else if (kStages == 2 && i + 1 < tiles) {
+        copy();
+      }
+      if (second) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const v4f w = p[e * 64];
+#pragma unroll
+          for (int z = 0; z < 4; ++z) s[4 * e + z] = w[z] * (s[4 * e + z] - l[e][z]);
+        }
+        if (masked) mask(s);
+        if constexpr (!BF16) {
+          reach.fit(s, acc);
+          s *= reach.g;
         }
       }
-      if constexpr (DK && !BF16) {
-        reach.fit(t, ak);
-        t *= reach.g;
-      }
+      uint4 w;
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        if constexpr (DV) {
-          const uint4 p = attn_pack<BF16>(s, k);
-#pragma unroll
-          for (int d = 0; d < ND; ++d) av[d] = Act16<BF16>::mma32(rd.channels(1, d, 2 * sb + k), p, av[d]);
-        }
-        if constexpr (DK) {
-          const uint4 p = attn_pack<BF16>(t, k);
-#pragma unroll
-          for (int d = 0; d < ND; ++d) ak[d] = Act16<BF16>::mma32(rd.channels(0, d, 2 * sb + k), p, ak[d]);
-        }
+      for (int k = 0; k < NQ; ++k) {
+        xr[k] = rd.rows(0, 1 - sb, k);  // nobody's after the last step
+        if (k % ND == 0) w = attn_pack<BF16>(s, k / ND);
+        acc[k % ND] = Act16<BF16>::mma32(xc[k], w, acc[k % ND]);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
     if (__builtin_expect(odd, 0)) {
       auto see = [&](int t) { return (base + t >= from) & (base + t < until); };
-      if constexpr (DV)
-        attn_others<DP, BF16>(av, gp + (int64_t)i_head * a.d_o.head, a.d_o.token, base, sq.n, D, see);
-      if constexpr (DK) attn_others<DP, BF16>(ak, qp + (int64_t)i_head * a.q.head, a.q.token, base, sq.n, D, see);
+      const KvRows& r = second ? a.q : a.d_o;
+      attn_others<DP, BF16>(acc, (second ? qp : gp) + (int64_t)i_head * r.head, r.token, base, sq.n, D, see);
     }
-    if (++i_at == lo + per) i_at = lo, ++i_head;
-    rd.next(stage ? -2 * Tile::kBytes : 2 * Tile::kBytes);
+    rd.next_channels((next_stage - stage) * kStage);
+    i_at = next_at, i_head = next_head, stage = next_stage, base = next_at << 6, masked = next_masked, odd = next_odd;
   }
 
   if (col >= sq.n) return;
-  auto store = [&](const KvRows& to, const v16f_t (&acc)[ND], float by) {
-    uint16_t* op = to.p + ((int64_t)sq.row0 + j) * to.token + (int64_t)h * to.head;
+  // P carries 2^15 in fp16; dS its column's power of two as well
+  const float by = (BF16 ? 1.0f : 3.0517578125e-5f) * (second ? a.scale / reach.g : 1.0f);
+  const KvRows& to = second ? a.dk : a.dv;
+  uint16_t* op = to.p + ((int64_t)sq.row0 + j) * to.token + (int64_t)h * to.head;
 #pragma unroll
-    for (int d = 0; d < ND; ++d)
+  for (int d = 0; d < ND; ++d)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int c = d * 32 + 8 * k + 4 * hf;
-        if (c >= D) continue;
-        *reinterpret_cast<uint2*>(op + c) =
-            make_uint2(Act16<BF16>::pack2(acc[d][4 * k] * by, acc[d][4 * k + 1] * by),
-                       Act16<BF16>::pack2(acc[d][4 * k + 2] * by, acc[d][4 * k + 3] * by));
-      }
-  };
-  if constexpr (DV) store(a.dv, av, BF16 ? 1.0f : 3.0517578125e-5f);
-  if constexpr (DK) store(a.dk, ak, a.scale / reach.g * (BF16 ? 1.0f : 3.0517578125e-5f));
+    for (int k = 0; k < 4; ++k) {
+      const int c = d * 32 + 8 * k + 4 * hf;
+      if (c >= D) continue;
+      *reinterpret_cast<uint2*>(op + c) =
+          make_uint2(Act16<BF16>::pack2(acc[d][4 * k] * by, acc[d][4 * k + 1] * by),
+                     Act16<BF16>::pack2(acc[d][4 * k + 2] * by, acc[d][4 * k + 3] * by));
+    }
 }
 
 template <int DP, bool BF16>
 static hipError_t launch_bwd(const AttnArgs& a, hipStream_t stream) {
+  constexpr int kShift = DP <= 128 ? 7 : 6;
   const int64_t rows = (((int64_t)a.T * (a.q_heads / a.heads) >> 7) + a.B) * a.heads;
-  const int64_t cols = (((int64_t)a.T >> 7) + a.B) * a.heads;
+  const int64_t cols = (((int64_t)a.T >> kShift) + a.B) * a.heads;
   if (rows > INT32_MAX || cols > INT32_MAX) return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL((ka_dq<DP, BF16>), dim3((unsigned)rows), dim3(256), 0, stream, a);
-  hipError_t e = hipGetLastError();
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if constexpr (DP <= 128) {
-    hipLaunchKernelGGL((ka_dkv<DP, BF16, true, true>), dim3((unsigned)cols), dim3(256), 0, stream, a);
-  } else {
-    hipLaunchKernelGGL((ka_dkv<DP, BF16, true, false>), dim3((unsigned)cols), dim3(256), 0, stream, a);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((ka_dkv<DP, BF16, false, true>), dim3((unsigned)cols), dim3(256), 0, stream, a);
-  }
+  hipLaunchKernelGGL((ka_dkv<DP, BF16>), dim3((unsigned)cols), dim3(DP <= 128 ? 512 : 256), 0, stream, a);
   return hipGetLastError();
 }
 

@@ -99,11 +99,17 @@ struct AttnRead {
 #pragma unroll
     for (int d = 0; d < 2; ++d) tr[d] = smem + Tile::at(t) + ((4 * d + c) ^ Tile::swizzle(t)) * 16 + 8 * (i & 1);
   }
-  __device__ __forceinline__ void next(int by) {
+  __device__ __forceinline__ void next_rows(int by) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) row[i] += by;
+  }
+  __device__ __forceinline__ void next_channels(int by) {
     tr[0] += by;
     tr[1] += by;
+  }
+  __device__ __forceinline__ void next(int by) {
+    next_rows(by);
+    next_channels(by);
   }
   // rows [32 block, +32) x channels [16 step, +16)
   __device__ __forceinline__ uint4 rows(int tile, int block, int step) const {
@@ -264,6 +270,32 @@ __device__ __forceinline__ v16f_t attn_rows_product(const AttnRead<DP>& rd, int 
     __builtin_amdgcn_sched_barrier(0);
   }
   return s;
+}
+
+// values 8 k .. 8 k + 7 as an operand
+template <bool BF16>
+__device__ __forceinline__ uint4 attn_pack(const v16f_t& t, int k) {
+  using A = Act16<BF16>;
+  return make_uint4(A::pack2(t[8 * k], t[8 * k + 1]), A::pack2(t[8 * k + 2], t[8 * k + 3]),
+                    A::pack2(t[8 * k + 4], t[8 * k + 5]), A::pack2(t[8 * k + 6], t[8 * k + 7]));
+}
+
+// acc += the tile's channels x rows [32 block, +32) times t, operands read two products ahead
+template <int DP, bool BF16>
+__device__ __forceinline__ void attn_channels_product(const AttnRead<DP>& rd, int tile, int block, const v16f_t& t,
+                                                      v16f_t (&acc)[DP / 32]) {
+  constexpr int ND = DP / 32, kAhead = 2;
+  uint4 x[kAhead + 1];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) x[i] = rd.channels(tile, i % ND, 2 * block + i / ND);
+  uint4 p;
+#pragma unroll
+  for (int i = 0; i < 2 * ND; ++i) {
+    if (i + kAhead < 2 * ND) x[(i + kAhead) % (kAhead + 1)] = rd.channels(tile, (i + kAhead) % ND, 2 * block + (i + kAhead) / ND);
+    if (i % ND == 0) p = attn_pack<BF16>(t, i / ND);
+    acc[i % ND] = Act16<BF16>::mma32(x[i % (kAhead + 1)], p, acc[i % ND]);
+    __builtin_amdgcn_sched_barrier(0);
+  }
 }
 
 }  // namespace llmint8

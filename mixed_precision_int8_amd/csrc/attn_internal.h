@@ -15,8 +15,8 @@ inline int admit_attention(int64_t seqs, int64_t rows, int64_t q_heads, int64_t 
   if (q_heads % heads != 0) return LLMINT8_ERR_INVALID_ARG;
   if (dim % 8 != 0 || dim > 256 || heads > 4096 || q_heads > 65536) return LLMINT8_ERR_UNSUPPORTED;
   if (rows > kKvMax || seqs > (int64_t(1) << 24)) return LLMINT8_ERR_UNSUPPORTED;
-  // workgroups of a launch: ((rows * group) / 128 + seqs) * heads
-  if (rows * q_heads > kKvMaxQRows || (rows * q_heads / 128 + (seqs + 1) * heads) >= kTwo31)
+  // workgroups of a launch: ((rows * group) / 128 + seqs) * heads, or rows / 64 for rows * group / 128
+  if (rows * q_heads > kKvMaxQRows || (rows * q_heads / 64 + (seqs + 1) * heads) >= kTwo31)
     return LLMINT8_ERR_UNSUPPORTED;
   return LLMINT8_OK;
 }
@@ -30,7 +30,7 @@ struct AttnArgs {
   int q_heads, heads, dim, causal, window, sinks;
   // backward
   KvRows d_o, dq, dk, dv;
-  float* stat;  // [2][q_heads][T]: a row's lse in powers of two, and sum do o
+  float* stat;  // [2][q_heads][T]: what a row's logits (in powers of two) are short of, and delta
 };
 
 // Rows [row0, row0 + n) of sequence b, cut to the call's rows whatever cu holds.

@@ -23,18 +23,17 @@ template <int DP, bool BF16>
 __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_attention(AttnArgs a) {
   using Tile = AttnTile<DP>;
   constexpr int W = 4, kRows = 32 * W, NQ = Tile::NQ, ND = Tile::ND;
-  __shared__ __attribute__((aligned(1024))) char smem[4 * Tile::kBytes];  // k, v; two stages
-  __shared__ int sh[4];
+  constexpr int kStage = 2 * Tile::kBytes;  // k, v
+  __shared__ __attribute__((aligned(1024))) char smem[2 * kStage + 16];
+  int* const flag = reinterpret_cast<int*>(smem + 2 * kStage);
   const int D = a.dim, H = a.heads, G = a.q_heads / H;
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
   const int hf = lane >> 5, nn = lane & 31;
-  // the last rows of a sequence see the most: they start first
-  const int h = (int)(blockIdx.x % H), item = (int)((gridDim.x - 1 - blockIdx.x) / H);
+  const int h = (int)(blockIdx.x % H), item = (int)(blockIdx.x / H);
   AttnSeq sq;
   int run;
-  if (!attn_find<64 * W>(a, item, G, 7, sh, &sq, &run)) return;
+  if (!attn_place<true>(a, item, G, 7, &sq, &run)) return;
   const int64_t rows = (int64_t)sq.n * G, row0 = (int64_t)run * kRows;
-  if (row0 >= rows) return;
   const int r = (int)min(row0 + wave * 32 + nn, rows - 1);
   const int pos = r / G, qh = h * G + (r - pos * G);
   const int64_t qrow = (int64_t)sq.row0 + pos;
@@ -52,10 +51,12 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_attention(AttnArgs 
   const uint16_t* kp = a.k.p + (int64_t)sq.row0 * a.k.token + (int64_t)h * a.k.head;
   const uint16_t* vp = a.v.p + (int64_t)sq.row0 * a.v.token + (int64_t)h * a.v.head;
   auto copy = [&](int i, int stage) {
-    ck.issue(kp, a.k.token, base_of(i), sq.n, smem + stage * 2 * Tile::kBytes);
-    cv.issue(vp, a.v.token, base_of(i), sq.n, smem + (stage * 2 + 1) * Tile::kBytes);
+    const int n = i < tiles ? sq.n : 0;  // past the last tile: zeros, to keep the loop free of branches
+    ck.issue(kp, a.k.token, base_of(i), n, smem + stage * kStage);
+    cv.issue(vp, a.v.token, base_of(i), n, smem + stage * kStage + Tile::kBytes);
   };
   copy(0, 0);
+  if (threadIdx.x == 0) *flag = 0;
 
   uint4 q[NQ];
   {
@@ -83,14 +84,15 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_attention(AttnArgs 
   AttnRead<DP> rd(smem);
   const AttnSees sees(a, pos, sq.n);
 
+  auto is_masked = [&](int base) { return base + 63 > all_end || base < all_begin; };
+  bool odd = false;  // whether a masked tile of v holds values that are not finite
   for (int i = 0; i < tiles; ++i) {
     const int stage = i & 1, base = base_of(i);
-    const bool masked = base + 63 > all_end || base < all_begin;
+    const bool masked = is_masked(base);
     attn_wait_copies();
-    __syncthreads();
-    bool odd = false;
-    if (masked) odd = attn_finite<DP, BF16, W>(smem + (stage * 2 + 1) * Tile::kBytes);
-    if (i + 1 < tiles) copy(i + 1, stage ^ 1);
+    attn_barrier();
+    if (masked) odd |= attn_finite<BF16, W>(smem + stage * kStage + Tile::kBytes, Tile::kBytes, flag, i + 1);
+    copy(i + 1, stage ^ 1);
 
     // operands are read two steps ahead of their products
     uint4 x[3][2];
@@ -152,9 +154,16 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_attention(AttnArgs 
       for (int d = 0; d < ND; ++d) acc[d] = Act16<BF16>::mma32(y[k & 1][d], p, acc[d]);
       __builtin_amdgcn_sched_barrier(0);
     }
-    if (__builtin_expect(odd, 0))
-      attn_others<DP, BF16>(acc, vp, a.v.token, base, sq.n, D, [&](int t) { return sees(base + t); });
-    rd.next(stage ? -2 * Tile::kBytes : 2 * Tile::kBytes);
+    rd.next(stage ? -kStage : kStage);
+  }
+  attn_wait_copies();
+  if (__builtin_expect(odd, 0)) {
+#pragma unroll 1
+    for (int i = 0; i < tiles; ++i) {
+      const int base = base_of(i);
+      if (is_masked(base))
+        attn_others<DP, BF16>(acc, vp, a.v.token, base, sq.n, D, [&](int t) { return sees(base + t); });
+    }
   }
 
   l_run = attn_pair_sum(l_run);

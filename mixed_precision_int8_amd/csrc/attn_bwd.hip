@@ -52,17 +52,17 @@ template <int DP, bool BF16>
 __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_dq(AttnArgs a) {
   using Tile = AttnTile<DP>;
   constexpr int W = 4, kRows = 32 * W, NQ = Tile::NQ, ND = Tile::ND;
-  __shared__ __attribute__((aligned(1024))) char smem[4 * Tile::kBytes];  // k, v; two stages
-  __shared__ int sh[4];
+  constexpr int kStage = 2 * Tile::kBytes;  // k, v
+  __shared__ __attribute__((aligned(1024))) char smem[2 * kStage + 16];
+  int* const flag = reinterpret_cast<int*>(smem + 2 * kStage);
   const int D = a.dim, H = a.heads, G = a.q_heads / H;
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
   const int hf = lane >> 5, nn = lane & 31;
-  const int h = (int)(blockIdx.x % H), item = (int)((gridDim.x - 1 - blockIdx.x) / H);
+  const int h = (int)(blockIdx.x % H), item = (int)(blockIdx.x / H);
   AttnSeq sq;
   int run;
-  if (!attn_find<64 * W>(a, item, G, 7, sh, &sq, &run)) return;
+  if (!attn_place<true>(a, item, G, 7, &sq, &run)) return;
   const int64_t rows = (int64_t)sq.n * G, row0 = (int64_t)run * kRows;
-  if (row0 >= rows) return;
   const int r = (int)min(row0 + wave * 32 + nn, rows - 1);
   const int pos = r / G, qh = h * G + (r - pos * G);
   const int64_t qrow = (int64_t)sq.row0 + pos;
@@ -80,10 +80,12 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_dq(AttnArgs a) {
   const uint16_t* kp = a.k.p + (int64_t)sq.row0 * a.k.token + (int64_t)h * a.k.head;
   const uint16_t* vp = a.v.p + (int64_t)sq.row0 * a.v.token + (int64_t)h * a.v.head;
   auto copy = [&](int i, int stage) {
-    ck.issue(kp, a.k.token, base_of(i), sq.n, smem + stage * 2 * Tile::kBytes);
-    cv.issue(vp, a.v.token, base_of(i), sq.n, smem + (stage * 2 + 1) * Tile::kBytes);
+    const int n = i < tiles ? sq.n : 0;  // past the last tile: zeros, to keep the loop free of branches
+    ck.issue(kp, a.k.token, base_of(i), n, smem + stage * kStage);
+    cv.issue(vp, a.v.token, base_of(i), n, smem + stage * kStage + Tile::kBytes);
   };
   copy(0, 0);
+  if (threadIdx.x == 0) *flag = 0;
 
   uint4 q[NQ], g[NQ];
   float delta = 0.0f;
@@ -129,14 +131,15 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_dq(AttnArgs a) {
   AttnRead<DP> rd(smem);
   const AttnSees sees(a, pos, sq.n);
 
+  auto is_masked = [&](int base) { return base + 63 > all_end || base < all_begin; };
+  bool odd = false;  // whether a masked tile of k holds values that are not finite
   for (int i = 0; i < tiles; ++i) {
     const int stage = i & 1, base = base_of(i);
-    const bool masked = base + 63 > all_end || base < all_begin;
+    const bool masked = is_masked(base);
     attn_wait_copies();
-    __syncthreads();
-    bool odd = false;
-    if (masked) odd = attn_finite<DP, BF16, W>(smem + stage * 2 * Tile::kBytes);
-    if (i + 1 < tiles) copy(i + 1, stage ^ 1);
+    attn_barrier();
+    if (masked) odd |= attn_finite<BF16, W>(smem + stage * kStage, Tile::kBytes, flag, i + 1);
+    copy(i + 1, stage ^ 1);
 #pragma unroll
     for (int sb = 0; sb < 2; ++sb) {
       v16f_t s = attn_rows_product<DP, BF16>(rd, 0, sb, q);
@@ -167,9 +170,16 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_dq(AttnArgs a) {
         __builtin_amdgcn_sched_barrier(0);
       }
     }
-    if (__builtin_expect(odd, 0))
-      attn_others<DP, BF16>(acc, kp, a.k.token, base, sq.n, D, [&](int t) { return sees(base + t); });
-    rd.next(stage ? -2 * Tile::kBytes : 2 * Tile::kBytes);
+    rd.next(stage ? -kStage : kStage);
+  }
+  attn_wait_copies();
+  if (__builtin_expect(odd, 0)) {
+#pragma unroll 1
+    for (int i = 0; i < tiles; ++i) {
+      const int base = base_of(i);
+      if (is_masked(base))
+        attn_others<DP, BF16>(acc, kp, a.k.token, base, sq.n, D, [&](int t) { return sees(base + t); });
+    }
   }
 
   if (!mine) return;
@@ -199,21 +209,19 @@ __global__ __launch_bounds__(DP <= 128 ? 512 : 256, DP <= 128 ? 2 : 1) void ka_d
   using Tile = AttnTile<DP>;
   constexpr int kPairs = DP <= 128 ? 4 : 2, W = 2 * kPairs, kCols = 32 * kPairs, NQ = Tile::NQ, ND = Tile::ND;
   constexpr int kStages = DP <= 128 ? 3 : 2, kStage = 2 * Tile::kBytes;
-  __shared__ __attribute__((aligned(1024))) char smem[kStages * kStage];             // q, do
-  __shared__ __attribute__((aligned(256))) float sh_stat[2 * kStages * 64];          // lse, delta
-  __shared__ __attribute__((aligned(1024))) v4f sh_p[2 * kPairs * 4 * 64];           // P, two steps
-  __shared__ int sh[4];
+  // q, do; P, two steps; lse, delta of the stages and a place that the other wavefronts' go to; a flag
+  constexpr int kAtP = kStages * kStage, kAtStat = kAtP + 2 * kPairs * 4096, kAtFlag = kAtStat + kStages * 512 + 256;
+  __shared__ __attribute__((aligned(1024))) char smem[kAtFlag + 16];
+  int* const flag = reinterpret_cast<int*>(smem + kAtFlag);
   const int D = a.dim, H = a.heads, G = a.q_heads / H;
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
   const int hf = lane >> 5, nn = lane & 31, pair = wave % kPairs;
   const bool second = wave >= kPairs;
-  // the first tokens of a sequence are seen by the most: they start first
   const int h = (int)(blockIdx.x % H), item = (int)(blockIdx.x / H);
   AttnSeq sq;
   int run;
-  if (!attn_find<64 * W>(a, item, 1, kPairs == 4 ? 7 : 6, sh, &sq, &run)) return;
+  if (!attn_place<false>(a, item, 1, kPairs == 4 ? 7 : 6, &sq, &run)) return;
   const int j0 = run * kCols;
-  if (j0 >= sq.n) return;
   const int col = j0 + pair * 32 + nn, j = min(col, sq.n - 1), j_hi = min(j0 + kCols, sq.n) - 1;
 
   // rows that see any of the tokens
@@ -228,18 +236,19 @@ __global__ __launch_bounds__(DP <= 128 ? 512 : 256, DP <= 128 ? 2 : 1) void ka_d
   const float* sp = a.stat + (int64_t)h * G * a.T + sq.row0;
   int c_head = 0, c_at = lo, c_stage = 0;  // the tile that is copied next
   auto copy = [&]() {
-    const int base = c_at << 6;
+    const int base = c_at << 6, n = c_head < G ? sq.n : 0;  // past the last tile: zeros
     char* to = smem + c_stage * kStage;
-    cq.issue(qp + (int64_t)c_head * a.q.head, a.q.token, base, sq.n, to);
-    cg.issue(gp + (int64_t)c_head * a.d_o.head, a.d_o.token, base, sq.n, to + Tile::kBytes);
-    if (wave < 2) {
-      const float* p = sp + (int64_t)c_head * a.T + base + (wave ? (int64_t)a.q_heads * a.T : 0);
-      attn_copy4(make_rsrc(p, (uint32_t)min(sq.n - base, 64) * 4), sh_stat + (c_stage * 2 + wave) * 64, (uint32_t)lane * 4);
-    }
+    cq.issue(qp + (int64_t)c_head * a.q.head, a.q.token, base, n, to);
+    cg.issue(gp + (int64_t)c_head * a.d_o.head, a.d_o.token, base, n, to + Tile::kBytes);
+    const float* p = sp + (int64_t)c_head * a.T + base + (wave ? (int64_t)a.q_heads * a.T : 0);
+    attn_copy4(make_rsrc(reinterpret_cast<const float*>(uniform((int64_t)p)),
+                         (uint32_t)uniform(wave < 2 ? max(min(n - base, 64), 0) * 4 : 0)),
+               smem + kAtStat + uniform(wave < 2 ? c_stage * 512 + wave * 256 : kStages * 512), (uint32_t)lane * 4);
     if (++c_at == lo + per) c_at = lo, ++c_head;
     if (++c_stage == kStages) c_stage = 0;
   };
   copy();
+  if (threadIdx.x == 0) *flag = 0;
 
   uint4 kv[NQ];  // k of this lane's token, v in the second wavefront
   {
@@ -268,103 +277,131 @@ __global__ __launch_bounds__(DP <= 128 ? 512 : 256, DP <= 128 ? 2 : 1) void ka_d
   // tiles that begin from here on and end before there are seen whole by all columns
   const int all_from = a.causal ? j_hi : 0;
   const int all_until = a.window > 0 && j_hi >= a.sinks ? max(j0, (int)min((int64_t)a.sinks, (int64_t)j_hi)) + a.window : INT32_MAX;
-  // once a tile's copies are there for all: the values that no masked product may meet
-  auto clean = [&](int stage, int base, bool* masked) {
-    *masked = base < all_from || base + 64 > all_until;
-    if (!*masked) return false;
-    const bool q_odd = attn_finite<DP, BF16, W>(smem + stage * kStage);
-    return attn_finite<DP, BF16, W>(smem + stage * kStage + Tile::kBytes) || q_odd;
-  };
+  auto is_masked = [&](int base) { return base < all_from || base + 64 > all_until; };
 
-  // the first wavefront's products are q's rows and do's channels, the second's the others
-  AttnRead<DP> rd(smem);
+  // A step takes 32 rows of a tile. The second wavefront is a step behind the first, so that
+  // P is there when it asks for it and neither waits for the other: one barrier to a step, P
+  // in two buffers. Copies of a tile have two steps to arrive (three stages: a tile is left
+  // by the second wavefront a step after the first).
+  AttnRead<DP> rd(smem);  // the first wavefront's products are q's rows and do's channels, the second's the others
   rd.next_rows(second ? Tile::kBytes : 0);
   rd.next_channels(second ? 0 : Tile::kBytes);
-  v4f* const p_mine = sh_p + pair * 256 + lane;
-  const float* const st_mine = sh_stat + (second ? 64 : 0) + 8 * hf;
+  v4f* const p_mine = reinterpret_cast<v4f*>(smem + kAtP) + pair * 256 + lane;
+  const char* st_mine = smem + kAtStat + (second ? 256 : 0) + 32 * hf;
+  bool odd = false;  // whether a masked tile holds values that are not finite
+  int w_at = lo;     // the tile that is cleaned next: of the values that no masked product may meet
+  auto clean = [&](int tile) {
+    const int base = w_at << 6;
+    if (++w_at == lo + per) w_at = lo;
+    if (is_masked(base)) odd |= attn_finite<BF16, W>(smem + tile % kStages * kStage, kStage, flag, tile + 1);
+  };
   attn_wait_copies();
-  __syncthreads();
-  int base = lo << 6, i_at = lo, i_head = 0, stage = 0;
-  bool masked;
-  bool odd = clean(0, base, &masked);
-  if (kStages > 2 && tiles > 1) copy();
-  // Operands are read a phase ahead: a step's channels during the products of its rows,
-  // the next step's rows during those of its channels.
+  attn_barrier();
+  clean(0);
+  if (kStages > 2) copy();
+  // A step's products: NQ of rows, NQ of channels. Operands are read kRing - 1 products ahead,
+  // beyond the step's end from the next step's rows.
   static_assert(NQ == 2 * ND, "a step has as many products of rows as of channels");
-  uint4 xr[NQ], xc[NQ];
+  constexpr int kRing = NQ == 4 ? 4 : NQ == 6 ? 6 : 8;
+  static_assert(2 * NQ % kRing == 0, "a product's place in the ring is the same in every step");
+  static_assert(kRing <= NQ + 1, "the next step's rows are read once the addresses have moved on");
+  uint4 ring[kRing];
+  auto fetch = [&](int n) {
+    if (n < NQ || (n >= 2 * NQ && kStages > 2)) ring[n % kRing] = rd.rows(0, 0, n % (2 * NQ));
+    else if (n < 2 * NQ) ring[n % kRing] = rd.channels(0, (n - NQ) % ND, (n - NQ) / ND);
+  };
+  if (kStages > 2) {
 #pragma unroll
-  for (int k = 0; k < NQ; ++k) xr[k] = rd.rows(0, 0, k);
-  for (int i = 0; i < tiles; ++i) {
-    int next_at = i_at + 1, next_head = i_head, next_stage = stage + 1;
-    if (next_at == lo + per) next_at = lo, ++next_head;
-    if (next_stage == kStages) next_stage = 0;
-    bool next_masked = false, next_odd = false;
+    for (int n = 0; n < kRing - 1; ++n) fetch(n);
+  }
+  int my = second ? -1 : 0, my_at = lo, my_stage = 0;
+  for (int k = 0; k <= 2 * tiles; ++k) {
+    const int tile = k >> 1;
+    if (kStages > 2) {
+      if (k & 1) {
+        if (tile + 1 < tiles) clean(tile + 1);
+        copy();
+      }
+    } else if (k & 1) {
+      copy();
+    } else if (k > 0 && tile < tiles) {
+      clean(tile);
+    }
+    if (my >= 0 && my < 2 * tiles) {
+      const int sb = my & 1, base = (my_at << 6) + 32 * sb;
+      const bool masked = is_masked(my_at << 6);
+      v4f* p = p_mine + sb * kPairs * 256;
+      v4f l[4], w[4];
 #pragma unroll
-    for (int sb = 0; sb < 2; ++sb) {
-      v4f l[4];
+      for (int e = 0; e < 4; ++e) l[e] = *reinterpret_cast<const v4f*>(st_mine + 64 * (e >> 1) + 16 * (e & 1));
+      if (second) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        l[e] = *reinterpret_cast<const v4f*>(st_mine + stage * 128 + 32 * sb + 16 * (e >> 1) + 4 * (e & 1));
+        for (int e = 0; e < 4; ++e) w[e] = p[e * 64];
+      }
+      if (kStages == 2) {
+#pragma unroll
+        for (int n = 0; n < kRing - 1; ++n) fetch(n);
+      }
       v16f_t s;
 #pragma unroll
-      for (int k = 0; k < NQ; ++k) {
-        xc[k] = rd.channels(0, k % ND, 2 * sb + k / ND);
-        s = Act16<BF16>::mma32(xr[k], kv[k], k == 0 ? attn_zero() : s);
+      for (int n = 0; n < NQ; ++n) {
+        fetch(n + kRing - 1);
+        s = Act16<BF16>::mma32(ring[n % kRing], kv[n], n == 0 ? attn_zero() : s);
         __builtin_amdgcn_sched_barrier(0);
       }
-      auto mask = [&](v16f_t& x) {
-#pragma unroll
-        for (int z = 0; z < 16; ++z) {
-          const int row = base + 32 * sb + 16 * (z >> 3) + 8 * hf + (z & 7);
-          if (!((row >= from) & (row < until))) x[z] = 0.0f;
-        }
-      };
-      v4f* p = p_mine + sb * kPairs * 256;
       if (!second) {
 #pragma unroll
         for (int z = 0; z < 16; ++z) s[z] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[z], f, l[z >> 2][z & 3]));
-        if (masked) mask(s);
+      } else {
+#pragma unroll
+        for (int z = 0; z < 16; ++z) s[z] = w[z >> 2][z & 3] * (s[z] - l[z >> 2][z & 3]);
+      }
+      if (masked) {
+#pragma unroll
+        for (int z = 0; z < 16; ++z) {
+          const int row = base + 16 * (z >> 3) + 8 * hf + (z & 7);
+          if (!((row >= from) & (row < until))) s[z] = 0.0f;
+        }
+      }
+      if (!second) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) p[e * 64] = v4f{s[4 * e], s[4 * e + 1], s[4 * e + 2], s[4 * e + 3]};
+      } else if constexpr (!BF16) {
+        reach.fit(s, acc);
+        s *= reach.g;
       }
-      if (sb == 1) attn_wait_copies();  // the next tile's
-      __syncthreads();
-      if (sb == 1) {
-        rd.next_rows((next_stage - stage) * kStage);
-        if (i + 1 < tiles) next_odd = clean(next_stage, next_at << 6, &next_masked);
-        if (kStages > 2 && i + 2 < tiles) copy();
-      } else if (kStages == 2 && i + 1 < tiles) {
-        copy();
-      }
-      if (second) {
+      int next_stage = my_stage;
+      if (sb == 1 && ++next_stage == kStages) next_stage = 0;
+      const int by = (next_stage - my_stage) * kStage + (sb == 0 ? 2 : -2) * Tile::kSixteen;
+      rd.next_rows(by);
+      uint4 x;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const v4f w = p[e * 64];
-#pragma unroll
-          for (int z = 0; z < 4; ++z) s[4 * e + z] = w[z] * (s[4 * e + z] - l[e][z]);
-        }
-        if (masked) mask(s);
-        if constexpr (!BF16) {
-          reach.fit(s, acc);
-          s *= reach.g;
-        }
-      }
-      uint4 w;
-#pragma unroll
-      for (int k = 0; k < NQ; ++k) {
-        xr[k] = rd.rows(0, 1 - sb, k);  // nobody's after the last step
-        if (k % ND == 0) w = attn_pack<BF16>(s, k / ND);
-        acc[k % ND] = Act16<BF16>::mma32(xc[k], w, acc[k % ND]);
+      for (int n = NQ; n < 2 * NQ; ++n) {
+        fetch(n + kRing - 1);  // nobody's after the last step
+        if (n % ND == 0) x = attn_pack<BF16>(s, (n - NQ) / ND);
+        acc[n % ND] = Act16<BF16>::mma32(ring[n % kRing], x, acc[n % ND]);
         __builtin_amdgcn_sched_barrier(0);
       }
+      rd.next_channels(by);
+      st_mine += (next_stage - my_stage) * 512 + (sb == 0 ? 128 : -128);
+      if (sb == 1) {
+        my_stage = next_stage;
+        if (++my_at == lo + per) my_at = lo;
+      }
     }
-    if (__builtin_expect(odd, 0)) {
-      auto see = [&](int t) { return (base + t >= from) & (base + t < until); };
-      const KvRows& r = second ? a.q : a.d_o;
-      attn_others<DP, BF16>(acc, (second ? qp : gp) + (int64_t)i_head * r.head, r.token, base, sq.n, D, see);
+    ++my;
+    if ((k & 1) == (kStages == 2)) attn_wait_copies();
+    attn_barrier();
+  }
+  attn_wait_copies();
+  if (__builtin_expect(odd, 0)) {
+    const KvRows& r = second ? a.q : a.d_o;
+#pragma unroll 1
+    for (int i = 0; i < tiles; ++i) {
+      const int at = (lo + i % per) << 6;
+      auto see = [&](int t) { return (at + t >= from) & (at + t < until); };
+      if (is_masked(at)) attn_others<DP, BF16>(acc, (second ? qp : gp) + (int64_t)(i / per) * r.head, r.token, at, sq.n, D, see);
     }
-    rd.next_channels((next_stage - stage) * kStage);
-    i_at = next_at, i_head = next_head, stage = next_stage, base = next_at << 6, masked = next_masked, odd = next_odd;
   }
 
   if (col >= sq.n) return;

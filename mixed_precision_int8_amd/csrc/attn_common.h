@@ -12,14 +12,14 @@
 // so that a lane's 16 results are rows 8 hf .. 8 hf + 7 of each sixteen: as they
 // stand, operand B of the next product, which sums over these rows.
 //
-// Rows of 16 are laid out so that the 16-byte reads of 16 rows at one chunk fall on all 64
-// banks, and so do the four rows x 32 bytes that a transposing read takes for 16 lanes:
-// chunks are stored at chunk ^ 2 (row % 4) and every four rows begin 16, 128 or 144 bytes
-// later (rows of 128 bytes: chunk ^ 2 (row / 2 % 4), 16 bytes later every eight rows). The
-// exclusive or touches three bits of a chunk's number, so that four addresses to a lane
-// serve all "rows" operands and two all "channels" operands: the rest of an address is a
-// constant of the instruction. (With the usual one over all bits each step had an address
-// of its own; the 128-channel kernels spilled 90 registers.)
+// An instruction of either kind takes LDS four cycles where no bank is asked twice: 16
+// rows of one chunk of 16 bytes, or four rows of four chunks. Chunks are stored at
+// chunk ^ 4 (row % 4), and every four rows begin 16 bytes later (rows of 128 bytes: at
+// chunk ^ 4 (row / 2 % 2) ^ (row / 4 % 2), 32 bytes later every eight rows). The exclusive
+// or touches few bits of a chunk's number, so that four addresses to a lane serve all
+// "rows" operands and four all "channels" operands: the rest of an address is a constant of
+// the instruction. (With one over all bits each step had an address of its own; the
+// 128-channel kernels spilled 90 registers.)
 #pragma once
 
 #include "attn_internal.h"
@@ -34,27 +34,44 @@ struct AttnTile {
   static constexpr int kPitch = DP <= 64 ? 128 : DP <= 128 ? 256 : 512;  // bytes of a row
   static constexpr int kChunks = kPitch / 16;
   static constexpr bool kNarrow = kPitch == 128;
-  static constexpr int kSixteen = 16 * kPitch + (kNarrow ? 32 : 256);  // bytes of 16 rows
+  static constexpr int kSixteen = 16 * kPitch + 64;  // bytes of 16 rows
   static constexpr int kBytes = 4 * kSixteen;
   static constexpr int NQ = DP / 16;  // 16-channel steps
   static constexpr int ND = DP / 32;  // 32-channel blocks
   static __device__ __forceinline__ constexpr int swizzle(int row) {
-    return kNarrow ? ((row >> 1) & 3) << 1 : (row & 3) << 1;
+    return kNarrow ? (row >> 1 & 1) << 2 | (row >> 2 & 1) : (row & 3) << 2;
   }
   static __device__ __forceinline__ constexpr int at(int row) {
-    const int pad = kNarrow ? (row >> 3 & 1) * 16 : (row >> 2 & 1) * 16 + (row >> 3 & 1) * 128;
-    return (row >> 4) * kSixteen + (row & 15) * kPitch + pad;
+    return (row >> 4) * kSixteen + (row & 15) * kPitch + (kNarrow ? (row >> 3 & 1) * 32 : (row >> 2 & 3) * 16);
   }
 };
 
 // Copies to LDS: 64 x 16 bytes (64 x 4) from the lanes' offsets to `to` on. (Functions of
 // their own, not of a template's: the host pass drops kernels whose instances use the
 // 16-byte form.)
+//
+// The compiler makes a read of LDS wait for every copy in flight unless it is told that the
+// two do not meet: the reads have to carry what it knows of types or scopes (a read of a
+// vector type does, one of uint4 does not, a transposing read does from a function with a
+// restricted pointer), and LDS has to be one array. Then the kernels' own waits are the only
+// ones: attn_wait_copies before a barrier that hands a tile over.
 __device__ __forceinline__ void attn_copy16(__amdgpu_buffer_rsrc_t r, char* to, uint32_t off) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 16, off, 0, 0, 0);
 }
-__device__ __forceinline__ void attn_copy4(__amdgpu_buffer_rsrc_t r, float* to, uint32_t off) {
+__device__ __forceinline__ void attn_copy4(__amdgpu_buffer_rsrc_t r, char* to, uint32_t off) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 4, off, 0, 0, 0);
+}
+__device__ __forceinline__ void attn_wait_copies() { __builtin_amdgcn_s_waitcnt(0x0f70); }  // vmcnt(0)
+// This wavefront's writes to LDS are done, then the workgroup's barrier. __syncthreads
+// would wait for the copies in flight as well.
+__device__ __forceinline__ void attn_barrier() {
+  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+  asm volatile("s_barrier" ::: "memory");
+}
+typedef short v4s __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ v4s attn_read_tr(const char* __restrict p) {
+  typedef __attribute__((address_space(3))) v4s* lds_v4s;
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)p);
 }
 
 // A matrix of rows in memory: the offset at which this thread's copies of a tile begin.
@@ -63,49 +80,56 @@ struct AttnCopy {
   using Tile = AttnTile<DP>;
   static constexpr int kIssues = 64 * Tile::kPitch / 1024 / W;  // of 1 KB to a wavefront and tile
   static constexpr int kRows = 1024 / Tile::kPitch;             // of an issue
-  static_assert(kRows * W % 4 == 0, "the rows of a thread's issues have one swizzle");
+  static_assert(kRows * W % 8 == 0, "the rows of a thread's issues have one swizzle and at() adds up");
   uint32_t off, step;
+  int to_mine;  // of this wavefront's first issue in a tile
   __device__ __forceinline__ AttnCopy(int64_t token, int dim) {
     const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
     const int row = wave * kRows + lane / Tile::kChunks, chunk = lane % Tile::kChunks ^ Tile::swizzle(row);
     off = chunk * 8 < dim ? (uint32_t)(row * (int)token * 2 + chunk * 16) : kOobOffset;
     step = (uint32_t)(kRows * W * (int)token * 2);
+    to_mine = Tile::at(wave * kRows);
   }
-  // rows [first, first + 64) of the n at p into LDS at `to`; those from n on are zeros
+  // rows [first, first + 64) of the n at p into LDS at `to`; those from n on are zeros. The
+  // window's numbers are the same in all lanes and have to be in scalar registers: of vector
+  // ones the compiler makes a loop around each copy.
   __device__ __forceinline__ void issue(const uint16_t* p, int64_t token, int first, int n, char* to) const {
-    const int wave = uniform((int)threadIdx.x >> 6);
     const int left = min(n - first, 64);
-    const __amdgpu_buffer_rsrc_t r = make_rsrc(p + (int64_t)first * token, (uint32_t)(max(left, 0) * (int)token * 2));
+    const uint16_t* at = reinterpret_cast<const uint16_t*>(uniform((int64_t)(p + (int64_t)first * token)));
+    const __amdgpu_buffer_rsrc_t r = make_rsrc(at, (uint32_t)uniform(max(left, 0) * (int)token * 2));
 #pragma unroll
-    for (int i = 0; i < kIssues; ++i) attn_copy16(r, to + Tile::at((i * W + wave) * kRows), off + i * step);
+    for (int i = 0; i < kIssues; ++i) attn_copy16(r, to + (to_mine + Tile::at(i * W * kRows)), off + i * step);
   }
 };
-
-__device__ __forceinline__ void attn_wait_copies() { __builtin_amdgcn_s_waitcnt(0x0f70); }  // vmcnt(0)
 
 // Operands from tiles: `tile` is the place of one among the tiles of a workgroup, a
 // constant; the addresses move between its stages (`next`).
 template <int DP>
 struct AttnRead {
   using Tile = AttnTile<DP>;
-  const char* row[4];
-  const char* tr[2];
+  static constexpr int kRowAt = Tile::kNarrow ? 2 : 4;  // addresses that differ by the exclusive or
+  const char* row[kRowAt];
+  const char* tr[4];
   __device__ __forceinline__ explicit AttnRead(const char* smem) {
     const int lane = threadIdx.x & 63, hf = lane >> 5, nn = lane & 31;
     const int r = (nn & 0x13) | (nn & 4) << 1 | (nn & 8) >> 1;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) row[i] = smem + Tile::at(r) + ((2 * i + hf) ^ Tile::swizzle(r)) * 16;
+    for (int i = 0; i < kRowAt; ++i) row[i] = smem + Tile::at(r) + ((4 * i + hf) ^ Tile::swizzle(r)) * 16;
     const int i = lane & 15, t = 8 * hf + (i >> 2), c = 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);
 #pragma unroll
-    for (int d = 0; d < 2; ++d) tr[d] = smem + Tile::at(t) + ((4 * d + c) ^ Tile::swizzle(t)) * 16 + 8 * (i & 1);
+    for (int d = 0; d < 4; ++d) {
+      // narrow: 32-channel block d / 2, and four rows on where d is odd
+      const int u = Tile::kNarrow ? t + 4 * (d & 1) : t, block = Tile::kNarrow ? d >> 1 : d;
+      tr[d] = smem + Tile::at(u) + ((4 * block + c) ^ Tile::swizzle(u)) * 16 + 8 * (i & 1);
+    }
   }
   __device__ __forceinline__ void next_rows(int by) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) row[i] += by;
+    for (int i = 0; i < kRowAt; ++i) row[i] += by;
   }
   __device__ __forceinline__ void next_channels(int by) {
-    tr[0] += by;
-    tr[1] += by;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) tr[i] += by;
   }
   __device__ __forceinline__ void next(int by) {
     next_rows(by);
@@ -113,52 +137,75 @@ struct AttnRead {
   }
   // rows [32 block, +32) x channels [16 step, +16)
   __device__ __forceinline__ uint4 rows(int tile, int block, int step) const {
-    return *reinterpret_cast<const uint4*>(row[step & 3] + (tile * Tile::kBytes + (step >> 2) * 128 + block * 2 * Tile::kSixteen));
+    const v4i x = *reinterpret_cast<const v4i*>(
+        row[(step >> 1) % kRowAt] + (tile * Tile::kBytes + (step & 1) * 32 + (step >> 3) * 256 + block * 2 * Tile::kSixteen));
+    return __builtin_bit_cast(uint4, x);
   }
   // channels [32 block, +32) x rows [16 step, +16)
   __device__ __forceinline__ uint4 channels(int tile, int block, int step) const {
-    typedef short v4s __attribute__((ext_vector_type(4)));
-    typedef __attribute__((address_space(3))) v4s* lds_v4s;
-    const int at = tile * Tile::kBytes + (block >> 1) * 128 + step * Tile::kSixteen;
-    // four rows on, the exclusive or of narrow rows has its bit 2 turned
-    const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(tr[block & 1] + at));
-    const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(tr[(block ^ (int)Tile::kNarrow) & 1] + at + Tile::at(4)));
+    const int at = tile * Tile::kBytes + (Tile::kNarrow ? 0 : (block >> 2) * 256) + step * Tile::kSixteen;
+    const char* first = tr[Tile::kNarrow ? 2 * block : block & 3] + at;
+    const char* second = Tile::kNarrow ? tr[(2 * block + 1) & 3] + at : first + Tile::at(4);
+    const v4s lo = attn_read_tr(first);
+    const v4s hi = attn_read_tr(second);
     const uint2 a = __builtin_bit_cast(uint2, lo), b = __builtin_bit_cast(uint2, hi);
     return make_uint4(a.x, a.y, b.x, b.y);
   }
 };
 
-// The sequence that owns work item `item` (kv_items), as kv_find does it, for rows alone.
-template <int kThreads>
-__device__ __forceinline__ bool attn_find(const AttnArgs& a, int item, int per, int shift, int (&sh)[4], AttnSeq* out,
-                                          int* index) {
-  if (a.B == 1) {
-    const AttnSeq q = attn_seq_of(a.cu[0], a.cu[1], a.T);
-    out->row0 = uniform(q.row0);
-    out->n = uniform(q.n);
-    *index = kv_item_index(kv_items(0, out->row0, out->n, per, shift), item);
-    return *index >= 0;
-  }
-  int b = -1;
-  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-    const int i = b0 + (int)threadIdx.x, lane = min(i, a.B - 1);
-    const AttnSeq q = attn_seq_of(a.cu[lane], a.cu[lane + 1], a.T);
-    const KvItems own = kv_items(lane, q.row0, q.n, per, shift);
-    const int mine = __syncthreads_count(i < a.B && own.first <= item);
-    if (mine > 0 && (int)threadIdx.x == mine - 1) {
-      sh[0] = q.row0;
-      sh[1] = q.n;
-      sh[2] = kv_item_index(own, item);
+// The sequence and tile of 2^shift rows (tokens times `per`) that is a workgroup's work, by
+// one wavefront alone: no LDS, no barrier. False where there is none (a launch has a few
+// workgroups more than there is work).
+//   Up to 64 sequences: a lane has one, and the tiles of all go by how many their sequence
+// has below (DOWN) or above them, most first: with a causal mask that is their length, and
+// the longest start first. The level of item x is the largest l with x < F(l), where F(l) =
+// sum max(0, tiles - l) tiles have l or more.
+//   More: in the order of the sequences, the owner found by 64 probes at a time of where
+// their items begin (kv_items).
+template <bool DOWN>
+__device__ __forceinline__ bool attn_place(const AttnArgs& a, int item, int per, int shift, AttnSeq* out, int* run) {
+  const int lane = threadIdx.x & 63;
+  if (a.B <= 64) {
+    const int b = min(lane, a.B - 1);
+    const AttnSeq q = attn_seq_of(a.cu[b], a.cu[b + 1], a.T);
+    const int tiles = lane < a.B ? (int)(((int64_t)q.n * per + (1 << shift) - 1) >> shift) : 0;
+    auto at_least = [&](int l) { return __builtin_amdgcn_readlane(wave_incl_sum(max(tiles - l, 0)), 63); };
+    if (item >= at_least(0)) return false;
+    int lo = 0, hi = __builtin_amdgcn_readfirstlane(wave_max_i(tiles)), above = 0;  // F(lo) > item >= F(hi)
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1, f = at_least(mid);
+      if (f > item) lo = mid;
+      else hi = mid, above = f;
     }
-    b += mine;
-    if (mine < min(kThreads, a.B - b0)) break;
+    const uint64_t have = __ballot(tiles > lo);
+    const int before = __builtin_amdgcn_mbcnt_hi((uint32_t)(have >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)have, 0));
+    const uint64_t mine = __ballot(tiles > lo && before == item - above);
+    if (mine == 0) return false;  // cu falls somewhere
+    const int owner = __builtin_ctzll(mine);
+    out->row0 = __builtin_amdgcn_readlane(q.row0, owner);
+    out->n = __builtin_amdgcn_readlane(q.n, owner);
+    *run = DOWN ? lo : __builtin_amdgcn_readlane(tiles, owner) - 1 - lo;
+    return true;
   }
-  if (b < 0) return false;
-  __syncthreads();
-  out->row0 = uniform(sh[0]);
-  out->n = uniform(sh[1]);
-  *index = uniform(sh[2]);
-  return *index >= 0;
+  int lo = 0, hi = a.B;
+  while (true) {
+    const int step = (hi - lo + 63) >> 6, b = min(lo + lane * step, hi - 1);
+    const AttnSeq q = attn_seq_of(a.cu[b], a.cu[b + 1], a.T);
+    const KvItems own = kv_items(b, q.row0, q.n, per, shift);
+    const int below = __popcll(__ballot(lo + lane * step < hi && own.first <= item));
+    if (below == 0) return false;
+    if (step == 1) {
+      out->row0 = __builtin_amdgcn_readlane(q.row0, below - 1);
+      out->n = __builtin_amdgcn_readlane(q.n, below - 1);
+      const int at = __builtin_amdgcn_readlane(kv_item_index(own, item), below - 1);
+      const int tiles = (int)(((int64_t)out->n * per + (1 << shift) - 1) >> shift);
+      if (at < 0 || at >= tiles) return false;
+      *run = DOWN ? tiles - 1 - at : at;
+      return true;
+    }
+    lo += (below - 1) * step;
+    hi = min(hi, lo + step);
+  }
 }
 
 // with the other half's lane of the same column (lanes n and n + 32)
@@ -202,29 +249,29 @@ __device__ __forceinline__ float attn_max(float a, float b, float c) {
 
 // A product whose weights are exactly zero where a column does not see a row must not
 // take that row's values that are not finite (0 times them is NaN). Where a tile has
-// masked rows the workgroup zeroes such values in LDS first; if there were any (the
-// result), attn_others adds them, from memory, to the sums of the columns that see them.
-template <int DP, bool BF16, int W>
-__device__ __forceinline__ bool attn_finite(char* tile) {
-  using Tile = AttnTile<DP>;
+// masked rows the workgroup zeroes such values in LDS first and says whether there were any;
+// if so, attn_others adds them, from memory, at the end, to the sums of the columns that see
+// them. `flag`: a word of LDS that holds no `id` (ids are above 0 and differ).
+template <bool BF16, int W>
+__device__ __forceinline__ bool attn_finite(char* tile, int bytes, int* flag, int id) {
   constexpr uint32_t kUp = BF16 ? 0x00800080u : 0x04000400u;  // carries an exponent of ones into bit 15
   uint32_t odd = 0;
-#pragma unroll
-  for (int i = 0; i < 64 * Tile::kChunks / (64 * W); ++i) {
-    const int u = i * 64 * W + (int)threadIdx.x;
-    uint4* at = reinterpret_cast<uint4*>(tile + Tile::at(u / Tile::kChunks) + u % Tile::kChunks * 16);
-    const uint4 x = *at;
-    uint32_t v[4] = {x.x, x.y, x.z, x.w}, any = 0;
+  for (int u = threadIdx.x * 16; u < bytes; u += 64 * W * 16) {
+    v4i* at = reinterpret_cast<v4i*>(tile + u);
+    v4i x = *at;
+    uint32_t any = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint32_t bad = ((v[j] & 0x7fff7fffu) + kUp) & 0x80008000u;
+      const uint32_t v = (uint32_t)x[j], bad = ((v & 0x7fff7fffu) + kUp) & 0x80008000u;
       any |= bad;
-      v[j] &= ~((bad >> 15) * 0xffffu);
+      x[j] = (int)(v & ~((bad >> 15) * 0xffffu));
     }
-    if (any) *at = make_uint4(v[0], v[1], v[2], v[3]);
+    if (any) *at = x;
     odd |= any;
   }
-  return __syncthreads_or(odd != 0);
+  if (odd) *flag = id;
+  attn_barrier();
+  return uniform(*flag) == id;
 }
 // Rows [first, first + 64) of the n at p; `see(row)`: whether this lane's column sees that
 // row of the 64.

@@ -57,6 +57,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_attention(AttnArgs 
   };
   copy(0, 0);
   if (threadIdx.x == 0) *flag = 0;
+  attn_barrier();
 
   uint4 q[NQ];
   {
@@ -85,13 +86,12 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_attention(AttnArgs 
   const AttnSees sees(a, pos, sq.n);
 
   auto is_masked = [&](int base) { return base + 63 > all_end || base < all_begin; };
-  bool odd = false;  // whether a masked tile of v holds values that are not finite
   for (int i = 0; i < tiles; ++i) {
     const int stage = i & 1, base = base_of(i);
     const bool masked = is_masked(base);
     attn_wait_copies();
+    if (masked) cv.template finite<BF16>(smem + stage * kStage + Tile::kBytes, flag);
     attn_barrier();
-    if (masked) odd |= attn_finite<BF16, W>(smem + stage * kStage + Tile::kBytes, Tile::kBytes, flag, i + 1);
     copy(i + 1, stage ^ 1);
 
     // operands are read two steps ahead of their products
@@ -157,7 +157,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_attention(AttnArgs 
     rd.next(stage ? -kStage : kStage);
   }
   attn_wait_copies();
-  if (__builtin_expect(odd, 0)) {
+  if (__builtin_expect(uniform(*flag), 0)) {
 #pragma unroll 1
     for (int i = 0; i < tiles; ++i) {
       const int base = base_of(i);

@@ -32,15 +32,13 @@ struct Reach {
 #pragma unroll
       for (int x = 0; x < 16; ++x) top = fmaxf(top, fabsf(t[x]));
       top = attn_pair_max(top);
-      if (__any(top * g > 32768.0f)) {
-        if (top * g > 32768.0f) {
-          const int e = (int)(__float_as_uint(top) >> 23) - 127;
-          const float to = __uint_as_float((uint32_t)(min(8 - e, 126) + 127) << 23);
-          const float by = to / g;
+      if (__builtin_expect(__any(top * g > 32768.0f), 0)) {
+        const int e = (int)(__float_as_uint(top) >> 23) - 127;
+        const float to = top * g > 32768.0f ? __uint_as_float((uint32_t)(min(8 - e, 126) + 127) << 23) : g;
+        const float by = to / g;
 #pragma unroll
-          for (int d = 0; d < ND; ++d) acc[d] *= by;
-          g = to;
-        }
+        for (int d = 0; d < ND; ++d) acc[d] *= by;
+        g = to;
       }
     }
   }
@@ -86,6 +84,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_dq(AttnArgs a) {
   };
   copy(0, 0);
   if (threadIdx.x == 0) *flag = 0;
+  attn_barrier();
 
   uint4 q[NQ], g[NQ];
   float delta = 0.0f;
@@ -132,13 +131,12 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_dq(AttnArgs a) {
   const AttnSees sees(a, pos, sq.n);
 
   auto is_masked = [&](int base) { return base + 63 > all_end || base < all_begin; };
-  bool odd = false;  // whether a masked tile of k holds values that are not finite
   for (int i = 0; i < tiles; ++i) {
     const int stage = i & 1, base = base_of(i);
     const bool masked = is_masked(base);
     attn_wait_copies();
+    if (masked) ck.template finite<BF16>(smem + stage * kStage, flag);
     attn_barrier();
-    if (masked) odd |= attn_finite<BF16, W>(smem + stage * kStage, Tile::kBytes, flag, i + 1);
     copy(i + 1, stage ^ 1);
 #pragma unroll
     for (int sb = 0; sb < 2; ++sb) {
@@ -173,7 +171,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_dq(AttnArgs a) {
     rd.next(stage ? -kStage : kStage);
   }
   attn_wait_copies();
-  if (__builtin_expect(odd, 0)) {
+  if (__builtin_expect(uniform(*flag), 0)) {
 #pragma unroll 1
     for (int i = 0; i < tiles; ++i) {
       const int base = base_of(i);
@@ -249,6 +247,7 @@ __global__ __launch_bounds__(DP <= 128 ? 512 : 256, DP <= 128 ? 2 : 1) void ka_d
   };
   copy();
   if (threadIdx.x == 0) *flag = 0;
+  attn_barrier();
 
   uint4 kv[NQ];  // k of this lane's token, v in the second wavefront
   {
@@ -288,16 +287,20 @@ __global__ __launch_bounds__(DP <= 128 ? 512 : 256, DP <= 128 ? 2 : 1) void ka_d
   rd.next_channels(second ? 0 : Tile::kBytes);
   v4f* const p_mine = reinterpret_cast<v4f*>(smem + kAtP) + pair * 256 + lane;
   const char* st_mine = smem + kAtStat + (second ? 256 : 0) + 32 * hf;
-  bool odd = false;  // whether a masked tile holds values that are not finite
-  int w_at = lo;     // the tile that is cleaned next: of the values that no masked product may meet
-  auto clean = [&](int tile) {
+  // this wavefront's pieces of the tile that was copied last are there; then of the next one
+  int w_at = lo;
+  auto arrive = [&](int tile) {
     const int base = w_at << 6;
     if (++w_at == lo + per) w_at = lo;
-    if (is_masked(base)) odd |= attn_finite<BF16, W>(smem + tile % kStages * kStage, kStage, flag, tile + 1);
+    attn_wait_copies();
+    if (tile < tiles && is_masked(base)) {
+      char* at = smem + tile % kStages * kStage;
+      cq.template finite<BF16>(at, flag);
+      cg.template finite<BF16>(at + Tile::kBytes, flag);
+    }
   };
-  attn_wait_copies();
+  arrive(0);
   attn_barrier();
-  clean(0);
   if (kStages > 2) copy();
   // A step's products: NQ of rows, NQ of channels. Operands are read kRing - 1 products ahead,
   // beyond the step's end from the next step's rows.
@@ -316,17 +319,7 @@ __global__ __launch_bounds__(DP <= 128 ? 512 : 256, DP <= 128 ? 2 : 1) void ka_d
   }
   int my = second ? -1 : 0, my_at = lo, my_stage = 0;
   for (int k = 0; k <= 2 * tiles; ++k) {
-    const int tile = k >> 1;
-    if (kStages > 2) {
-      if (k & 1) {
-        if (tile + 1 < tiles) clean(tile + 1);
-        copy();
-      }
-    } else if (k & 1) {
-      copy();
-    } else if (k > 0 && tile < tiles) {
-      clean(tile);
-    }
+    if (k & 1) copy();
     if (my >= 0 && my < 2 * tiles) {
       const int sb = my & 1, base = (my_at << 6) + 32 * sb;
       const bool masked = is_masked(my_at << 6);
@@ -334,7 +327,9 @@ __global__ __launch_bounds__(DP <= 128 ? 512 : 256, DP <= 128 ? 2 : 1) void ka_d
       v4f l[4], w[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) l[e] = *reinterpret_cast<const v4f*>(st_mine + 64 * (e >> 1) + 16 * (e & 1));
-      if (second) {
+      // P is read before the products or, where that leaves no registers, after them
+      constexpr bool kEarly = BF16 || DP < 128;
+      if (kEarly && second) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) w[e] = p[e * 64];
       }
@@ -353,6 +348,10 @@ __global__ __launch_bounds__(DP <= 128 ? 512 : 256, DP <= 128 ? 2 : 1) void ka_d
 #pragma unroll
         for (int z = 0; z < 16; ++z) s[z] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[z], f, l[z >> 2][z & 3]));
       } else {
+        if (!kEarly) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = p[e * 64];
+        }
 #pragma unroll
         for (int z = 0; z < 16; ++z) s[z] = w[z >> 2][z & 3] * (s[z] - l[z >> 2][z & 3]);
       }
@@ -390,11 +389,11 @@ __global__ __launch_bounds__(DP <= 128 ? 512 : 256, DP <= 128 ? 2 : 1) void ka_d
       }
     }
     ++my;
-    if ((k & 1) == (kStages == 2)) attn_wait_copies();
+    if ((k & 1) == (kStages == 2)) arrive((k >> 1) + 1);
     attn_barrier();
   }
   attn_wait_copies();
-  if (__builtin_expect(odd, 0)) {
+  if (__builtin_expect(uniform(*flag), 0)) {
     const KvRows& r = second ? a.q : a.d_o;
 #pragma unroll 1
     for (int i = 0; i < tiles; ++i) {

@@ -100,6 +100,33 @@ struct AttnCopy {
 #pragma unroll
     for (int i = 0; i < kIssues; ++i) attn_copy16(r, to + (to_mine + Tile::at(i * W * kRows)), off + i * step);
   }
+  // A product whose weights are exactly zero where a column does not see a row must not take
+  // that row's values that are not finite (0 times them is NaN). Where a tile has masked rows
+  // every wavefront zeroes such values in the pieces that it copied, once they are there and
+  // before the barrier that hands the tile over, and sets *flag if there were any; attn_others
+  // then adds them, from memory, at the end, to the sums of the columns that see them.
+  template <bool BF16>
+  __device__ __forceinline__ void finite(char* to, int* flag) const {
+    constexpr uint32_t kUp = BF16 ? 0x00800080u : 0x04000400u;  // carries an exponent of ones into bit 15
+    v4i x[kIssues];
+    char* const at = to + to_mine + (threadIdx.x & 63) * 16;
+#pragma unroll
+    for (int i = 0; i < kIssues; ++i) x[i] = *reinterpret_cast<const v4i*>(at + Tile::at(i * W * kRows));
+#pragma unroll
+    for (int i = 0; i < kIssues; ++i) {
+      uint32_t odd = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t v = (uint32_t)x[i][j], bad = ((v & 0x7fff7fffu) + kUp) & 0x80008000u;
+        odd |= bad;
+        x[i][j] = (int)(v & ~((bad >> 15) * 0xffffu));
+      }
+      if (__builtin_expect(odd != 0, 0)) {
+        *reinterpret_cast<v4i*>(at + Tile::at(i * W * kRows)) = x[i];
+        *flag = 1;
+      }
+    }
+  }
 };
 
 // Operands from tiles: `tile` is the place of one among the tiles of a workgroup, a
@@ -247,32 +274,6 @@ __device__ __forceinline__ float attn_max(float a, float b, float c) {
   return __builtin_elementwise_maximum(__builtin_elementwise_maximum(a, b), c);
 }
 
-// A product whose weights are exactly zero where a column does not see a row must not
-// take that row's values that are not finite (0 times them is NaN). Where a tile has
-// masked rows the workgroup zeroes such values in LDS first and says whether there were any;
-// if so, attn_others adds them, from memory, at the end, to the sums of the columns that see
-// them. `flag`: a word of LDS that holds no `id` (ids are above 0 and differ).
-template <bool BF16, int W>
-__device__ __forceinline__ bool attn_finite(char* tile, int bytes, int* flag, int id) {
-  constexpr uint32_t kUp = BF16 ? 0x00800080u : 0x04000400u;  // carries an exponent of ones into bit 15
-  uint32_t odd = 0;
-  for (int u = threadIdx.x * 16; u < bytes; u += 64 * W * 16) {
-    v4i* at = reinterpret_cast<v4i*>(tile + u);
-    v4i x = *at;
-    uint32_t any = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t v = (uint32_t)x[j], bad = ((v & 0x7fff7fffu) + kUp) & 0x80008000u;
-      any |= bad;
-      x[j] = (int)(v & ~((bad >> 15) * 0xffffu));
-    }
-    if (any) *at = x;
-    odd |= any;
-  }
-  if (odd) *flag = id;
-  attn_barrier();
-  return uniform(*flag) == id;
-}
 // Rows [first, first + 64) of the n at p; `see(row)`: whether this lane's column sees that
 // row of the 64.
 template <int DP, bool BF16, class See>

@@ -8,18 +8,19 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import math
+import struct
+import sys
 
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
 
+m8 = sys.modules[__package__]  # the package: its loader and helpers are looked up when a call needs them
+torch = None                   # imported by the first call, as elsewhere in the package
 
-class _Shape(ctypes.Structure):
-    _fields_ = [("cu", _vp), ("seqs", _i64), ("rows", _i64), ("q_heads", _i64), ("heads", _i64), ("dim", _i64),
-                ("scale", ctypes.c_float), ("causal", ctypes.c_int), ("window", _i64), ("sinks", _i64)]
-
-
-class _Rows(ctypes.Structure):
-    _fields_ = [("data", _vp), ("token", _i64), ("head", _i64)]
+# llmint8_rows and llmint8_attention_shape as the calls hand them over: packed, which costs a third of filling
+# a ctypes structure (12 of them to an attention step with its gradient)
+_ROWS = struct.Struct("=3q").pack
+_SHAPE = struct.Struct("=6qfi2q").pack
 
 
 class _Grad(ctypes.Structure):
@@ -29,10 +30,10 @@ class _Grad(ctypes.Structure):
 def bind(lib):
     """Argument types of the library's entry points of this file."""
     i, p, d = ctypes.c_int, ctypes.POINTER, ctypes.c_double
-    r = p(_Rows)
+    r = ctypes.c_char_p  # packed structures
     types = {
-        "attention": [p(_Shape), i, r, r, r, r, _vp, _vp],
-        "attention_backward": [p(_Shape), i, r, r, r, r, _vp, r, r, r, r, _vp, ctypes.c_size_t, _vp],
+        "attention": [r, i, r, r, r, r, _vp, _vp],
+        "attention_backward": [r, i, r, r, r, r, _vp, r, r, r, r, _vp, ctypes.c_size_t, _vp],
         "rope": [i, r, r, _i64, r, r, _i64, _i64, _i64, _vp, _i64, ctypes.c_char_p, _vp, _i64, _i64, i, i, _vp],
         "layer_norm": [_vp, _i64, i, _i64, _i64, _vp, _vp, i, ctypes.c_float, _vp, _i64, _vp, _vp],
         "layer_norm_backward": [_vp, _i64, _vp, _i64, i, _i64, _i64, _vp, i, _vp, _vp, _i64, _vp, _vp, _vp,
@@ -41,7 +42,7 @@ def bind(lib):
         "grad_clip": [p(_Grad), _i64, _vp, d, d, _vp],
     }
     sizes = {
-        "attention_backward_workspace_bytes": [p(_Shape)],
+        "attention_backward_workspace_bytes": [r],
         "layer_norm_workspace_bytes": [_i64, _i64],
         "grad_norm_workspace_bytes": [p(_Grad), _i64],
     }
@@ -51,14 +52,16 @@ def bind(lib):
             fn.argtypes, fn.restype = args, result
 
 
-def _m8():
-    import mixed_precision_int8_amd as m8
-    return m8
+def _library():
+    global torch
+    if torch is None:
+        import torch as t
+        torch = t
+    return m8.load_library()
 
 
 def _handle(stream, device):
-    from .kvcache import _stream
-    return _stream(stream, device)
+    return m8.kvcache._stream(stream, device)
 
 
 _NOTHING = contextlib.nullcontext()
@@ -66,46 +69,56 @@ _NOTHING = contextlib.nullcontext()
 
 def _on(device):
     """The call's device as the current one: a launch on a device's default stream goes to the current device."""
-    import torch
-    if device.type != "cuda" or device.index is None or torch.cuda.current_device() == device.index:
+    if device.type != "cuda" or device.index in (None, torch._C._cuda_getDevice()):
         return _NOTHING
     return torch.cuda.device(device)
 
 
 def _dtype(dtype, name):
-    import torch
-    m8 = _m8()
-    codes = {torch.float16: m8.LLMINT8_DTYPE_F16, torch.bfloat16: m8.LLMINT8_DTYPE_BF16,
-             torch.float32: m8.LLMINT8_DTYPE_F32}
-    if dtype not in codes:
-        raise ValueError(f"{name}: fp16, bf16 or fp32 only, got {dtype}")
-    return codes[dtype]
+    if dtype == torch.float16:
+        return m8.LLMINT8_DTYPE_F16
+    if dtype == torch.bfloat16:
+        return m8.LLMINT8_DTYPE_BF16
+    if dtype == torch.float32:
+        return m8.LLMINT8_DTYPE_F32
+    raise ValueError(f"{name}: fp16, bf16 or fp32 only, got {dtype}")
 
 
-def _plain(t, name, instead):
+def _half(dtype):
+    if dtype == torch.float16:
+        return m8.LLMINT8_DTYPE_F16
+    if dtype == torch.bfloat16:
+        return m8.LLMINT8_DTYPE_BF16
+    raise ValueError(f"fp16 or bf16 only, got {dtype}")
+
+
+def _plain(tensors, names, instead):
     """The calls named as the library's leave the graph without a word, so what would need one is refused."""
-    import torch
-    if t is not None and t.requires_grad and torch.is_grad_enabled():
-        raise ValueError(f"{name}: requires a gradient, which this call does not record: use {instead} (or detach it, "
-                         "or call under torch.no_grad())")
+    for t in tensors:
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            raise ValueError(f"{names}: one requires a gradient, which this call does not record: use {instead} (or "
+                             "detach it, or call under torch.no_grad())")
 
 
 def _rows(t, dtype, shape, device, name):
     """16-bit rows [rows, heads, dim] with dense channels, as the library takes them."""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device:
+    if t.dtype != dtype or t.shape != shape or t.device != device:
         raise ValueError(f"{name}: expected {dtype} {tuple(shape)} on {device}, got {t.dtype} {tuple(t.shape)} on "
                          f"{t.device}")
     st, sh, sc = t.stride()
-    if sc != 1 and t.shape[2] > 1 and t.numel() > 0:
+    if sc != 1 and shape[2] > 1 and t.numel() > 0:
         raise ValueError(f"{name}: the channels must be dense, got strides {t.stride()}")
-    return _Rows(t.data_ptr(), st, sh)
+    return _ROWS(t.data_ptr(), st, sh)
+
+
+def _new(shape, dtype, device, stream):
+    return torch.empty(shape, dtype=dtype, device=device) if stream is None else m8._empty(shape, dtype, device, stream)
 
 
 def _like(t, stream):
-    import torch
     if stream is None:
         return torch.empty_like(t, memory_format=torch.contiguous_format)
-    return _m8()._empty(t.shape, t.dtype, t.device, stream)
+    return m8._empty(t.shape, t.dtype, t.device, stream)
 
 
 # ---- attention
@@ -119,11 +132,11 @@ class PackedRows:
     __slots__ = ("cu", "seqs", "rows", "device", "used", "max_len")
 
     def __init__(self, cu, rows, max_len=0, used=None):
-        import torch
+        _library()
         self.seqs = cu.shape[0] - 1 if cu.dim() == 1 else -1
         if self.seqs < 0:
             raise ValueError(f"cu: expected [seqs + 1], got {tuple(cu.shape)}")
-        _m8()._need(cu, torch.int32, (self.seqs + 1,), "cu")
+        m8._need(cu, torch.int32, (self.seqs + 1,), "cu")
         self.rows = int(rows)
         if self.rows < 0 or max_len < 0:
             raise ValueError("rows and max_len: expected >= 0")
@@ -133,7 +146,7 @@ class PackedRows:
     @classmethod
     def of(cls, lengths, rows=None, device="cuda"):
         """Of sequences of these lengths (a list), in a call of ``rows`` rows (their sum by default)."""
-        import torch
+        _library()
         at = [0]
         for n in lengths:
             if n < 0:
@@ -149,7 +162,7 @@ def _shape(batch, q, k, scale, causal, window, sinks):
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError(f"q and k: expected [rows, heads, dim], got {tuple(q.shape)} and {tuple(k.shape)}")
     dim = q.shape[2]
-    return _Shape(batch.cu.data_ptr(), batch.seqs, batch.rows, q.shape[1], k.shape[1], dim,
+    return _SHAPE(batch.cu.data_ptr(), batch.seqs, batch.rows, q.shape[1], k.shape[1], dim,
                   1.0 / math.sqrt(max(dim, 1)) if scale is None else float(scale), 1 if causal else 0, window, sinks)
 
 
@@ -158,21 +171,19 @@ def llmint8_attention(batch, q, k, v, scale=None, causal=True, window=0, sinks=0
     tokens. q [rows, q_heads, dim], k and v [rows, heads, dim], fp16 or bf16; ``scale`` is 1 / sqrt(dim) by default;
     ``window`` > 0 (causal) keeps the last ``window`` tokens and the first ``sinks`` ones. Rows of no sequence are
     left as they were."""
-    import torch
-    m8 = _m8()
-    lib = m8.load_library()
-    for t, name in ((q, "q"), (k, "k"), (v, "v")):
-        _plain(t, name, "packed_attention")
+    lib = _library()
+    _plain((q, k, v), "q, k and v", "packed_attention")
     dev, dt = batch.device, q.dtype
     s = _shape(batch, q, k, scale, causal, window, sinks)
-    code = m8._act_dtype(dt)
-    wide, narrow = (batch.rows, s.q_heads, s.dim), (batch.rows, s.heads, s.dim)
+    code = _half(dt)
+    heads, dim, n = q.shape[1], q.shape[2], batch.rows
+    wide, narrow = (n, heads, dim), (n, k.shape[1], dim)
     rows = [_rows(q, dt, wide, dev, "q"), _rows(k, dt, narrow, dev, "k"), _rows(v, dt, narrow, dev, "v")]
     if out is None:
         out = _like(q, stream)
     rows.append(_rows(out, dt, wide, dev, "out"))
     if lse is None:
-        lse = m8._empty(wide[:2], torch.float32, dev, stream)
+        lse = _new(wide[:2], torch.float32, dev, stream)
     else:
         m8._need(lse, torch.float32, wide[:2], "lse")
         if lse.device != dev:
@@ -183,36 +194,36 @@ def llmint8_attention(batch, q, k, v, scale=None, causal=True, window=0, sinks=0
 
 
 def llmint8_attention_backward_workspace_bytes(batch, q_heads, heads, dim) -> int:
-    s = _Shape(batch.cu.data_ptr(), batch.seqs, batch.rows, q_heads, heads, dim, 1.0, 1, 0, 0)
-    return int(_m8().load_library().llmint8_attention_backward_workspace_bytes(s))
+    s = _SHAPE(batch.cu.data_ptr(), batch.seqs, batch.rows, q_heads, heads, dim, 1.0, 1, 0, 0)
+    return int(_library().llmint8_attention_backward_workspace_bytes(s))
 
 
 def llmint8_attention_backward(batch, q, k, v, out, lse, dout, scale=None, causal=True, window=0, sinks=0, dq=None,
                                dk=None, dv=None, workspace=None, stream=None):
     """(dq, dk, dv) of ``llmint8_attention`` for the gradient ``dout`` of ``out``, from its inputs and results."""
-    import torch
-    m8 = _m8()
-    lib = m8.load_library()
+    lib = _library()
     dev, dt = batch.device, q.dtype
     s = _shape(batch, q, k, scale, causal, window, sinks)
-    code = m8._act_dtype(dt)
-    wide, narrow = (batch.rows, s.q_heads, s.dim), (batch.rows, s.heads, s.dim)
+    code = _half(dt)
+    heads, dim, n = q.shape[1], q.shape[2], batch.rows
+    wide, narrow = (n, heads, dim), (n, k.shape[1], dim)
     dq = _like(q, stream) if dq is None else dq
     dk = _like(k, stream) if dk is None else dk
     dv = _like(v, stream) if dv is None else dv
     m8._need(lse, torch.float32, wide[:2], "lse")
     if lse.device != dev:
         raise ValueError(f"lse: expected on {dev}, got {lse.device}")
-    rows = {n: _rows(t, dt, narrow if n in ("k", "v", "dk", "dv") else wide, dev, n)
-            for n, t in (("q", q), ("k", k), ("v", v), ("out", out), ("dout", dout), ("dq", dq), ("dk", dk), ("dv", dv))}
+    rows = (_rows(q, dt, wide, dev, "q"), _rows(k, dt, narrow, dev, "k"), _rows(v, dt, narrow, dev, "v"),
+            _rows(out, dt, wide, dev, "out"))
+    more = (_rows(dout, dt, wide, dev, "dout"), _rows(dq, dt, wide, dev, "dq"), _rows(dk, dt, narrow, dev, "dk"),
+            _rows(dv, dt, narrow, dev, "dv"))
     if workspace is None:
-        workspace = m8._empty((max(1, 8 * batch.rows * s.q_heads),), torch.uint8, dev, stream)
+        workspace = _new((max(1, 8 * n * heads),), torch.uint8, dev, stream)
     else:
         m8._need_workspace(workspace, dev)
     with _on(dev):
-        m8._check(lib.llmint8_attention_backward(s, code, rows["q"], rows["k"], rows["v"], rows["out"], lse.data_ptr(),
-                                                 rows["dout"], rows["dq"], rows["dk"], rows["dv"],
-                                                 workspace.data_ptr(), m8._ws_bytes(workspace), _handle(stream, dev)),
+        m8._check(lib.llmint8_attention_backward(s, code, *rows, lse.data_ptr(), *more, workspace.data_ptr(),
+                                                 m8._ws_bytes(workspace), _handle(stream, dev)),
                   "llmint8_attention_backward")
     return dq, dk, dv
 
@@ -243,13 +254,10 @@ def llmint8_rope(table, pos, axis, q, k=None, interleaved=False, inverse=False, 
     ``llmint8_rope_table``). ``pos`` int32 [rows, axes] or [rows]; ``axis``: the axis of every pair
     (``rope_axes``), a list or bytes. ``inverse`` turns back, which is the gradient. The outputs are new by default;
     they may be the inputs."""
-    import torch
-    m8 = _m8()
-    lib = m8.load_library()
-    for t, name in ((q, "q"), (k, "k")):
-        _plain(t, name, "rotary")
+    lib = _library()
+    _plain((q, k), "q and k", "rotary")
     dev, dt = q.device, q.dtype
-    code = m8._act_dtype(dt)
+    code = _half(dt)
     if q.dim() != 3 or (k is not None and k.dim() != 3):
         raise ValueError("q and k: expected [rows, heads, dim]")
     n, heads, dim = q.shape
@@ -285,7 +293,7 @@ def llmint8_rope(table, pos, axis, q, k=None, interleaved=False, inverse=False, 
 
 
 def _norm_rows(t, dtype, shape, device, name):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device:
+    if t.dtype != dtype or t.shape != shape or t.device != device:
         raise ValueError(f"{name}: expected {dtype} {tuple(shape)} on {device}, got {t.dtype} {tuple(t.shape)} on "
                          f"{t.device}")
     if t.stride(1) != 1 and shape[1] > 1 and t.numel() > 0:
@@ -294,10 +302,9 @@ def _norm_rows(t, dtype, shape, device, name):
 
 
 def _norm_weight(w, K, dtype, w_dtype, device, name):
-    import torch
     if w is None:
         return None
-    if w.dtype != w_dtype or w_dtype not in (dtype, torch.float32) or tuple(w.shape) != (K,) or not w.is_contiguous() \
+    if w.dtype != w_dtype or w_dtype not in (dtype, torch.float32) or w.shape != (K,) or not w.is_contiguous() \
             or w.device != device:
         raise ValueError(f"{name}: expected contiguous [{K}] of {dtype} or fp32 on {device} (weight and bias alike), "
                          f"got {w.dtype} {tuple(w.shape)} on {w.device}")
@@ -308,22 +315,20 @@ def llmint8_layer_norm(x, weight=None, bias=None, eps=1e-5, y=None, stats=True, 
     """(y, stats): layer norm of x [rows, K] (fp16, bf16 or fp32). weight and bias [K] are of x's type or fp32, or
     None. stats fp32 [rows, 2] (what the backward call reads) is new, a tensor of the caller's, or None with
     ``stats=False``."""
-    import torch
-    m8 = _m8()
-    lib = m8.load_library()
-    for t, name in ((x, "x"), (weight, "weight"), (bias, "bias")):
-        _plain(t, name, "layer_norm")
+    lib = _library()
+    _plain((x, weight, bias), "x, weight and bias", "layer_norm")
     if x.dim() != 2 or not x.is_cuda:
         raise ValueError(f"x: expected CUDA [rows, K], got {tuple(x.shape)} on {x.device}")
     n, K = x.shape
     dev, dt = x.device, x.dtype
     code = _dtype(dt, "x")
     w_dtype = weight.dtype if weight is not None else bias.dtype if bias is not None else dt
-    w, b = (_norm_weight(t, K, dt, w_dtype, dev, name) for t, name in ((weight, "weight"), (bias, "bias")))
+    w = _norm_weight(weight, K, dt, w_dtype, dev, "weight")
+    b = _norm_weight(bias, K, dt, w_dtype, dev, "bias")
     y = _like(x, stream) if y is None else y
     xr, yr = _norm_rows(x, dt, (n, K), dev, "x"), _norm_rows(y, dt, (n, K), dev, "y")
     if stats is True:
-        stats = m8._empty((n, 2), torch.float32, dev, stream)
+        stats = _new((n, 2), torch.float32, dev, stream)
     elif stats is False:
         stats = None
     else:
@@ -336,16 +341,14 @@ def llmint8_layer_norm(x, weight=None, bias=None, eps=1e-5, y=None, stats=True, 
 
 
 def llmint8_layer_norm_workspace_bytes(rows: int, K: int) -> int:
-    return int(_m8().load_library().llmint8_layer_norm_workspace_bytes(rows, K))
+    return int(_library().llmint8_layer_norm_workspace_bytes(rows, K))
 
 
 def llmint8_layer_norm_backward(dy, x, stats, weight=None, dx=None, dw=None, db=None, sums=None, workspace=None,
                                 stream=None):
     """(dx, dw, db) of ``llmint8_layer_norm`` for the gradient ``dy`` of y, from x and its stats. dw and db take
     the weight's type; they are formed where there is a weight, or as ``sums`` says."""
-    import torch
-    m8 = _m8()
-    lib = m8.load_library()
+    lib = _library()
     if x.dim() != 2 or not x.is_cuda:
         raise ValueError(f"x: expected CUDA [rows, K], got {tuple(x.shape)} on {x.device}")
     n, K = x.shape
@@ -356,19 +359,21 @@ def llmint8_layer_norm_backward(dy, x, stats, weight=None, dx=None, dw=None, db=
     if sums is None:
         sums = given is not None
     if sums:
-        dw = m8._empty((K,), w_dtype, dev, stream) if dw is None else dw
-        db = m8._empty((K,), w_dtype, dev, stream) if db is None else db
-    w, wr, br = (_norm_weight(t, K, dt, w_dtype, dev, name) for t, name in ((weight, "weight"), (dw, "dw"), (db, "db")))
+        dw = _new((K,), w_dtype, dev, stream) if dw is None else dw
+        db = _new((K,), w_dtype, dev, stream) if db is None else db
+    w = _norm_weight(weight, K, dt, w_dtype, dev, "weight")
+    wr, br = _norm_weight(dw, K, dt, w_dtype, dev, "dw"), _norm_weight(db, K, dt, w_dtype, dev, "db")
     dx = _like(x, stream) if dx is None else dx
     m8._need(stats, torch.float32, (n, 2), "stats")
     if stats.device != dev:
         raise ValueError(f"stats: expected on {dev}, got {stats.device}")
-    gr, xr, dr = (_norm_rows(t, dt, (n, K), dev, name) for t, name in ((dy, "dy"), (x, "x"), (dx, "dx")))
+    gr, xr = _norm_rows(dy, dt, (n, K), dev, "dy"), _norm_rows(x, dt, (n, K), dev, "x")
+    dr = _norm_rows(dx, dt, (n, K), dev, "dx")
     if workspace is not None:
         m8._need_workspace(workspace, dev)
     with _on(dev):
         if workspace is None and (wr or br):
-            workspace = m8._empty((lib.llmint8_layer_norm_workspace_bytes(n, K),), torch.uint8, dev, stream)
+            workspace = _new((lib.llmint8_layer_norm_workspace_bytes(n, K),), torch.uint8, dev, stream)
         m8._check(lib.llmint8_layer_norm_backward(*gr, *xr, code, n, K, w, _dtype(w_dtype, "weight"), stats.data_ptr(),
                                                   *dr, wr, br, m8._ptr(workspace), m8._ws_bytes(workspace),
                                                   _handle(stream, dev)), "llmint8_layer_norm_backward")
@@ -387,6 +392,7 @@ class GradientSet:
     __slots__ = ("grads", "out", "device", "_arr", "_need")
 
     def __init__(self, grads, out=None):
+        _library()
         self.grads = [g for g in grads if g is not None]
         self.out = self.grads if out is None else list(out)
         if len(self.out) != len(self.grads):
@@ -398,21 +404,34 @@ class GradientSet:
                 if t.device != self.device or not t.is_cuda or not _dense(t):
                     raise ValueError(f"gradients: expected dense CUDA tensors on {self.device}, got {tuple(t.shape)} "
                                      f"with strides {t.stride()} on {t.device}")
-            if g is not o and (o.shape != g.shape or o.stride() != g.stride()):
+            if g is not o and (o.shape != g.shape or o.stride() != g.stride() and not (
+                    g.is_contiguous() and o.is_contiguous())):
                 raise ValueError(f"out: expected {tuple(g.shape)} with strides {g.stride()}, got {tuple(o.shape)} "
                                  f"with {o.stride()}")
             code, to = _dtype(g.dtype, "gradients"), _dtype(o.dtype, "out")
-            if to not in (code, _m8().LLMINT8_DTYPE_F32):
+            if to not in (code, m8.LLMINT8_DTYPE_F32):
                 raise ValueError(f"out: {g.dtype} or fp32, got {o.dtype}")
             a.data, a.out, a.n, a.dtype, a.out_dtype = g.data_ptr(), o.data_ptr(), g.numel(), code, to
         self._need = None
+        # what is written is nobody else's: a tensor that is there twice would be scaled twice, or not
+        spans = []
+        for g, o in zip(self.grads, self.out):
+            spans.append((o.data_ptr(), o.data_ptr() + o.numel() * o.element_size(), True))
+            if g.data_ptr() != o.data_ptr() or g.dtype != o.dtype:
+                spans.append((g.data_ptr(), g.data_ptr() + g.numel() * g.element_size(), False))
+        end = [0, 0]  # of what was written so far, and of what was only read
+        for first, last, written in sorted(spans):
+            if first < last:
+                if first < end[1] or (written and first < end[0]):
+                    raise ValueError("gradients: two of them, or two outputs, share memory that is written")
+                end[1 if written else 0] = max(end[1 if written else 0], last)
 
     def __len__(self):
         return len(self.grads)
 
     def workspace_bytes(self) -> int:
         if self._need is None:
-            self._need = int(_m8().load_library().llmint8_grad_norm_workspace_bytes(self._arr, len(self)))
+            self._need = int(_library().llmint8_grad_norm_workspace_bytes(self._arr, len(self)))
         return self._need
 
 
@@ -435,20 +454,18 @@ def _set(grads):
 def llmint8_grad_norm(grads, scale=1.0, norm=None, workspace=None, device=None, stream=None):
     """fp32 scalar on the device: ``scale`` times the root of the sum of all squares of ``grads`` (a GradientSet, or
     a list of tensors, None among them left out). ``device`` is needed where there are none."""
-    import torch
-    m8 = _m8()
-    lib = m8.load_library()
+    lib = _library()
     grads = _set(grads)
     dev = grads.device or torch.device(device or "cuda")
     if norm is None:
-        norm = m8._empty((), torch.float32, dev, stream)
+        norm = _new((), torch.float32, dev, stream)
     else:
         m8._need(norm, torch.float32, (), "norm")
     dev = norm.device
     if grads.device not in (None, dev):
         raise ValueError(f"norm: expected on {grads.device}, got {dev}")
     if workspace is None:
-        workspace = m8._empty((grads.workspace_bytes(),), torch.uint8, dev, stream)
+        workspace = _new((grads.workspace_bytes(),), torch.uint8, dev, stream)
     else:
         m8._need_workspace(workspace, dev)
     with _on(dev):
@@ -461,9 +478,7 @@ def llmint8_grad_clip(grads, norm, max_norm, scale=1.0, stream=None):
     """The gradients times scale min(1, max_norm / (norm + 1e-6)), written where the set says (in place for a list
     of tensors); ``norm`` is an fp32 scalar on the device (from ``llmint8_grad_norm``). Returns the tensors
     written."""
-    import torch
-    m8 = _m8()
-    lib = m8.load_library()
+    lib = _library()
     grads = _set(grads)
     m8._need(norm, torch.float32, (), "norm")
     if grads.device not in (None, norm.device):
@@ -478,7 +493,7 @@ def clip_grad_norm(parameters, max_norm, scale=1.0):
     """Clips the gradients of ``parameters`` (tensors; those without one are left out) in place, so that their norm
     is at most ``max_norm``; ``scale`` (1 / loss scale) is applied first. Returns the norm before clipping, an fp32
     scalar on the device."""
-    import torch
+    _library()
     parameters = list(parameters)
     grads = GradientSet([p.grad for p in parameters])
     if not len(grads):
@@ -501,12 +516,11 @@ def _unused(t, batch):
 
 
 def _empty_rows(shape, like, batch):
-    import torch
     return _unused(torch.empty(shape, dtype=like.dtype, device=like.device), batch)
 
 
 def _functions():
-    import torch
+    _library()
 
     class Attention(torch.autograd.Function):
         @staticmethod

@@ -32,7 +32,7 @@ __all__ = [
     "PackedRows", "llmint8_attention", "llmint8_attention_backward",
     "llmint8_attention_backward_workspace_bytes", "rope_axes", "llmint8_rope", "llmint8_layer_norm",
     "llmint8_layer_norm_backward", "llmint8_layer_norm_workspace_bytes", "GradientSet", "llmint8_grad_norm",
-    "llmint8_grad_clip", "packed_attention", "rotary", "layer_norm", "LayerNorm", "clip_grad_norm",
+    "llmint8_grad_clip", "packed_attention", "qkv_attention", "rotary", "layer_norm", "LayerNorm", "clip_grad_norm",
 ]
 
 LLMINT8_PATH_AUTO = 0
@@ -849,4 +849,5 @@ from . import training as _training  # noqa: E402
 from .training import (  # noqa: E402
     GradientSet, LayerNorm, PackedRows, clip_grad_norm, layer_norm, llmint8_attention, llmint8_attention_backward,
     llmint8_attention_backward_workspace_bytes, llmint8_grad_clip, llmint8_grad_norm, llmint8_layer_norm,
-    llmint8_layer_norm_backward, llmint8_layer_norm_workspace_bytes, llmint8_rope, packed_attention, rope_axes, rotary)
+    llmint8_layer_norm_backward, llmint8_layer_norm_workspace_bytes, llmint8_rope, packed_attention, qkv_attention, rope_axes,
+    rotary)

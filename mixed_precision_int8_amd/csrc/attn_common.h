@@ -29,23 +29,6 @@ namespace llmint8 {
 
 constexpr float kAttnNegInf = -__builtin_inff();
 
-template <int DP>
-struct AttnTile {
-  static constexpr int kPitch = DP <= 64 ? 128 : DP <= 128 ? 256 : 512;  // bytes of a row
-  static constexpr int kChunks = kPitch / 16;
-  static constexpr bool kNarrow = kPitch == 128;
-  static constexpr int kSixteen = 16 * kPitch + 64;  // bytes of 16 rows
-  static constexpr int kBytes = 4 * kSixteen;
-  static constexpr int NQ = DP / 16;  // 16-channel steps
-  static constexpr int ND = DP / 32;  // 32-channel blocks
-  static __device__ __forceinline__ constexpr int swizzle(int row) {
-    return kNarrow ? (row >> 1 & 1) << 2 | (row >> 2 & 1) : (row & 3) << 2;
-  }
-  static __device__ __forceinline__ constexpr int at(int row) {
-    return (row >> 4) * kSixteen + (row & 15) * kPitch + (kNarrow ? (row >> 3 & 1) * 32 : (row >> 2 & 3) * 16);
-  }
-};
-
 // Copies to LDS: 64 x 16 bytes (64 x 4) from the lanes' offsets to `to` on. (Functions of
 // their own, not of a template's: the host pass drops kernels whose instances use the
 // 16-byte form.)

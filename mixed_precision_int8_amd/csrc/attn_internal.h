@@ -43,6 +43,25 @@ __host__ __device__ inline AttnSeq attn_seq_of(int cu0, int cu1, int T) {
   return AttnSeq{cu0, cu1 > cu0 ? cu1 - cu0 : 0};
 }
 
+// A tile of 64 rows of a head in LDS (attn_common.h): where rows begin, and at which chunk of
+// 16 bytes of its row a chunk is kept.
+template <int DP>
+struct AttnTile {
+  static constexpr int kPitch = DP <= 64 ? 128 : DP <= 128 ? 256 : 512;  // bytes of a row
+  static constexpr int kChunks = kPitch / 16;
+  static constexpr bool kNarrow = kPitch == 128;
+  static constexpr int kSixteen = 16 * kPitch + 64;  // bytes of 16 rows
+  static constexpr int kBytes = 4 * kSixteen;
+  static constexpr int NQ = DP / 16;  // 16-channel steps
+  static constexpr int ND = DP / 32;  // 32-channel blocks
+  static __host__ __device__ constexpr int swizzle(int row) {
+    return kNarrow ? (row >> 1 & 1) << 2 | (row >> 2 & 1) : (row & 3) << 2;
+  }
+  static __host__ __device__ constexpr int at(int row) {
+    return (row >> 4) * kSixteen + (row & 15) * kPitch + (kNarrow ? (row >> 3 & 1) * 32 : (row >> 2 & 3) * 16);
+  }
+};
+
 hipError_t launch_attention(const AttnArgs& a, bool bf16, hipStream_t stream);
 hipError_t launch_attention_backward(const AttnArgs& a, bool bf16, hipStream_t stream);
 

@@ -357,35 +357,80 @@ class PagedSequences:
 
 
 class Int8SelfAttention:
-    """Self-attention of a decoder layer on int8 weights and an int8 cache: q, k, v from one Int8Linear,
-    rotated and written by ``llmint8_kv_append``, attended by ``llmint8_kv_attention``, and projected by a
-    second Int8Linear. ``qkv_weight`` is [(q_heads + 2 heads) * dim, hidden], ``out_weight`` [hidden,
-    q_heads * dim]. For serving: there is no backward through the cache, and X that requires a gradient is
-    refused (but under ``torch.no_grad()``)."""
+    """Self-attention of a decoder layer on int8 weights: q, k, v from one Int8Linear, rotated, attended, and projected
+    by a second Int8Linear. ``qkv_weight`` is [(q_heads + 2 heads) * dim, hidden], ``out_weight`` [hidden,
+    q_heads * dim]; ``norm``, if given, is applied to X first (a ``LayerNorm``).
+
+    ``forward`` serves: new tokens join an int8 cache (``llmint8_kv_append``) and attend to it
+    (``llmint8_kv_attention``). There is no backward through the cache, and X that requires a gradient is refused
+    (but under ``torch.no_grad()``). ``packed`` trains: whole sequences attend to themselves in 16 bits
+    (``packed_attention``), with gradients for X and the norm's parameters; the int8 weights stay frozen. A layer
+    that only trains needs no cache (None, with ``heads`` and ``dim``).
+
+    ``axis``: the axis of every pair of ``rope`` (``rope_axes``); the calls then take the rows' positions, ``pos``
+    int32 [rows, axes], instead of counting tokens."""
 
     def __init__(self, qkv_weight, out_weight, q_heads, cache, rope=None, interleaved=False, window=0,
-                 sinks=0, threshold=6.0):
+                 sinks=0, threshold=6.0, norm=None, axis=None, heads=None, dim=None):
         m8 = _m8()
-        if qkv_weight.shape[0] != (q_heads + 2 * cache.heads) * cache.dim:
-            raise ValueError(f"qkv_weight: expected {(q_heads + 2 * cache.heads) * cache.dim} rows, got "
+        if cache is not None:
+            heads, dim = cache.heads, cache.dim
+        elif heads is None or dim is None:
+            raise ValueError("heads and dim: needed where there is no cache")
+        if qkv_weight.shape[0] != (q_heads + 2 * heads) * dim:
+            raise ValueError(f"qkv_weight: expected {(q_heads + 2 * heads) * dim} rows, got "
                              f"{qkv_weight.shape[0]}")
+        if axis is not None and rope is None:
+            raise ValueError("axis without rope")
         self.qkv = m8.Int8Linear(qkv_weight, threshold)
         self.out = m8.Int8Linear(out_weight, threshold)
-        self.cache, self.q_heads = cache, int(q_heads)
+        self.cache, self.q_heads, self.heads, self.dim = cache, int(q_heads), int(heads), int(dim)
         self.rope, self.interleaved, self.window, self.sinks = rope, interleaved, window, sinks
+        self.norm, self.axis = norm, None if axis is None else bytes(axis)
 
-    def forward(self, X, batch):
+    def _positions(self, pos):
+        if (pos is None) != (self.axis is None):
+            raise ValueError("pos: needed with axes" if pos is None else "pos: for layers with axes")
+
+    def forward(self, X, batch, pos=None):
         """Y [rows, hidden] for the batch's new tokens X [rows, hidden], which join the cache. Rows of X past
         the batch's attend to nothing: their attention is zero."""
         import torch
+        m8 = _m8()
+        self._positions(pos)
         c, nq = self.cache, self.q_heads
+        if c is None:
+            raise ValueError("forward: the layer has no cache")
+        if self.norm is not None:
+            X = self.norm(X)
         qkv = self.qkv(X).view(X.shape[0], nq + 2 * c.heads, c.dim)
+        rope = self.rope
+        if pos is not None:
+            turn = qkv[:, :nq + c.heads]
+            m8.llmint8_rope(rope, pos, self.axis, turn, interleaved=self.interleaved, q_out=turn)
+            rope = None
         q = llmint8_kv_append(c, batch, qkv[:, nq:nq + c.heads], qkv[:, nq + c.heads:], qkv[:, :nq],
-                              self.rope, self.interleaved, q_out=qkv[:, :nq])
+                              rope, self.interleaved, q_out=qkv[:, :nq])
         # the attention writes the batch's rows only, and the second projection decides its outlier columns over
         # all rows: what memory held in the others must not reach it
         o = torch.zeros((X.shape[0], nq, c.dim), dtype=qkv.dtype, device=qkv.device)
         llmint8_kv_attention(c, batch, q, window=self.window, sinks=self.sinks, out=o)
         return self.out(o.view(X.shape[0], nq * c.dim))
+
+    def packed(self, X, rows, pos=None):
+        """Y [rows, hidden] of whole sequences X [rows, hidden] (``PackedRows``), differentiable; no cache is read
+        or written. Rows of no sequence attend to nothing."""
+        m8 = _m8()
+        self._positions(pos)
+        nq, n = self.q_heads, X.shape[0]
+        if self.norm is not None:
+            X = self.norm(X)
+        qkv = self.qkv(X).view(n, nq + 2 * self.heads, self.dim)
+        rope = None
+        if self.rope is not None:
+            axis = self.axis if pos is not None else bytes(self.rope.shape[1] // 2)
+            rope = self.rope, rows.positions() if pos is None else pos, axis, self.interleaved
+        o = m8.qkv_attention(qkv, self.heads, rows, rope, window=self.window, sinks=self.sinks)
+        return self.out(o.view(n, nq * self.dim))
 
     __call__ = forward

@@ -157,6 +157,12 @@ class PackedRows:
         return cls(torch.tensor(at, dtype=torch.int32).to(device), at[-1] if rows is None else rows,
                    max_len=max(lengths, default=0), used=at[-1])
 
+    def positions(self):
+        """int32 [rows]: every row's place in its sequence, from what cu holds now (rows of no sequence: any)."""
+        row = torch.arange(self.rows, dtype=torch.int32, device=self.device)
+        seq = torch.searchsorted(self.cu[1:], row, right=True, out_int32=True)
+        return (row - self.cu[seq]).clamp_(min=0)
+
 
 def _shape(batch, q, k, scale, causal, window, sinks):
     if q.dim() != 3 or k.dim() != 3:
@@ -525,7 +531,9 @@ def _functions():
     class Attention(torch.autograd.Function):
         @staticmethod
         def forward(ctx, q, k, v, batch, how):
+            q, k, v = _fit(q), _fit(k), _fit(v)
             out, lse = llmint8_attention(batch, q, k, v, out=_empty_rows(q.shape, q, batch), **how)
+            # cu among them, so that a backward pass after a change of cu is an error
             ctx.save_for_backward(q, k, v, out, lse, batch.cu)
             ctx.batch, ctx.how = batch, how
             return out
@@ -544,7 +552,8 @@ def _functions():
         def forward(ctx, q, k, table, pos, axis, interleaved):
             ctx.save_for_backward(table, pos)
             ctx.how = axis, interleaved
-            return llmint8_rope(table, pos, axis, q, k, interleaved)
+            return llmint8_rope(table, pos, axis, _dense_channels(q), None if k is None else _dense_channels(k),
+                                interleaved)
 
         @staticmethod
         @torch.autograd.function.once_differentiable
@@ -578,7 +587,7 @@ def _functions():
 
         @staticmethod
         def forward(ctx, qkv, heads, rope, batch, how):
-            nq = qkv.shape[1] - 2 * heads
+            nq, qkv = qkv.shape[1] - 2 * heads, _fit(qkv)
             if rope is not None:
                 table, pos, axis, interleaved = rope
                 turned, _ = llmint8_rope(table, pos, axis, qkv[:, :nq + heads], None, interleaved)
@@ -609,7 +618,7 @@ def _functions():
 
 
 def _dense_channels(t):
-    """A gradient as the kernels take it: autograd hands on expanded and strided ones."""
+    """A tensor as the kernels take it: inputs may be, and autograd hands on, expanded and strided ones."""
     strides = t.stride()
     return t if strides[-1] == 1 and 0 not in strides[:-1] and all(
         s >= t.shape[-1] for s in strides[:-1]) else t.contiguous()
@@ -639,6 +648,14 @@ def packed_attention(q, k, v, batch, scale=None, causal=True, window=0, sinks=0)
     return _fn("attention")(q, k, v, batch, how)
 
 
+def qkv_attention(qkv, heads, batch, rope=None, scale=None, causal=True, window=0, sinks=0):
+    """``packed_attention`` of a fused projection's output [rows, q_heads + 2 heads, dim] (q, k, v side by side), its q
+    and k turned by ``rope`` = (table, pos, axis, interleaved) first, with one gradient for all of qkv: the slices'
+    gradients are written side by side, where separate functions would each give one of qkv's size, to be added."""
+    how = {"scale": scale, "causal": causal, "window": window, "sinks": sinks}
+    return _fn("qkv")(qkv, heads, rope, batch, how)
+
+
 def rotary(q, k, table, pos, axis, interleaved=False):
     """(q, k) turned by ``llmint8_rope``, with gradients; k may be None."""
     return _fn("rotary")(q, k, table, pos, bytes(axis), interleaved)
@@ -648,7 +665,7 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5):
     """``llmint8_layer_norm`` over the last axis of x, with gradients for x, weight and bias."""
     shape = x.shape
     x2 = x.reshape(-1, shape[-1])
-    return _fn("norm")(x2 if x2.stride(-1) == 1 else x2.contiguous(), weight, bias, float(eps)).reshape(shape)
+    return _fn("norm")(_dense_channels(x2), weight, bias, float(eps)).reshape(shape)
 
 
 class LayerNorm:

@@ -37,13 +37,16 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_attention(AttnArgs 
   const int r = (int)min(row0 + wave * 32 + nn, rows - 1);
   const int pos = r / G, qh = h * G + (r - pos * G);
   const int64_t qrow = (int64_t)sq.row0 + pos;
-  const int pos_lo = (int)row0 / G, pos_hi = (int)(min(row0 + kRows, rows) - 1) / G;
+  auto span_of = [&](int64_t from, int64_t to) {  // of rows [from, to)
+    return AttnSpan(a, (int)(min(from, rows) / G), (int)((min(to, rows) - 1) / G), sq.n);
+  };
+  const AttnSpan all = span_of(row0, row0 + kRows);
+  const bool idle = row0 + wave * 32 >= rows;  // this wavefront has no row
+  const AttnSpan own = span_of(row0 + wave * 32, row0 + wave * 32 + 32);
 
   // tiles that any of the rows sees
-  const int end = a.causal ? pos_hi + 1 : sq.n;
-  const int hi = (end + 63) >> 6;
-  const int lo = a.window > 0 ? min(max(pos_lo - a.window + 1, 0) >> 6, hi) : 0;
-  const int sink = a.window > 0 ? min((int)(((int64_t)a.sinks + 63) >> 6), lo) : 0;
+  const int hi = (all.last >> 6) + 1, lo = min(max(all.begin, 0) >> 6, hi);
+  const int sink = min((int)(((int64_t)a.sinks + 63) >> 6), lo);
   const int tiles = sink + hi - lo;
   auto base_of = [&](int i) { return (i < sink ? i : lo + i - sink) << 6; };
 
@@ -80,79 +83,78 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_attention(AttnArgs 
 #pragma unroll
   for (int d = 0; d < ND; ++d) acc[d] = attn_zero();
   float m_run = kAttnNegInf, l_run = 0.0f;  // l_run: of this lane's tokens
-  const int all_end = a.causal ? min(pos_lo, sq.n - 1) : sq.n - 1;
-  const int all_begin = a.window > 0 ? pos_hi - a.window + 1 : 0;
   AttnRead<DP> rd(smem);
   const AttnSees sees(a, pos, sq.n);
 
-  auto is_masked = [&](int base) { return base + 63 > all_end || base < all_begin; };
   for (int i = 0; i < tiles; ++i) {
     const int stage = i & 1, base = base_of(i);
-    const bool masked = is_masked(base);
+    const bool masked = all.masked(base);
     attn_wait_copies();
     if (masked) cv.template finite<BF16>(smem + stage * kStage + Tile::kBytes, flag);
     attn_barrier();
     copy(i + 1, stage ^ 1);
 
-    // operands are read two steps ahead of their products
-    uint4 x[3][2];
+    if (!(idle | own.none(base, 64))) {
+      // operands are read two steps ahead of their products
+      uint4 x[3][2];
 #pragma unroll
-    for (int st = 0; st < 2; ++st)
+      for (int st = 0; st < 2; ++st)
 #pragma unroll
-      for (int sb = 0; sb < 2; ++sb) x[st][sb] = rd.rows(0, sb, st);
-    v16f_t s[2];
+        for (int sb = 0; sb < 2; ++sb) x[st][sb] = rd.rows(0, sb, st);
+      v16f_t s[2];
 #pragma unroll
-    for (int st = 0; st < NQ; ++st) {
+      for (int st = 0; st < NQ; ++st) {
 #pragma unroll
-      for (int sb = 0; sb < 2; ++sb) {
-        if (st + 2 < NQ) x[(st + 2) % 3][sb] = rd.rows(0, sb, st + 2);
-        s[sb] = Act16<BF16>::mma32(x[st % 3][sb], q[st], st == 0 ? attn_zero() : s[sb]);
+        for (int sb = 0; sb < 2; ++sb) {
+          if (st + 2 < NQ) x[(st + 2) % 3][sb] = rd.rows(0, sb, st + 2);
+          s[sb] = Act16<BF16>::mma32(x[st % 3][sb], q[st], st == 0 ? attn_zero() : s[sb]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    uint4 y[2][ND];
+      uint4 y[2][ND];
 #pragma unroll
-    for (int d = 0; d < ND; ++d) y[0][d] = rd.channels(1, d, 0);
-    // a lane's values 8 k .. 8 k + 7 are tokens 16 k + 8 hf .. of the tile
-    if (masked) {
+      for (int d = 0; d < ND; ++d) y[0][d] = rd.channels(1, d, 0);
+      // a lane's values 8 k .. 8 k + 7 are tokens 16 k + 8 hf .. of the tile
+      if (own.masked(base)) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < 4; ++k)
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (!sees(base + 16 * k + 8 * hf + j)) s[k >> 1][(k & 1) * 8 + j] = kAttnNegInf;
-    }
-    float mt = s[0][0];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) mt = attn_max(mt, s[0][j], s[1][j]);
-    mt = attn_pair_max(mt) * f;
-    // a row that has outgrown its maximum: what was summed moves to the new one (its own row
-    // decides, so that results do not depend on the rows beside it)
-    if (__any(mt > m_run + 7.0f)) {
-      const float m_new = mt > m_run + 7.0f ? mt : m_run;
-      const float alpha = m_run == kAttnNegInf ? 0.0f : __builtin_amdgcn_exp2f(m_run - m_new);
-      m_run = m_new;
-      l_run *= alpha;
-#pragma unroll
-      for (int d = 0; d < ND; ++d) acc[d] *= alpha;
-    }
-    const float off = m_run == kAttnNegInf ? 0.0f : 8.0f - m_run;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (k < 3) {
-#pragma unroll
-        for (int d = 0; d < ND; ++d) y[(k + 1) & 1][d] = rd.channels(1, d, k + 1);
+          for (int j = 0; j < 8; ++j)
+            if (!sees(base + 16 * k + 8 * hf + j)) s[k >> 1][(k & 1) * 8 + j] = kAttnNegInf;
       }
-      float w[8];
+      float mt = s[0][0];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        w[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k >> 1][(k & 1) * 8 + j], f, off));
-        l_run += w[j];
+      for (int j = 0; j < 16; ++j) mt = attn_max(mt, s[0][j], s[1][j]);
+      mt = attn_pair_max(mt) * f;
+      // a row that has outgrown its maximum: what was summed moves to the new one (its own row
+      // decides, so that results do not depend on the rows beside it)
+      if (__any(mt > m_run + 7.0f)) {
+        const float m_new = mt > m_run + 7.0f ? mt : m_run;
+        const float alpha = m_run == kAttnNegInf ? 0.0f : __builtin_amdgcn_exp2f(m_run - m_new);
+        m_run = m_new;
+        l_run *= alpha;
+#pragma unroll
+        for (int d = 0; d < ND; ++d) acc[d] *= alpha;
       }
-      const uint4 p = make_uint4(Act16<BF16>::pack2(w[0], w[1]), Act16<BF16>::pack2(w[2], w[3]),
-                                 Act16<BF16>::pack2(w[4], w[5]), Act16<BF16>::pack2(w[6], w[7]));
+      const float off = m_run == kAttnNegInf ? 0.0f : 8.0f - m_run;
 #pragma unroll
-      for (int d = 0; d < ND; ++d) acc[d] = Act16<BF16>::mma32(y[k & 1][d], p, acc[d]);
-      __builtin_amdgcn_sched_barrier(0);
+      for (int k = 0; k < 4; ++k) {
+        if (k < 3) {
+#pragma unroll
+          for (int d = 0; d < ND; ++d) y[(k + 1) & 1][d] = rd.channels(1, d, k + 1);
+        }
+        float w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          w[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k >> 1][(k & 1) * 8 + j], f, off));
+          l_run += w[j];
+        }
+        const uint4 p = make_uint4(Act16<BF16>::pack2(w[0], w[1]), Act16<BF16>::pack2(w[2], w[3]),
+                                   Act16<BF16>::pack2(w[4], w[5]), Act16<BF16>::pack2(w[6], w[7]));
+#pragma unroll
+        for (int d = 0; d < ND; ++d) acc[d] = Act16<BF16>::mma32(y[k & 1][d], p, acc[d]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
     rd.next(stage ? -kStage : kStage);
   }
@@ -161,7 +163,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_attention(AttnArgs 
 #pragma unroll 1
     for (int i = 0; i < tiles; ++i) {
       const int base = base_of(i);
-      if (is_masked(base))
+      if (all.masked(base))
         attn_others<DP, BF16>(acc, vp, a.v.token, base, sq.n, D, [&](int t) { return sees(base + t); });
     }
   }

@@ -44,6 +44,40 @@ struct Reach {
   }
 };
 
+// A lane's channels of a row: times `by`, rounded, to row `row` of head h.
+template <int DP, bool BF16>
+__device__ __forceinline__ void store_sums(const v16f_t (&acc)[DP / 32], float by, const KvRows& to, int64_t row, int h,
+                                           int dim, int hf) {
+  uint16_t* p = to.p + row * to.token + (int64_t)h * to.head;
+#pragma unroll
+  for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int c = d * 32 + 8 * k + 4 * hf;
+      if (c >= dim) continue;
+      *reinterpret_cast<uint2*>(p + c) =
+          make_uint2(Act16<BF16>::pack2(acc[d][4 * k] * by, acc[d][4 * k + 1] * by),
+                     Act16<BF16>::pack2(acc[d][4 * k + 2] * by, acc[d][4 * k + 3] * by));
+    }
+}
+
+// What tokens j0 .. j_hi of k and v are seen by: rows [first, end) at most; token `col`, this
+// lane's, by rows [from, until).
+struct AttnRowsOf {
+  int first, end, from, until, all_from, all_until;
+  __device__ __forceinline__ AttnRowsOf(const AttnArgs& a, int n, int j0, int j_hi, int col) {
+    first = a.causal ? j0 : 0;
+    end = a.window > 0 && j0 >= a.sinks ? (int)min((int64_t)n, (int64_t)j_hi + a.window) : n;
+    from = a.causal ? col : 0;
+    until = a.window > 0 && col >= a.sinks ? (int)min((int64_t)n, (int64_t)col + a.window) : n;
+    all_from = a.causal ? j_hi : 0;
+    all_until = a.window > 0 && j_hi >= a.sinks ? max(j0, (int)min((int64_t)a.sinks, (int64_t)j_hi)) + a.window : INT32_MAX;
+  }
+  __device__ __forceinline__ bool operator()(int row) const { return (row >= from) & (row < until); }
+  // a tile that some of the tokens do not see whole
+  __device__ __forceinline__ bool masked(int base) const { return (base < all_from) | (base + 64 > all_until); }
+};
+
 }  // namespace
 
 template <int DP, bool BF16>
@@ -64,13 +98,16 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_dq(AttnArgs a) {
   const int r = (int)min(row0 + wave * 32 + nn, rows - 1);
   const int pos = r / G, qh = h * G + (r - pos * G);
   const int64_t qrow = (int64_t)sq.row0 + pos;
-  const int pos_lo = (int)row0 / G, pos_hi = (int)(min(row0 + kRows, rows) - 1) / G;
+  auto span_of = [&](int64_t from, int64_t to) {  // of rows [from, to)
+    return AttnSpan(a, (int)(min(from, rows) / G), (int)((min(to, rows) - 1) / G), sq.n);
+  };
+  const AttnSpan all = span_of(row0, row0 + kRows);
+  const bool idle = row0 + wave * 32 >= rows;  // this wavefront has no row
+  const AttnSpan own = span_of(row0 + wave * 32, row0 + wave * 32 + 32);
 
   // tiles that any of the rows sees
-  const int end = a.causal ? pos_hi + 1 : sq.n;
-  const int hi = (end + 63) >> 6;
-  const int lo = a.window > 0 ? min(max(pos_lo - a.window + 1, 0) >> 6, hi) : 0;
-  const int sink = a.window > 0 ? min((int)(((int64_t)a.sinks + 63) >> 6), lo) : 0;
+  const int hi = (all.last >> 6) + 1, lo = min(max(all.begin, 0) >> 6, hi);
+  const int sink = min((int)(((int64_t)a.sinks + 63) >> 6), lo);
   const int tiles = sink + hi - lo;
   auto base_of = [&](int i) { return (i < sink ? i : lo + i - sink) << 6; };
 
@@ -125,21 +162,19 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_dq(AttnArgs a) {
 #pragma unroll
   for (int d = 0; d < ND; ++d) acc[d] = attn_zero();
   Reach<BF16, ND> reach;
-  const int all_end = a.causal ? min(pos_lo, sq.n - 1) : sq.n - 1;
-  const int all_begin = a.window > 0 ? pos_hi - a.window + 1 : 0;
   AttnRead<DP> rd(smem);
   const AttnSees sees(a, pos, sq.n);
 
-  auto is_masked = [&](int base) { return base + 63 > all_end || base < all_begin; };
   for (int i = 0; i < tiles; ++i) {
     const int stage = i & 1, base = base_of(i);
-    const bool masked = is_masked(base);
+    const bool masked = all.masked(base);
     attn_wait_copies();
     if (masked) ck.template finite<BF16>(smem + stage * kStage, flag);
     attn_barrier();
     copy(i + 1, stage ^ 1);
 #pragma unroll
     for (int sb = 0; sb < 2; ++sb) {
+      if (idle | own.none(base + 32 * sb, 32)) continue;
       v16f_t s = attn_rows_product<DP, BF16>(rd, 0, sb, q);
       v16f_t t = attn_rows_product<DP, BF16>(rd, 1, sb, g);
       uint4 y[2][ND];
@@ -147,7 +182,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_dq(AttnArgs a) {
       for (int d = 0; d < ND; ++d) y[0][d] = rd.channels(0, d, 2 * sb);
 #pragma unroll
       for (int x = 0; x < 16; ++x) t[x] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x], f, -lse2)) * (t[x] - delta);
-      if (masked) {
+      if (own.masked(base)) {
 #pragma unroll
         for (int x = 0; x < 16; ++x)
           if (!sees(base + 32 * sb + 16 * (x >> 3) + 8 * hf + (x & 7))) t[x] = 0.0f;
@@ -175,24 +210,154 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_dq(AttnArgs a) {
 #pragma unroll 1
     for (int i = 0; i < tiles; ++i) {
       const int base = base_of(i);
-      if (is_masked(base))
+      if (all.masked(base))
         attn_others<DP, BF16>(acc, kp, a.k.token, base, sq.n, D, [&](int t) { return sees(base + t); });
     }
   }
 
   if (!mine) return;
-  const float by = a.scale / reach.g;
-  uint16_t* op = a.dq.p + qrow * a.dq.token + (int64_t)qh * a.dq.head;
+  store_sums<DP, BF16>(acc, a.scale / reach.g, a.dq, qrow, qh, D, hf);
+}
+
+// Up to 96 channels a wavefront has the registers for dV and dK of 32 tokens, two to a SIMD.
+template <int DP, bool BF16>
+__global__ __launch_bounds__(256, 2) void ka_dkv_alone(AttnArgs a) {
+  using Tile = AttnTile<DP>;
+  constexpr int W = 4, kCols = 32 * W, NQ = Tile::NQ, ND = Tile::ND;
+  constexpr int kStage = 2 * Tile::kBytes;  // q, do
+  // lse, delta of the stages and a place that the other wavefronts' go to; a flag
+  constexpr int kAtStat = 2 * kStage, kAtFlag = kAtStat + 2 * 512 + 256;
+  __shared__ __attribute__((aligned(1024))) char smem[kAtFlag + 16];
+  int* const flag = reinterpret_cast<int*>(smem + kAtFlag);
+  const int D = a.dim, H = a.heads, G = a.q_heads / H;
+  const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
+  const int hf = lane >> 5, nn = lane & 31;
+  const int h = (int)(blockIdx.x % H), item = (int)(blockIdx.x / H);
+  AttnSeq sq;
+  int run;
+  if (!attn_place<false>(a, item, 1, 7, &sq, &run)) return;
+  const int j0 = run * kCols;
+  const int col = j0 + wave * 32 + nn, j = min(col, sq.n - 1), j_hi = min(j0 + kCols, sq.n) - 1;
+
+  const AttnRowsOf see(a, sq.n, j0, j_hi, col);
+  const int w0 = j0 + wave * 32;
+  const AttnRowsOf own(a, sq.n, w0, min(w0 + 31, sq.n - 1), col);  // of this wavefront's tokens
+  const bool idle = w0 >= sq.n;
+  const int lo = see.first >> 6, per = ((see.end + 63) >> 6) - lo, tiles = per * G;
+
+  const AttnCopy<DP, W> cq(a.q.token, D), cg(a.d_o.token, D);
+  const uint16_t* qp = a.q.p + (int64_t)sq.row0 * a.q.token + (int64_t)h * G * a.q.head;
+  const uint16_t* gp = a.d_o.p + (int64_t)sq.row0 * a.d_o.token + (int64_t)h * G * a.d_o.head;
+  const float* sp = a.stat + (int64_t)h * G * a.T + sq.row0;
+  int c_head = 0, c_at = lo;  // the tile that is copied next
+  auto copy = [&](int stage) {
+    const int base = c_at << 6, n = c_head < G ? sq.n : 0;  // past the last tile: zeros
+    char* to = smem + stage * kStage;
+    cq.issue(qp + (int64_t)c_head * a.q.head, a.q.token, base, n, to);
+    cg.issue(gp + (int64_t)c_head * a.d_o.head, a.d_o.token, base, n, to + Tile::kBytes);
+    const float* p = sp + (int64_t)c_head * a.T + base + (wave ? (int64_t)a.q_heads * a.T : 0);
+    attn_copy4(make_rsrc(reinterpret_cast<const float*>(uniform((int64_t)p)),
+                         (uint32_t)uniform(wave < 2 ? max(min(n - base, 64), 0) * 4 : 0)),
+               smem + kAtStat + uniform(wave < 2 ? stage * 512 + wave * 256 : 1024), (uint32_t)lane * 4);
+    if (++c_at == lo + per) c_at = lo, ++c_head;
+  };
+  copy(0);
+  if (threadIdx.x == 0) *flag = 0;
+  attn_barrier();
+
+  uint4 kr[NQ], vr[NQ];
+  {
+    const uint16_t* kp = a.k.p + ((int64_t)sq.row0 + j) * a.k.token + (int64_t)h * a.k.head;
+    const uint16_t* vp = a.v.p + ((int64_t)sq.row0 + j) * a.v.token + (int64_t)h * a.v.head;
+    const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
 #pragma unroll
-  for (int d = 0; d < ND; ++d)
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int c = d * 32 + 8 * k + 4 * hf;
-      if (c >= D) continue;
-      *reinterpret_cast<uint2*>(op + c) =
-          make_uint2(Act16<BF16>::pack2(acc[d][4 * k] * by, acc[d][4 * k + 1] * by),
-                     Act16<BF16>::pack2(acc[d][4 * k + 2] * by, acc[d][4 * k + 3] * by));
+    for (int ks = 0; ks < NQ; ++ks) {
+      const int c0 = ks * 16 + hf * 8;
+      kr[ks] = vr[ks] = make_uint4(0, 0, 0, 0);
+      if (c0 < D) {
+        kr[ks] = *reinterpret_cast<const uint4*>(kp + c0);
+        kr[ks] = make_uint4(kr[ks].x ^ flip, kr[ks].y ^ flip, kr[ks].z ^ flip, kr[ks].w ^ flip);
+        vr[ks] = *reinterpret_cast<const uint4*>(vp + c0);
+      }
     }
+  }
+  const float f = fabsf(a.scale) * 1.44269504088896341f;
+
+  v16f_t dv[ND], dk[ND];
+#pragma unroll
+  for (int d = 0; d < ND; ++d) dv[d] = dk[d] = attn_zero();
+  Reach<BF16, ND> reach;
+  AttnRead<DP> rd(smem);
+  const char* st = smem + kAtStat + 32 * hf;
+  int at = lo;
+  for (int i = 0; i < tiles; ++i) {
+    const int stage = i & 1, base = at << 6;
+    const bool masked = see.masked(base), hidden = own.masked(base);
+    attn_wait_copies();
+    if (masked) {
+      cq.template finite<BF16>(smem + stage * kStage, flag);
+      cg.template finite<BF16>(smem + stage * kStage + Tile::kBytes, flag);
+    }
+    attn_barrier();
+    copy(stage ^ 1);
+#pragma unroll
+    for (int sb = 0; sb < 2; ++sb) {
+      if (idle | (base + 32 * sb + 32 <= own.first) | (base + 32 * sb >= own.end)) continue;
+      auto stat = [&](int which, int e) {
+        return *reinterpret_cast<const v4f*>(st + 256 * which + 128 * sb + 64 * (e >> 1) + 16 * (e & 1));
+      };
+      v16f_t s = attn_rows_product<DP, BF16>(rd, 0, sb, kr);
+      v16f_t t = attn_rows_product<DP, BF16>(rd, 1, sb, vr);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const v4f l = stat(0, e);
+#pragma unroll
+        for (int z = 0; z < 4; ++z) s[4 * e + z] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[4 * e + z], f, l[z]));
+      }
+      if (hidden) {
+#pragma unroll
+        for (int z = 0; z < 16; ++z)
+          if (!see(base + 32 * sb + 16 * (z >> 3) + 8 * hf + (z & 7))) s[z] = 0.0f;
+      }
+      attn_channels_product<DP, BF16>(rd, 1, sb, s, dv);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const v4f l = stat(1, e);
+#pragma unroll
+        for (int z = 0; z < 4; ++z) t[4 * e + z] = s[4 * e + z] * (t[4 * e + z] - l[z]);
+      }
+      if (hidden) {  // do is not finite in a row that this token does not see, or its delta
+#pragma unroll
+        for (int z = 0; z < 16; ++z)
+          if (!see(base + 32 * sb + 16 * (z >> 3) + 8 * hf + (z & 7))) t[z] = 0.0f;
+      }
+      if constexpr (!BF16) {
+        reach.fit(t, dk);
+        t *= reach.g;
+      }
+      attn_channels_product<DP, BF16>(rd, 0, sb, t, dk);
+    }
+    rd.next(stage ? -kStage : kStage);
+    st += stage ? -512 : 512;
+    if (++at == lo + per) at = lo;
+  }
+  attn_wait_copies();
+  if (__builtin_expect(uniform(*flag), 0)) {
+#pragma unroll 1
+    for (int i = 0; i < tiles; ++i) {
+      const int base = (lo + i % per) << 6;
+      if (!see.masked(base)) continue;
+      auto sees = [&](int t) { return see(base + t); };
+      attn_others<DP, BF16>(dv, gp + (int64_t)(i / per) * a.d_o.head, a.d_o.token, base, sq.n, D, sees);
+      attn_others<DP, BF16>(dk, qp + (int64_t)(i / per) * a.q.head, a.q.token, base, sq.n, D, sees);
+    }
+  }
+
+  if (col >= sq.n) return;
+  // P carries 2^15 in fp16; dS its column's power of two as well
+  constexpr float kBy = BF16 ? 1.0f : 3.0517578125e-5f;
+  store_sums<DP, BF16>(dv, kBy, a.dv, sq.row0 + j, h, D, hf);
+  store_sums<DP, BF16>(dk, kBy * (a.scale / reach.g), a.dk, sq.row0 + j, h, D, hf);
 }
 
 // Two wavefronts share 32 tokens: one forms S and P and sums dV, the other do V^T and dS
@@ -222,11 +387,8 @@ __global__ __launch_bounds__(DP <= 128 ? 512 : 256, DP <= 128 ? 2 : 1) void ka_d
   const int j0 = run * kCols;
   const int col = j0 + pair * 32 + nn, j = min(col, sq.n - 1), j_hi = min(j0 + kCols, sq.n) - 1;
 
-  // rows that see any of the tokens
-  const int first = a.causal ? j0 : 0;
-  int end = sq.n;
-  if (a.window > 0 && j0 >= a.sinks) end = (int)min((int64_t)sq.n, (int64_t)j_hi + a.window);
-  const int lo = first >> 6, per = ((end + 63) >> 6) - lo, tiles = per * G;
+  const AttnRowsOf see(a, sq.n, j0, j_hi, col);
+  const int lo = see.first >> 6, per = ((see.end + 63) >> 6) - lo, tiles = per * G;
 
   const AttnCopy<DP, W> cq(a.q.token, D), cg(a.d_o.token, D);
   const uint16_t* qp = a.q.p + (int64_t)sq.row0 * a.q.token + (int64_t)h * G * a.q.head;
@@ -270,13 +432,6 @@ __global__ __launch_bounds__(DP <= 128 ? 512 : 256, DP <= 128 ? 2 : 1) void ka_d
 #pragma unroll
   for (int d = 0; d < ND; ++d) acc[d] = attn_zero();
   Reach<BF16, ND> reach;
-  // this lane's token is seen by rows i in [j, until) of a causal sequence, all of another
-  const int from = a.causal ? col : 0;
-  const int until = a.window > 0 && col >= a.sinks ? (int)min((int64_t)sq.n, (int64_t)col + a.window) : sq.n;
-  // tiles that begin from here on and end before there are seen whole by all columns
-  const int all_from = a.causal ? j_hi : 0;
-  const int all_until = a.window > 0 && j_hi >= a.sinks ? max(j0, (int)min((int64_t)a.sinks, (int64_t)j_hi)) + a.window : INT32_MAX;
-  auto is_masked = [&](int base) { return base < all_from || base + 64 > all_until; };
 
   // A step takes 32 rows of a tile. The second wavefront is a step behind the first, so that
   // P is there when it asks for it and neither waits for the other: one barrier to a step, P
@@ -293,7 +448,7 @@ __global__ __launch_bounds__(DP <= 128 ? 512 : 256, DP <= 128 ? 2 : 1) void ka_d
     const int base = w_at << 6;
     if (++w_at == lo + per) w_at = lo;
     attn_wait_copies();
-    if (tile < tiles && is_masked(base)) {
+    if (tile < tiles && see.masked(base)) {
       char* at = smem + tile % kStages * kStage;
       cq.template finite<BF16>(at, flag);
       cg.template finite<BF16>(at + Tile::kBytes, flag);
@@ -322,7 +477,7 @@ __global__ __launch_bounds__(DP <= 128 ? 512 : 256, DP <= 128 ? 2 : 1) void ka_d
     if (k & 1) copy();
     if (my >= 0 && my < 2 * tiles) {
       const int sb = my & 1, base = (my_at << 6) + 32 * sb;
-      const bool masked = is_masked(my_at << 6);
+      const bool masked = see.masked(my_at << 6);
       v4f* p = p_mine + sb * kPairs * 256;
       v4f l[4], w[4];
 #pragma unroll
@@ -359,7 +514,7 @@ __global__ __launch_bounds__(DP <= 128 ? 512 : 256, DP <= 128 ? 2 : 1) void ka_d
 #pragma unroll
         for (int z = 0; z < 16; ++z) {
           const int row = base + 16 * (z >> 3) + 8 * hf + (z & 7);
-          if (!((row >= from) & (row < until))) s[z] = 0.0f;
+          if (!see(row)) s[z] = 0.0f;
         }
       }
       if (!second) {
@@ -398,30 +553,20 @@ __global__ __launch_bounds__(DP <= 128 ? 512 : 256, DP <= 128 ? 2 : 1) void ka_d
 #pragma unroll 1
     for (int i = 0; i < tiles; ++i) {
       const int at = (lo + i % per) << 6;
-      auto see = [&](int t) { return (at + t >= from) & (at + t < until); };
-      if (is_masked(at)) attn_others<DP, BF16>(acc, (second ? qp : gp) + (int64_t)(i / per) * r.head, r.token, at, sq.n, D, see);
+      auto sees = [&](int t) { return see(at + t); };
+      if (see.masked(at)) attn_others<DP, BF16>(acc, (second ? qp : gp) + (int64_t)(i / per) * r.head, r.token, at, sq.n, D, sees);
     }
   }
 
   if (col >= sq.n) return;
   // P carries 2^15 in fp16; dS its column's power of two as well
   const float by = (BF16 ? 1.0f : 3.0517578125e-5f) * (second ? a.scale / reach.g : 1.0f);
-  const KvRows& to = second ? a.dk : a.dv;
-  uint16_t* op = to.p + ((int64_t)sq.row0 + j) * to.token + (int64_t)h * to.head;
-#pragma unroll
-  for (int d = 0; d < ND; ++d)
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int c = d * 32 + 8 * k + 4 * hf;
-      if (c >= D) continue;
-      *reinterpret_cast<uint2*>(op + c) =
-          make_uint2(Act16<BF16>::pack2(acc[d][4 * k] * by, acc[d][4 * k + 1] * by),
-                     Act16<BF16>::pack2(acc[d][4 * k + 2] * by, acc[d][4 * k + 3] * by));
-    }
+  store_sums<DP, BF16>(acc, by, second ? a.dk : a.dv, sq.row0 + j, h, D, hf);
 }
 
 template <int DP, bool BF16>
 static hipError_t launch_bwd(const AttnArgs& a, hipStream_t stream) {
+  constexpr bool kAlone = DP <= 96;
   constexpr int kShift = DP <= 128 ? 7 : 6;
   const int64_t rows = (((int64_t)a.T * (a.q_heads / a.heads) >> 7) + a.B) * a.heads;
   const int64_t cols = (((int64_t)a.T >> kShift) + a.B) * a.heads;
@@ -429,7 +574,8 @@ static hipError_t launch_bwd(const AttnArgs& a, hipStream_t stream) {
   hipLaunchKernelGGL((ka_dq<DP, BF16>), dim3((unsigned)rows), dim3(256), 0, stream, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((ka_dkv<DP, BF16>), dim3((unsigned)cols), dim3(DP <= 128 ? 512 : 256), 0, stream, a);
+  if constexpr (kAlone) hipLaunchKernelGGL((ka_dkv_alone<DP, BF16>), dim3((unsigned)cols), dim3(256), 0, stream, a);
+  else hipLaunchKernelGGL((ka_dkv<DP, BF16>), dim3((unsigned)cols), dim3(DP <= 128 ? 512 : 256), 0, stream, a);
   return hipGetLastError();
 }
 

@@ -251,6 +251,24 @@ struct AttnSees {
   __device__ __forceinline__ bool operator()(int j) const { return (j <= last) & ((j > from) | (j < sinks)); }
 };
 
+// What rows at tokens lo .. hi of a sequence of n see: `last` and `begin` bound what any of them
+// does, all_end and all_begin what all do (but for sinks).
+struct AttnSpan {
+  int last, begin, all_end, all_begin, sinks;
+  __device__ __forceinline__ AttnSpan(const AttnArgs& a, int lo, int hi, int n)
+      : last(a.causal ? min(hi, n - 1) : n - 1),
+        begin(a.window > 0 ? lo - a.window + 1 : 0),
+        all_end(a.causal ? min(lo, n - 1) : n - 1),
+        all_begin(a.window > 0 ? hi - a.window + 1 : 0),
+        sinks(a.sinks) {}
+  // of the tile of 64 tokens from base on some row does not see some token
+  __device__ __forceinline__ bool masked(int base) const { return (base + 63 > all_end) | (base < all_begin); }
+  // no row sees any of `len` tokens from base on
+  __device__ __forceinline__ bool none(int base, int len) const {
+    return (base > last) | ((base + len <= begin) & (base >= sinks));
+  }
+};
+
 // The largest of three, NaN if one of them is (one instruction; fmaxf costs two more, as it
 // takes the other one and quiets its operands first).
 __device__ __forceinline__ float attn_max(float a, float b, float c) {

@@ -50,13 +50,14 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_attention(AttnArgs 
   const int tiles = sink + hi - lo;
   auto base_of = [&](int i) { return (i < sink ? i : lo + i - sink) << 6; };
 
-  const AttnCopy<DP, W> ck(a.k.token, D), cv(a.v.token, D);
   const uint16_t* kp = a.k.p + (int64_t)sq.row0 * a.k.token + (int64_t)h * a.k.head;
   const uint16_t* vp = a.v.p + (int64_t)sq.row0 * a.v.token + (int64_t)h * a.v.head;
+  const int start = base_of(0), past = (lo - sink + 1) * 64;  // past: from the last tile of the sinks to the next
+  AttnStream<DP, W> ck(kp, a.k.token, D, start, past * a.k.token), cv(vp, a.v.token, D, start, past * a.v.token);
   auto copy = [&](int i, int stage) {
-    const int n = i < tiles ? sq.n : 0;  // past the last tile: zeros, to keep the loop free of branches
-    ck.issue(kp, a.k.token, base_of(i), n, smem + stage * kStage);
-    cv.issue(vp, a.v.token, base_of(i), n, smem + stage * kStage + Tile::kBytes);
+    const int n = i < tiles ? min(sq.n - base_of(i), 64) : 0;  // past the last tile: zeros, to keep the loop free of branches
+    ck.next(n, smem + stage * kStage, i + 1 == sink);
+    cv.next(n, smem + stage * kStage + Tile::kBytes, i + 1 == sink);
   };
   copy(0, 0);
   if (threadIdx.x == 0) *flag = 0;

@@ -111,13 +111,14 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_dq(AttnArgs a) {
   const int tiles = sink + hi - lo;
   auto base_of = [&](int i) { return (i < sink ? i : lo + i - sink) << 6; };
 
-  const AttnCopy<DP, W> ck(a.k.token, D), cv(a.v.token, D);
   const uint16_t* kp = a.k.p + (int64_t)sq.row0 * a.k.token + (int64_t)h * a.k.head;
   const uint16_t* vp = a.v.p + (int64_t)sq.row0 * a.v.token + (int64_t)h * a.v.head;
+  const int start = base_of(0), past = (lo - sink + 1) * 64;  // past: from the last tile of the sinks to the next
+  AttnStream<DP, W> ck(kp, a.k.token, D, start, past * a.k.token), cv(vp, a.v.token, D, start, past * a.v.token);
   auto copy = [&](int i, int stage) {
-    const int n = i < tiles ? sq.n : 0;  // past the last tile: zeros, to keep the loop free of branches
-    ck.issue(kp, a.k.token, base_of(i), n, smem + stage * kStage);
-    cv.issue(vp, a.v.token, base_of(i), n, smem + stage * kStage + Tile::kBytes);
+    const int n = i < tiles ? min(sq.n - base_of(i), 64) : 0;  // past the last tile: zeros, to keep the loop free of branches
+    ck.next(n, smem + stage * kStage, i + 1 == sink);
+    cv.next(n, smem + stage * kStage + Tile::kBytes, i + 1 == sink);
   };
   copy(0, 0);
   if (threadIdx.x == 0) *flag = 0;
@@ -245,21 +246,25 @@ __global__ __launch_bounds__(256, 2) void ka_dkv_alone(AttnArgs a) {
   const bool idle = w0 >= sq.n;
   const int lo = see.first >> 6, per = ((see.end + 63) >> 6) - lo, tiles = per * G;
 
-  const AttnCopy<DP, W> cq(a.q.token, D), cg(a.d_o.token, D);
   const uint16_t* qp = a.q.p + (int64_t)sq.row0 * a.q.token + (int64_t)h * G * a.q.head;
   const uint16_t* gp = a.d_o.p + (int64_t)sq.row0 * a.d_o.token + (int64_t)h * G * a.d_o.head;
-  const float* sp = a.stat + (int64_t)h * G * a.T + sq.row0;
-  int c_head = 0, c_at = lo;  // the tile that is copied next
-  auto copy = [&](int stage) {
-    const int base = c_at << 6, n = c_head < G ? sq.n : 0;  // past the last tile: zeros
-    char* to = smem + stage * kStage;
-    cq.issue(qp + (int64_t)c_head * a.q.head, a.q.token, base, n, to);
-    cg.issue(gp + (int64_t)c_head * a.d_o.head, a.d_o.token, base, n, to + Tile::kBytes);
-    const float* p = sp + (int64_t)c_head * a.T + base + (wave ? (int64_t)a.q_heads * a.T : 0);
-    attn_copy4(make_rsrc(reinterpret_cast<const float*>(uniform((int64_t)p)),
-                         (uint32_t)uniform(wave < 2 ? max(min(n - base, 64), 0) * 4 : 0)),
-               smem + kAtStat + uniform(wave < 2 ? stage * 512 + wave * 256 : 1024), (uint32_t)lane * 4);
-    if (++c_at == lo + per) c_at = lo, ++c_head;
+  const int64_t back = (int64_t)(per - 1) * 64;  // from a head's last tile to the next one's first
+  AttnStream<DP, W> cq(qp, a.q.token, D, (int64_t)lo * 64, a.q.head - back * a.q.token);
+  AttnStream<DP, W> cg(gp, a.d_o.token, D, (int64_t)lo * 64, a.d_o.head - back * a.d_o.token);
+  const float* sp = a.stat + (int64_t)h * G * a.T + sq.row0 + lo * 64 + (wave ? (int64_t)a.q_heads * a.T : 0);
+  int left = tiles, c_at = lo;  // tiles to copy, the next one
+  auto copy = [&](int c_stage) {
+    // past the last tile: zeros
+    const int n = left > 0 ? min(sq.n - c_at * 64, 64) : 0;
+    const bool jump = ++c_at == lo + per;
+    char* to = smem + c_stage * kStage;
+    cq.next(n, to, jump);
+    cg.next(n, to + Tile::kBytes, jump);
+    attn_copy4(make_rsrc(reinterpret_cast<const float*>(uniform(reinterpret_cast<int64_t>(sp))), (uint32_t)uniform(wave < 2 ? n * 4 : 0)),
+               smem + kAtStat + uniform(wave < 2 ? c_stage * 512 + wave * 256 : 2 * 512), (uint32_t)lane * 4);
+    sp += jump ? a.T - back : 64;
+    if (jump) c_at = lo;
+    --left;
   };
   copy(0);
   if (threadIdx.x == 0) *flag = 0;
@@ -390,21 +395,25 @@ __global__ __launch_bounds__(DP <= 128 ? 512 : 256, DP <= 128 ? 2 : 1) void ka_d
   const AttnRowsOf see(a, sq.n, j0, j_hi, col);
   const int lo = see.first >> 6, per = ((see.end + 63) >> 6) - lo, tiles = per * G;
 
-  const AttnCopy<DP, W> cq(a.q.token, D), cg(a.d_o.token, D);
   const uint16_t* qp = a.q.p + (int64_t)sq.row0 * a.q.token + (int64_t)h * G * a.q.head;
   const uint16_t* gp = a.d_o.p + (int64_t)sq.row0 * a.d_o.token + (int64_t)h * G * a.d_o.head;
-  const float* sp = a.stat + (int64_t)h * G * a.T + sq.row0;
-  int c_head = 0, c_at = lo, c_stage = 0;  // the tile that is copied next
+  const int64_t back = (int64_t)(per - 1) * 64;  // from a head's last tile to the next one's first
+  AttnStream<DP, W> cq(qp, a.q.token, D, (int64_t)lo * 64, a.q.head - back * a.q.token);
+  AttnStream<DP, W> cg(gp, a.d_o.token, D, (int64_t)lo * 64, a.d_o.head - back * a.d_o.token);
+  const float* sp = a.stat + (int64_t)h * G * a.T + sq.row0 + lo * 64 + (wave ? (int64_t)a.q_heads * a.T : 0);
+  int left = tiles, c_at = lo, c_stage = 0;  // tiles to copy, the next one
   auto copy = [&]() {
-    const int base = c_at << 6, n = c_head < G ? sq.n : 0;  // past the last tile: zeros
+    // past the last tile: zeros
+    const int n = left > 0 ? min(sq.n - c_at * 64, 64) : 0;
+    const bool jump = ++c_at == lo + per;
     char* to = smem + c_stage * kStage;
-    cq.issue(qp + (int64_t)c_head * a.q.head, a.q.token, base, n, to);
-    cg.issue(gp + (int64_t)c_head * a.d_o.head, a.d_o.token, base, n, to + Tile::kBytes);
-    const float* p = sp + (int64_t)c_head * a.T + base + (wave ? (int64_t)a.q_heads * a.T : 0);
-    attn_copy4(make_rsrc(reinterpret_cast<const float*>(uniform((int64_t)p)),
-                         (uint32_t)uniform(wave < 2 ? max(min(n - base, 64), 0) * 4 : 0)),
+    cq.next(n, to, jump);
+    cg.next(n, to + Tile::kBytes, jump);
+    attn_copy4(make_rsrc(reinterpret_cast<const float*>(uniform(reinterpret_cast<int64_t>(sp))), (uint32_t)uniform(wave < 2 ? n * 4 : 0)),
                smem + kAtStat + uniform(wave < 2 ? c_stage * 512 + wave * 256 : kStages * 512), (uint32_t)lane * 4);
-    if (++c_at == lo + per) c_at = lo, ++c_head;
+    sp += jump ? a.T - back : 64;
+    if (jump) c_at = lo;
+    --left;
     if (++c_stage == kStages) c_stage = 0;
   };
   copy();
@@ -433,10 +442,12 @@ __global__ __launch_bounds__(DP <= 128 ? 512 : 256, DP <= 128 ? 2 : 1) void ka_d
   for (int d = 0; d < ND; ++d) acc[d] = attn_zero();
   Reach<BF16, ND> reach;
 
-  // A step takes 32 rows of a tile. The second wavefront is a step behind the first, so that
-  // P is there when it asks for it and neither waits for the other: one barrier to a step, P
-  // in two buffers. Copies of a tile have two steps to arrive (three stages: a tile is left
-  // by the second wavefront a step after the first).
+  // A step takes 32 rows of a tile. The first wavefront forms S, P and its part of dV in a step,
+  // the second in the same one dS and its part of dK for the step before, from the P that the
+  // first left then, and afterwards do V^T for this one: each has its vector instructions where
+  // the other has matrix instructions. One barrier to a step, P in two buffers. Copies of a tile
+  // have two steps to arrive (three stages: the second wavefront leaves a tile a step after the
+  // first).
   AttnRead<DP> rd(smem);  // the first wavefront's products are q's rows and do's channels, the second's the others
   rd.next_rows(second ? Tile::kBytes : 0);
   rd.next_channels(second ? 0 : Tile::kBytes);
@@ -457,95 +468,134 @@ __global__ __launch_bounds__(DP <= 128 ? 512 : 256, DP <= 128 ? 2 : 1) void ka_d
   arrive(0);
   attn_barrier();
   if (kStages > 2) copy();
-  // A step's products: NQ of rows, NQ of channels. Operands are read kRing - 1 products ahead,
-  // beyond the step's end from the next step's rows.
+  // A step has NQ products of rows and NQ of channels, in this order or the other. Operands are
+  // read kRing - 1 products ahead, beyond the step's end from the next step's.
   static_assert(NQ == 2 * ND, "a step has as many products of rows as of channels");
   constexpr int kRing = NQ == 4 ? 4 : NQ == 6 ? 6 : 8;
   static_assert(2 * NQ % kRing == 0, "a product's place in the ring is the same in every step");
-  static_assert(kRing <= NQ + 1, "the next step's rows are read once the addresses have moved on");
+  static_assert(kRing <= NQ + 1, "the next step's operands are read once the addresses have moved on");
   uint4 ring[kRing];
-  auto fetch = [&](int n) {
-    if (n < NQ || (n >= 2 * NQ && kStages > 2)) ring[n % kRing] = rd.rows(0, 0, n % (2 * NQ));
-    else if (n < 2 * NQ) ring[n % kRing] = rd.channels(0, (n - NQ) % ND, (n - NQ) / ND);
+  constexpr int kCopyAt = 1;  // scalar instructions run beside matrix instructions
+  int at = lo, stage = 0;
+  // from a tile's step sb to the next one: how far the addresses move
+  auto advance = [&](int sb) {
+    if (sb == 0) return 2 * Tile::kSixteen;
+    const int was = stage;
+    if (++stage == kStages) stage = 0;
+    if (++at == lo + per) at = lo;
+    return (stage - was) * kStage - 2 * Tile::kSixteen;
   };
-  if (kStages > 2) {
+  auto stat = [&](v4f (&l)[4]) {
 #pragma unroll
-    for (int n = 0; n < kRing - 1; ++n) fetch(n);
-  }
-  int my = second ? -1 : 0, my_at = lo, my_stage = 0;
-  for (int k = 0; k <= 2 * tiles; ++k) {
-    if (k & 1) copy();
-    if (my >= 0 && my < 2 * tiles) {
-      const int sb = my & 1, base = (my_at << 6) + 32 * sb;
-      const bool masked = see.masked(my_at << 6);
-      v4f* p = p_mine + sb * kPairs * 256;
-      v4f l[4], w[4];
+    for (int e = 0; e < 4; ++e) l[e] = *reinterpret_cast<const v4f*>(st_mine + 64 * (e >> 1) + 16 * (e & 1));
+  };
+  auto mask = [&](v16f_t& s, int base) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) l[e] = *reinterpret_cast<const v4f*>(st_mine + 64 * (e >> 1) + 16 * (e & 1));
-      // P is read before the products or, where that leaves no registers, after them
-      constexpr bool kEarly = BF16 || DP < 128;
-      if (kEarly && second) {
+    for (int z = 0; z < 16; ++z)
+      if (!see(base + 16 * (z >> 3) + 8 * hf + (z & 7))) s[z] = 0.0f;
+  };
+  // the end of the first wavefront's step (i, sb)
+  auto turn = [&](int i, int sb) {
+    if (sb == (kStages == 2)) arrive(i + 1);
+    attn_barrier();
+  };
+  if (!second) {
+    auto fetch = [&](int n) {
+      if (n < NQ || (n >= 2 * NQ && kStages > 2)) ring[n % kRing] = rd.rows(0, 0, n % (2 * NQ));
+      else if (n < 2 * NQ) ring[n % kRing] = rd.channels(0, (n - NQ) % ND, (n - NQ) / ND);
+    };
+    if (kStages > 2) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = p[e * 64];
-      }
-      if (kStages == 2) {
+      for (int n = 0; n < kRing - 1; ++n) fetch(n);
+    }
+    for (int i = 0; i < tiles; ++i)
 #pragma unroll
-        for (int n = 0; n < kRing - 1; ++n) fetch(n);
-      }
-      v16f_t s;
+      for (int sb = 0; sb < 2; ++sb) {
+        v4f l[4];
+        stat(l);
+        if (kStages == 2) {
 #pragma unroll
-      for (int n = 0; n < NQ; ++n) {
-        fetch(n + kRing - 1);
-        s = Act16<BF16>::mma32(ring[n % kRing], kv[n], n == 0 ? attn_zero() : s);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      if (!second) {
+          for (int n = 0; n < kRing - 1; ++n) fetch(n);
+        }
+        v16f_t s;
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+          fetch(n + kRing - 1);
+          s = Act16<BF16>::mma32(ring[n % kRing], kv[n], n == 0 ? attn_zero() : s);
+          if (sb == 1 && n == kCopyAt) copy();
+          __builtin_amdgcn_sched_barrier(0);
+        }
 #pragma unroll
         for (int z = 0; z < 16; ++z) s[z] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[z], f, l[z >> 2][z & 3]));
-      } else {
-        if (!kEarly) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = p[e * 64];
-        }
-#pragma unroll
-        for (int z = 0; z < 16; ++z) s[z] = w[z >> 2][z & 3] * (s[z] - l[z >> 2][z & 3]);
-      }
-      if (masked) {
-#pragma unroll
-        for (int z = 0; z < 16; ++z) {
-          const int row = base + 16 * (z >> 3) + 8 * hf + (z & 7);
-          if (!see(row)) s[z] = 0.0f;
-        }
-      }
-      if (!second) {
+        if (see.masked(at << 6)) mask(s, (at << 6) + 32 * sb);
+        v4f* p = p_mine + sb * kPairs * 256;
 #pragma unroll
         for (int e = 0; e < 4; ++e) p[e * 64] = v4f{s[4 * e], s[4 * e + 1], s[4 * e + 2], s[4 * e + 3]};
-      } else if constexpr (!BF16) {
-        reach.fit(s, acc);
-        s *= reach.g;
+        const int was = stage, by = advance(sb);
+        rd.next_rows(by);
+        uint4 x;
+#pragma unroll
+        for (int n = NQ; n < 2 * NQ; ++n) {
+          fetch(n + kRing - 1);  // nobody's after the last step
+          if (n % ND == 0) x = attn_pack<BF16>(s, (n - NQ) / ND);
+          acc[n % ND] = Act16<BF16>::mma32(ring[n % kRing], x, acc[n % ND]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        rd.next_channels(by);
+        st_mine += (stage - was) * 512 + (sb ? -128 : 128);
+        turn(i, sb);
       }
-      int next_stage = my_stage;
-      if (sb == 1 && ++next_stage == kStages) next_stage = 0;
-      const int by = (next_stage - my_stage) * kStage + (sb == 0 ? 2 : -2) * Tile::kSixteen;
-      rd.next_rows(by);
-      uint4 x;
+    turn(tiles, 0);
+  } else {
+    auto fetch = [&](int n) {  // channels of the step before, rows, channels of this one
+      const int c = n % (2 * NQ);
+      if (n >= NQ && n < 2 * NQ) ring[n % kRing] = rd.rows(0, 0, n - NQ);
+      else ring[n % kRing] = rd.channels(0, c % ND, c / ND);
+    };
+    v16f_t t;
+    auto rows_product = [&]() {
 #pragma unroll
       for (int n = NQ; n < 2 * NQ; ++n) {
-        fetch(n + kRing - 1);  // nobody's after the last step
-        if (n % ND == 0) x = attn_pack<BF16>(s, (n - NQ) / ND);
-        acc[n % ND] = Act16<BF16>::mma32(ring[n % kRing], x, acc[n % ND]);
+        fetch(n + kRing - 1);
+        t = Act16<BF16>::mma32(ring[n % kRing], kv[n - NQ], n == NQ ? attn_zero() : t);
         __builtin_amdgcn_sched_barrier(0);
       }
-      rd.next_channels(by);
-      st_mine += (next_stage - my_stage) * 512 + (sb == 0 ? 128 : -128);
-      if (sb == 1) {
-        my_stage = next_stage;
-        if (++my_at == lo + per) my_at = lo;
+    };
+#pragma unroll
+    for (int n = NQ; n < NQ + kRing - 1; ++n) fetch(n);
+    rows_product();
+    turn(0, 0);
+    for (int i = 0; i < tiles; ++i)
+#pragma unroll
+      for (int sb = 0; sb < 2; ++sb) {  // sums of step (i, sb), do V^T of the next one
+        const v4f* p = p_mine + sb * kPairs * 256;
+        v4f l[4], w[4];
+        stat(l);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = p[e * 64];
+#pragma unroll
+        for (int z = 0; z < 16; ++z) t[z] = w[z >> 2][z & 3] * (t[z] - l[z >> 2][z & 3]);
+        if (see.masked(at << 6)) mask(t, (at << 6) + 32 * sb);
+        if constexpr (!BF16) {
+          reach.fit(t, acc);
+          t *= reach.g;
+        }
+        const int was = stage, by = advance(sb);
+        rd.next_rows(by);
+        uint4 x;
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+          fetch(n + kRing - 1);
+          if (n % ND == 0) x = attn_pack<BF16>(t, n / ND);
+          acc[n % ND] = Act16<BF16>::mma32(ring[n % kRing], x, acc[n % ND]);
+          if (sb == 0 && n == kCopyAt) copy();
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        rd.next_channels(by);
+        st_mine += (stage - was) * 512 + (sb ? -128 : 128);
+        rows_product();  // nobody's after the last step
+        turn(i + sb, sb ^ 1);
       }
-    }
-    ++my;
-    if ((k & 1) == (kStages == 2)) arrive((k >> 1) + 1);
-    attn_barrier();
   }
   attn_wait_copies();
   if (__builtin_expect(uniform(*flag), 0)) {

@@ -73,13 +73,11 @@ struct AttnCopy {
     step = (uint32_t)(kRows * W * (int)token * 2);
     to_mine = Tile::at(wave * kRows);
   }
-  // rows [first, first + 64) of the n at p into LDS at `to`; those from n on are zeros. The
-  // window's numbers are the same in all lanes and have to be in scalar registers: of vector
-  // ones the compiler makes a loop around each copy.
-  __device__ __forceinline__ void issue(const uint16_t* p, int64_t token, int first, int n, char* to) const {
-    const int left = min(n - first, 64);
-    const uint16_t* at = reinterpret_cast<const uint16_t*>(uniform((int64_t)(p + (int64_t)first * token)));
-    const __amdgpu_buffer_rsrc_t r = make_rsrc(at, (uint32_t)uniform(max(left, 0) * (int)token * 2));
+  // The tile at address `at` into LDS at `to`; what is `bytes` or more from its start on reads
+  // as zeros. The window's numbers are the same in all lanes and have to be in scalar
+  // registers: of vector ones the compiler makes a loop around each copy.
+  __device__ __forceinline__ void issue(int64_t at, int bytes, char* to) const {
+    const __amdgpu_buffer_rsrc_t r = make_rsrc(reinterpret_cast<const void*>(uniform(at)), (uint32_t)uniform(bytes));
 #pragma unroll
     for (int i = 0; i < kIssues; ++i) attn_copy16(r, to + (to_mine + Tile::at(i * W * kRows)), off + i * step);
   }
@@ -109,6 +107,25 @@ struct AttnCopy {
         *flag = 1;
       }
     }
+  }
+};
+
+// Tiles of a matrix one after the other, by address (a product of 64 bits for each would be a
+// dozen scalar instructions): `step` on from tile to tile, but `jump` where a caller says so.
+template <int DP, int W>
+struct AttnStream : AttnCopy<DP, W> {
+  int64_t at, step_by, jump_by;
+  int row;  // bytes of a token
+  // from row `first` on; a jump goes from one tile's begin to `jump` elements on
+  __device__ __forceinline__ AttnStream(const uint16_t* p, int64_t token, int dim, int64_t first, int64_t jump)
+      : AttnCopy<DP, W>(token, dim),
+        at(reinterpret_cast<int64_t>(p + first * token)),
+        step_by(128 * token),
+        jump_by(2 * jump),
+        row((int)(2 * token)) {}
+  __device__ __forceinline__ void next(int rows, char* to, bool jump) {
+    this->issue(at, rows * row, to);
+    at += jump ? jump_by : step_by;
   }
 };
 

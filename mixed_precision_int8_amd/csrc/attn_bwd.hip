@@ -471,7 +471,7 @@ __global__ __launch_bounds__(DP <= 128 ? 512 : 256, DP <= 128 ? 2 : 1) void ka_d
   // A step has NQ products of rows and NQ of channels, in this order or the other. Operands are
   // read kRing - 1 products ahead, beyond the step's end from the next step's.
   static_assert(NQ == 2 * ND, "a step has as many products of rows as of channels");
-  constexpr int kRing = NQ == 4 ? 4 : NQ == 6 ? 6 : 8;
+  constexpr int kRing = 8;
   static_assert(2 * NQ % kRing == 0, "a product's place in the ring is the same in every step");
   static_assert(kRing <= NQ + 1, "the next step's operands are read once the addresses have moved on");
   uint4 ring[kRing];
@@ -547,24 +547,36 @@ __global__ __launch_bounds__(DP <= 128 ? 512 : 256, DP <= 128 ? 2 : 1) void ka_d
       }
     turn(tiles, 0);
   } else {
-    auto fetch = [&](int n) {  // channels of the step before, rows, channels of this one
+    // products of a step: kBegin of this step's rows while P is on its way from LDS, channels of the
+    // step before, the other rows
+    constexpr int kBegin = kStages > 2 ? NQ / 2 : 0;
+    auto fetch = [&](int n) {
       const int c = n % (2 * NQ);
-      if (n >= NQ && n < 2 * NQ) ring[n % kRing] = rd.rows(0, 0, n - NQ);
-      else ring[n % kRing] = rd.channels(0, c % ND, c / ND);
+      if (c < kBegin) ring[n % kRing] = rd.rows(0, 0, c);
+      else if (c < kBegin + NQ) ring[n % kRing] = rd.channels(0, (c - kBegin) % ND, (c - kBegin) / ND);
+      else ring[n % kRing] = rd.rows(0, 0, c - NQ);
     };
-    v16f_t t;
-    auto rows_product = [&]() {
+    int rows_by = 0;  // to the rows of the step after
+    auto ahead = [&](int n) {
+      fetch(n + kRing - 1);
+      if (n + kRing == 2 * NQ) rd.next_rows(rows_by);
+    };
+    v16f_t t, u;
+    auto rows_products = [&](int from, int to, v16f_t& t) {
 #pragma unroll
-      for (int n = NQ; n < 2 * NQ; ++n) {
-        fetch(n + kRing - 1);
-        t = Act16<BF16>::mma32(ring[n % kRing], kv[n - NQ], n == NQ ? attn_zero() : t);
+      for (int r = from; r < to; ++r) {
+        const int n = r < kBegin ? r : r + NQ;
+        ahead(n);
+        t = Act16<BF16>::mma32(ring[n % kRing], kv[r], r == 0 ? attn_zero() : t);
         __builtin_amdgcn_sched_barrier(0);
       }
     };
 #pragma unroll
-    for (int n = NQ; n < NQ + kRing - 1; ++n) fetch(n);
-    rows_product();
+    for (int r = 0; r < NQ; ++r) t = Act16<BF16>::mma32(rd.rows(0, 0, r), kv[r], r == 0 ? attn_zero() : t);
     turn(0, 0);
+    rd.next_rows(2 * Tile::kSixteen);
+#pragma unroll
+    for (int n = 0; n < kRing - 1; ++n) fetch(n);
     for (int i = 0; i < tiles; ++i)
 #pragma unroll
       for (int sb = 0; sb < 2; ++sb) {  // sums of step (i, sb), do V^T of the next one
@@ -573,6 +585,8 @@ __global__ __launch_bounds__(DP <= 128 ? 512 : 256, DP <= 128 ? 2 : 1) void ka_d
         stat(l);
 #pragma unroll
         for (int e = 0; e < 4; ++e) w[e] = p[e * 64];
+        rows_by = sb ? 2 * Tile::kSixteen : ((stage + 1 == kStages ? 0 : stage + 1) - stage) * kStage - 2 * Tile::kSixteen;
+        rows_products(0, kBegin, u);
 #pragma unroll
         for (int z = 0; z < 16; ++z) t[z] = w[z >> 2][z & 3] * (t[z] - l[z >> 2][z & 3]);
         if (see.masked(at << 6)) mask(t, (at << 6) + 32 * sb);
@@ -581,19 +595,20 @@ __global__ __launch_bounds__(DP <= 128 ? 512 : 256, DP <= 128 ? 2 : 1) void ka_d
           t *= reach.g;
         }
         const int was = stage, by = advance(sb);
-        rd.next_rows(by);
         uint4 x;
 #pragma unroll
-        for (int n = 0; n < NQ; ++n) {
-          fetch(n + kRing - 1);
-          if (n % ND == 0) x = attn_pack<BF16>(t, n / ND);
-          acc[n % ND] = Act16<BF16>::mma32(ring[n % kRing], x, acc[n % ND]);
-          if (sb == 0 && n == kCopyAt) copy();
+        for (int c = 0; c < NQ; ++c) {
+          const int n = c + kBegin;
+          ahead(n);
+          if (c % ND == 0) x = attn_pack<BF16>(t, c / ND);
+          acc[c % ND] = Act16<BF16>::mma32(ring[n % kRing], x, acc[c % ND]);
+          if (sb == 0 && c == kCopyAt) copy();
           __builtin_amdgcn_sched_barrier(0);
         }
         rd.next_channels(by);
         st_mine += (stage - was) * 512 + (sb ? -128 : 128);
-        rows_product();  // nobody's after the last step
+        rows_products(kBegin, NQ, u);  // nobody's after the last step
+        t = u;
         turn(i + sb, sb ^ 1);
       }
   }

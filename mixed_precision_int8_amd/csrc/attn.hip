@@ -20,7 +20,7 @@
 namespace llmint8 {
 
 template <int DP, bool BF16>
-__global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_attention(AttnArgs a) {
+__global__ __launch_bounds__(256, DP <= 64 ? 4 : DP <= 128 ? 2 : 1) void ka_attention(AttnArgs a) {
   using Tile = AttnTile<DP>;
   constexpr int W = 4, kRows = 32 * W, NQ = Tile::NQ, ND = Tile::ND;
   constexpr int kStage = 2 * Tile::kBytes;  // k, v
@@ -34,9 +34,14 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_attention(AttnArgs 
   int run;
   if (!attn_place<true>(a, item, G, 7, &sq, &run)) return;
   const int64_t rows = (int64_t)sq.n * G, row0 = (int64_t)run * kRows;
-  const int r = (int)min(row0 + wave * 32 + nn, rows - 1);
-  const int pos = r / G, qh = h * G + (r - pos * G);
-  const int64_t qrow = (int64_t)sq.row0 + pos;
+  // the token and head of a lane's row
+  auto place = [&](int n, int* pos, int* qh) {
+    const int r = (int)min(row0 + wave * 32 + n, rows - 1);
+    *pos = r / G;
+    *qh = h * G + (r - *pos * G);
+  };
+  int pos, qh;
+  place(nn, &pos, &qh);
   auto span_of = [&](int64_t from, int64_t to) {  // of rows [from, to)
     return AttnSpan(a, (int)(min(from, rows) / G), (int)((min(to, rows) - 1) / G), sq.n);
   };
@@ -65,7 +70,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_attention(AttnArgs 
 
   uint4 q[NQ];
   {
-    const uint16_t* qp = a.q.p + qrow * a.q.token + (int64_t)qh * a.q.head;
+    const uint16_t* qp = a.q.p + (int64_t)(sq.row0 + pos) * a.q.token + (int64_t)qh * a.q.head;
     const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
 #pragma unroll
     for (int ks = 0; ks < NQ; ++ks) {
@@ -170,7 +175,11 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_attention(AttnArgs 
   }
 
   l_run = attn_pair_sum(l_run);
-  if (row0 + wave * 32 + nn >= rows) return;
+  int n = threadIdx.x & 31;
+  asm volatile("" : "+v"(n));  // computed again rather than kept in registers (64 channels have 128 of them)
+  if (row0 + wave * 32 + n >= rows) return;
+  place(n, &pos, &qh);
+  const int64_t qrow = (int64_t)sq.row0 + pos;
   const float inv = l_run == 0.0f ? 0.0f : 1.0f / l_run;
   uint16_t* op = a.o.p + qrow * a.o.token + (int64_t)qh * a.o.head;
 #pragma unroll

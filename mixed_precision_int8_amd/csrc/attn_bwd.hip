@@ -62,18 +62,19 @@ __device__ __forceinline__ void store_sums(const v16f_t (&acc)[DP / 32], float b
 }
 
 // What tokens j0 .. j_hi of k and v are seen by: rows [first, end) at most; token `col`, this
-// lane's, by rows [from, until).
+// lane's, by `count` rows from `from` on.
 struct AttnRowsOf {
-  int first, end, from, until, all_from, all_until;
+  int first, end, from, all_from, all_until;
+  uint32_t count;
   __device__ __forceinline__ AttnRowsOf(const AttnArgs& a, int n, int j0, int j_hi, int col) {
     first = a.causal ? j0 : 0;
     end = a.window > 0 && j0 >= a.sinks ? (int)min((int64_t)n, (int64_t)j_hi + a.window) : n;
     from = a.causal ? col : 0;
-    until = a.window > 0 && col >= a.sinks ? (int)min((int64_t)n, (int64_t)col + a.window) : n;
+    count = (uint32_t)max((a.window > 0 && col >= a.sinks ? (int)min((int64_t)n, (int64_t)col + a.window) : n) - from, 0);
     all_from = a.causal ? j_hi : 0;
     all_until = a.window > 0 && j_hi >= a.sinks ? max(j0, (int)min((int64_t)a.sinks, (int64_t)j_hi)) + a.window : INT32_MAX;
   }
-  __device__ __forceinline__ bool operator()(int row) const { return (row >= from) & (row < until); }
+  __device__ __forceinline__ bool operator()(int row) const { return (uint32_t)(row - from) < count; }
   // a tile that some of the tokens do not see whole
   __device__ __forceinline__ bool masked(int base) const { return (base < all_from) | (base + 64 > all_until); }
 };
@@ -97,7 +98,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_dq(AttnArgs a) {
   const int64_t rows = (int64_t)sq.n * G, row0 = (int64_t)run * kRows;
   const int r = (int)min(row0 + wave * 32 + nn, rows - 1);
   const int pos = r / G, qh = h * G + (r - pos * G);
-  const int64_t qrow = (int64_t)sq.row0 + pos;
+  const int qrow = sq.row0 + pos;
   auto span_of = [&](int64_t from, int64_t to) {  // of rows [from, to)
     return AttnSpan(a, (int)(min(from, rows) / G), (int)((min(to, rows) - 1) / G), sq.n);
   };
@@ -127,9 +128,9 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_dq(AttnArgs a) {
   uint4 q[NQ], g[NQ];
   float delta = 0.0f;
   {
-    const uint16_t* qp = a.q.p + qrow * a.q.token + (int64_t)qh * a.q.head;
-    const uint16_t* gp = a.d_o.p + qrow * a.d_o.token + (int64_t)qh * a.d_o.head;
-    const uint16_t* op = a.o.p + qrow * a.o.token + (int64_t)qh * a.o.head;
+    const uint16_t* qp = a.q.p + (int64_t)qrow * a.q.token + (int64_t)qh * a.q.head;
+    const uint16_t* gp = a.d_o.p + (int64_t)qrow * a.d_o.token + (int64_t)qh * a.d_o.head;
+    const uint16_t* op = a.o.p + (int64_t)qrow * a.o.token + (int64_t)qh * a.o.head;
     const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
 #pragma unroll
     for (int ks = 0; ks < NQ; ++ks) {
@@ -151,7 +152,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_dq(AttnArgs a) {
     delta = attn_pair_sum(delta);
   }
   const float f = fabsf(a.scale) * 1.44269504088896341f;
-  const float lse2 = a.lse[qrow * a.q_heads + qh] * 1.44269504088896341f;
+  const float lse2 = a.lse[(int64_t)qrow * a.q_heads + qh] * 1.44269504088896341f;
   const bool mine = row0 + wave * 32 + nn < rows;
   if (mine && hf == 0) {
     float* st = a.stat + (int64_t)qh * a.T + qrow;

@@ -198,7 +198,7 @@ __device__ __forceinline__ bool attn_place(const AttnArgs& a, int item, int per,
     const int tiles = lane < a.B ? (int)(((int64_t)q.n * per + (1 << shift) - 1) >> shift) : 0;
     auto at_least = [&](int l) { return __builtin_amdgcn_readlane(wave_incl_sum(max(tiles - l, 0)), 63); };
     if (item >= at_least(0)) return false;
-    int lo = 0, hi = __builtin_amdgcn_readfirstlane(wave_max_i(tiles)), above = 0;  // F(lo) > item >= F(hi)
+    int lo = 0, hi = (int)(((int64_t)a.T * per >> shift) + 1), above = 0;  // F(lo) > item >= F(hi)
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1, f = at_least(mid);
       if (f > item) lo = mid;

@@ -15,11 +15,12 @@ namespace llmint8 {
 namespace {
 
 // This workgroup's tensor and values [lo, hi) of it.
-__device__ __forceinline__ const GradItem& grad_place(const GradBatch& g, int64_t* lo, int64_t* hi) {
+template <int N>
+__device__ __forceinline__ const GradItem& grad_place(const GradBatch<N>& g, int64_t* lo, int64_t* hi) {
   const int b = blockIdx.x;
   int t = 0;
 #pragma unroll
-  for (int step = 64; step > 0; step >>= 1)
+  for (int step = N > 256 ? 256 : 64; step > 0; step >>= 1)
     if (t + step < g.count && g.item[t + step].start <= b) t += step;
   const GradItem& i = g.item[t];
   *lo = (int64_t)(b - i.start) * g.chunk;
@@ -73,7 +74,8 @@ __device__ __forceinline__ void scale_to(const void* p, void* out, int64_t lo, i
 
 }  // namespace
 
-__global__ __launch_bounds__(256) void kg_squares(GradBatch g, double* parts) {
+template <int N>
+__global__ __launch_bounds__(256) void kg_squares(GradBatch<N> g, double* parts) {
   __shared__ double sh[4];
   int64_t lo, hi;
   const GradItem& i = grad_place(g, &lo, &hi);
@@ -94,7 +96,8 @@ __global__ __launch_bounds__(256) void kg_norm(const double* parts, int64_t n, d
   if (threadIdx.x == 0) *norm = (float)(sqrt(s) * scale);
 }
 
-__global__ __launch_bounds__(256) void kg_scale(GradBatch g, const float* norm, double max_norm, double scale) {
+template <int N>
+__global__ __launch_bounds__(256) void kg_scale(GradBatch<N> g, const float* norm, double max_norm, double scale) {
   int64_t lo, hi;
   const GradItem& i = grad_place(g, &lo, &hi);
   const double by = max_norm == __builtin_inf() ? 1.0 : max_norm / ((double)*norm + 1e-6);
@@ -107,8 +110,9 @@ __global__ __launch_bounds__(256) void kg_scale(GradBatch g, const float* norm, 
   else scale_to<kF16, kF16>(i.p, i.out, lo, hi, f);
 }
 
-hipError_t launch_grad_squares(const GradBatch& g, double* parts, hipStream_t stream) {
-  hipLaunchKernelGGL(kg_squares, dim3((unsigned)g.blocks), dim3(256), 0, stream, g, parts);
+template <int N>
+hipError_t launch_grad_squares(const GradBatch<N>& g, double* parts, hipStream_t stream) {
+  hipLaunchKernelGGL(kg_squares<N>, dim3((unsigned)g.blocks), dim3(256), 0, stream, g, parts);
   return hipGetLastError();
 }
 
@@ -117,9 +121,15 @@ hipError_t launch_grad_norm(const double* parts, int64_t n, double scale, float*
   return hipGetLastError();
 }
 
-hipError_t launch_grad_scale(const GradBatch& g, const float* norm, double max_norm, double scale, hipStream_t stream) {
-  hipLaunchKernelGGL(kg_scale, dim3((unsigned)g.blocks), dim3(256), 0, stream, g, norm, max_norm, scale);
+template <int N>
+hipError_t launch_grad_scale(const GradBatch<N>& g, const float* norm, double max_norm, double scale, hipStream_t stream) {
+  hipLaunchKernelGGL(kg_scale<N>, dim3((unsigned)g.blocks), dim3(256), 0, stream, g, norm, max_norm, scale);
   return hipGetLastError();
 }
+
+template hipError_t launch_grad_squares(const GradBatch<kGradFew>&, double*, hipStream_t);
+template hipError_t launch_grad_squares(const GradBatch<kGradMany>&, double*, hipStream_t);
+template hipError_t launch_grad_scale(const GradBatch<kGradFew>&, const float*, double, double, hipStream_t);
+template hipError_t launch_grad_scale(const GradBatch<kGradMany>&, const float*, double, double, hipStream_t);
 
 }  // namespace llmint8

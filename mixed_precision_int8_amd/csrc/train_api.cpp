@@ -274,9 +274,9 @@ size_t llmint8_grad_norm_workspace_bytes(const llmint8_grad* grads, int64_t coun
 }  // extern "C"
 
 // `launch` for batches of the tensors that hold anything.
-template <class Launch>
-static hipError_t grad_batches(const llmint8_grad* grads, int64_t count, Launch&& launch) {
-  GradBatch b;
+template <int N, class Launch>
+static hipError_t grad_batches_of(const llmint8_grad* grads, int64_t count, Launch&& launch) {
+  GradBatch<N> b;
   b.chunk = (int)grad_chunk(grads, count);
   b.count = b.blocks = 0;
   for (int64_t i = 0; i < count; ++i) {
@@ -284,13 +284,19 @@ static hipError_t grad_batches(const llmint8_grad* grads, int64_t count, Launch&
       b.item[b.count++] = {grads[i].data, grads[i].out, grads[i].n, b.blocks, grads[i].dtype | grads[i].out_dtype << 8};
       b.blocks += (int)ceil_div(grads[i].n, b.chunk);
     }
-    if (b.count == kGradBatch || (i + 1 == count && b.count > 0)) {
+    if (b.count == N || (i + 1 == count && b.count > 0)) {
       const hipError_t e = launch(b);
       if (e != hipSuccess) return e;
       b.count = b.blocks = 0;
     }
   }
   return hipSuccess;
+}
+// Many tensors in few launches, 16 KB of arguments each; a few are not made to carry those.
+template <class Launch>
+static hipError_t grad_batches(const llmint8_grad* grads, int64_t count, Launch&& launch) {
+  return count > kGradFew ? grad_batches_of<kGradMany>(grads, count, launch)
+                          : grad_batches_of<kGradFew>(grads, count, launch);
 }
 
 extern "C" {
@@ -305,7 +311,7 @@ llmint8_status llmint8_grad_norm(const llmint8_grad* grads, int64_t count, doubl
   const hipStream_t s = static_cast<hipStream_t>(stream);
   double* parts = static_cast<double*>(workspace);
   int64_t blocks = 0;
-  const hipError_t e = grad_batches(grads, count, [&](const GradBatch& b) {
+  const hipError_t e = grad_batches(grads, count, [&](const auto& b) {
     const hipError_t err = launch_grad_squares(b, parts + blocks, s);
     blocks += b.blocks;
     return err;
@@ -320,7 +326,7 @@ llmint8_status llmint8_grad_clip(const llmint8_grad* grads, int64_t count, const
   if (st != LLMINT8_OK) return st;
   if (!(scale > 0.0) || !std::isfinite(scale) || !(max_norm > 0.0) || !norm || !aligned(norm, 4))
     return LLMINT8_ERR_INVALID_ARG;
-  return abi_hip_status(grad_batches(grads, count, [&](const GradBatch& b) {
+  return abi_hip_status(grad_batches(grads, count, [&](const auto& b) {
     return launch_grad_scale(b, norm, max_norm, scale, static_cast<hipStream_t>(stream));
   }));
 }

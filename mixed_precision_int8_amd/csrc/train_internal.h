@@ -46,12 +46,12 @@ struct RopeArgs {
 };
 hipError_t launch_rope(const RopeArgs& a, bool bf16, int num_cus, hipStream_t stream);
 
-// Gradients: `kGradBatch` tensors to a launch, as its arguments. A workgroup takes
+// Gradients: up to N tensors to a launch, as its arguments (N one of the two). A workgroup takes
 // `chunk` values of one; tensor t's workgroups begin at `start`. One entry is 32 bytes
 // for all that is read of a tensor: beside an array of bytes indexed by the tensor the
 // compiler has split 8 t into t and 7 t for a scalar load of an address, and scalar
 // loads drop the lowest two bits of each.
-constexpr int kGradBatch = 120;
+constexpr int kGradFew = 120, kGradMany = 480;
 struct GradItem {
   const void* p;
   void* out;
@@ -59,14 +59,17 @@ struct GradItem {
   int start;
   int types;  // type | out_type << 8
 };
+template <int N>
 struct GradBatch {
-  GradItem item[kGradBatch];
+  GradItem item[N];
   int count, chunk;
   int blocks;  // of all the items
 };
-static_assert(sizeof(GradItem) == 32 && sizeof(GradBatch) + 32 <= 4096, "a launch's arguments");
-hipError_t launch_grad_squares(const GradBatch& g, double* parts, hipStream_t stream);
+static_assert(sizeof(GradItem) == 32 && sizeof(GradBatch<kGradFew>) + 32 <= 4096, "the arguments of a launch of few");
+template <int N>
+hipError_t launch_grad_squares(const GradBatch<N>& g, double* parts, hipStream_t stream);
 hipError_t launch_grad_norm(const double* parts, int64_t n, double scale, float* norm, hipStream_t stream);
-hipError_t launch_grad_scale(const GradBatch& g, const float* norm, double max_norm, double scale, hipStream_t stream);
+template <int N>
+hipError_t launch_grad_scale(const GradBatch<N>& g, const float* norm, double max_norm, double scale, hipStream_t stream);
 
 }  // namespace llmint8

@@ -256,3 +256,30 @@ def test_everything_in_a_captured_step():
         torch.cuda.synchronize()
         for a, b in zip((*held, *gs), want):
             assert torch.equal(a, b), i
+
+
+@pytest.mark.parametrize("count", [1, 119, 120, 121, 480, 481, 1000])
+def test_batches_of_gradients(count):
+    """Tensors go to a launch in batches; each is counted and scaled once, eagerly and in a replayed graph."""
+    print(f"[case] {count} gradients", flush=True)
+    grads = [randn(i, 1 + i * 37 % 300) if i % 5 else torch.zeros(0, dtype=torch.float16, device="cuda") for i in range(1, count + 1)]
+    wide = [torch.zeros_like(g, dtype=torch.float32) for g in grads]
+    gset = m8.GradientSet(grads, out=wide)
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        m8.llmint8_grad_clip(gset, m8.llmint8_grad_norm(gset), 0.5)
+        stream.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            norm = m8.llmint8_grad_norm(gset)
+            m8.llmint8_grad_clip(gset, norm, 0.5)
+    for k in range(3):
+        for g in grads:
+            g.mul_(0.5)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        want = ref.grad_norm([g.cpu().numpy() for g in grads])
+        assert abs(float(norm) - want) <= 2.0 ** -23 * want, k
+        f = np.float32(ref.grad_factor(norm.item(), 0.5))
+        assert np.array_equal(torch.cat(wide).cpu().numpy(), torch.cat(grads).cpu().numpy().astype(np.float32) * f), k

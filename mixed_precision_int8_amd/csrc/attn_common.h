@@ -15,7 +15,8 @@
 // An instruction of either kind takes LDS four cycles where no bank is asked twice: 16
 // rows of one chunk of 16 bytes, or four rows of four chunks. Chunks are stored at
 // chunk ^ 4 (row % 4), and every four rows begin 16 bytes later (rows of 128 bytes: at
-// chunk ^ 4 (row / 2 % 2) ^ (row / 4 % 2), 32 bytes later every eight rows). The exclusive
+// chunk ^ 4 (row / 2 % 2) ^ (row / 4 % 2), 32 bytes later every eight rows; rows of 192 bytes begin
+// at four different places of 256 as they are: at chunk ^ (row / 4 % 4)). The exclusive
 // or touches few bits of a chunk's number, so that four addresses to a lane serve all
 // "rows" operands and four all "channels" operands: the rest of an address is a constant of
 // the instruction. (With one over all bits each step had an address of its own; the
@@ -61,17 +62,20 @@ __device__ __forceinline__ v4s attn_read_tr(const char* __restrict p) {
 template <int DP, int W>
 struct AttnCopy {
   using Tile = AttnTile<DP>;
-  static constexpr int kIssues = 64 * Tile::kPitch / 1024 / W;  // of 1 KB to a wavefront and tile
-  static constexpr int kRows = 1024 / Tile::kPitch;             // of an issue
-  static_assert(kRows * W % 8 == 0, "the rows of a thread's issues have one swizzle and at() adds up");
-  uint32_t off, step;
+  static constexpr int kIssues = 64 * Tile::kPitch / 1024 / W;  // of 64 chunks to a wavefront and tile
+  static constexpr int kRows = 1024 / Tile::kPitch;             // of an issue, where they are whole
+  static_assert(Tile::kMiddle || kRows * W % 8 == 0, "the rows of a thread's issues have one swizzle and copy_at adds up");
+  uint32_t off[Tile::kMiddle ? kIssues : 1], step;
   int to_mine;  // of this wavefront's first issue in a tile
   __device__ __forceinline__ AttnCopy(int64_t token, int dim) {
     const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
-    const int row = wave * kRows + lane / Tile::kChunks, chunk = lane % Tile::kChunks ^ Tile::swizzle(row);
-    off = chunk * 8 < dim ? (uint32_t)(row * (int)token * 2 + chunk * 16) : kOobOffset;
+#pragma unroll
+    for (int i = 0; i < (Tile::kMiddle ? kIssues : 1); ++i) {
+      const int n = (i * W + wave) * 64 + lane, row = n / Tile::kChunks, chunk = n % Tile::kChunks ^ Tile::swizzle(row);
+      off[i] = chunk * 8 < dim ? (uint32_t)(row * (int)token * 2 + chunk * 16) : kOobOffset;
+    }
     step = (uint32_t)(kRows * W * (int)token * 2);
-    to_mine = Tile::at(wave * kRows);
+    to_mine = Tile::copy_at(wave);
   }
   // The tile at address `at` into LDS at `to`; what is `bytes` or more from its start on reads
   // as zeros. The window's numbers are the same in all lanes and have to be in scalar
@@ -79,7 +83,8 @@ struct AttnCopy {
   __device__ __forceinline__ void issue(int64_t at, int bytes, char* to) const {
     const __amdgpu_buffer_rsrc_t r = make_rsrc(reinterpret_cast<const void*>(uniform(at)), (uint32_t)uniform(bytes));
 #pragma unroll
-    for (int i = 0; i < kIssues; ++i) attn_copy16(r, to + (to_mine + Tile::at(i * W * kRows)), off + i * step);
+    for (int i = 0; i < kIssues; ++i)
+      attn_copy16(r, to + (to_mine + Tile::copy_at(i * W)), Tile::kMiddle ? off[i] : off[0] + i * step);
   }
   // A product whose weights are exactly zero where a column does not see a row must not take
   // that row's values that are not finite (0 times them is NaN). Where a tile has masked rows
@@ -92,7 +97,7 @@ struct AttnCopy {
     v4i x[kIssues];
     char* const at = to + to_mine + (threadIdx.x & 63) * 16;
 #pragma unroll
-    for (int i = 0; i < kIssues; ++i) x[i] = *reinterpret_cast<const v4i*>(at + Tile::at(i * W * kRows));
+    for (int i = 0; i < kIssues; ++i) x[i] = *reinterpret_cast<const v4i*>(at + Tile::copy_at(i * W));
 #pragma unroll
     for (int i = 0; i < kIssues; ++i) {
       uint32_t odd = 0;
@@ -103,7 +108,7 @@ struct AttnCopy {
         x[i][j] = (int)(v & ~((bad >> 15) * 0xffffu));
       }
       if (__builtin_expect(odd != 0, 0)) {
-        *reinterpret_cast<v4i*>(at + Tile::at(i * W * kRows)) = x[i];
+        *reinterpret_cast<v4i*>(at + Tile::copy_at(i * W)) = x[i];
         *flag = 1;
       }
     }
@@ -134,19 +139,22 @@ struct AttnStream : AttnCopy<DP, W> {
 template <int DP>
 struct AttnRead {
   using Tile = AttnTile<DP>;
-  static constexpr int kRowAt = Tile::kNarrow ? 2 : 4;  // addresses that differ by the exclusive or
+  // addresses that differ by the exclusive or
+  static constexpr int kRowAt = Tile::kNarrow || Tile::kMiddle ? 2 : 4, kTrAt = Tile::kMiddle ? 2 : 4;
   const char* row[kRowAt];
-  const char* tr[4];
+  const char* tr[kTrAt];
   __device__ __forceinline__ explicit AttnRead(const char* smem) {
     const int lane = threadIdx.x & 63, hf = lane >> 5, nn = lane & 31;
     const int r = (nn & 0x13) | (nn & 4) << 1 | (nn & 8) >> 1;
 #pragma unroll
-    for (int i = 0; i < kRowAt; ++i) row[i] = smem + Tile::at(r) + ((4 * i + hf) ^ Tile::swizzle(r)) * 16;
+    for (int i = 0; i < kRowAt; ++i)
+      row[i] = smem + Tile::at(r) + (((Tile::kMiddle ? 2 : 4) * i + hf) ^ Tile::swizzle(r)) * 16;
     const int i = lane & 15, t = 8 * hf + (i >> 2), c = 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);
 #pragma unroll
-    for (int d = 0; d < 4; ++d) {
-      // narrow: 32-channel block d / 2, and four rows on where d is odd
-      const int u = Tile::kNarrow ? t + 4 * (d & 1) : t, block = Tile::kNarrow ? d >> 1 : d;
+    for (int d = 0; d < kTrAt; ++d) {
+      // narrow: 32-channel block d / 2, and four rows on where d is odd; middle: four rows on
+      const int u = Tile::kNarrow || Tile::kMiddle ? t + 4 * (d & 1) : t;
+      const int block = Tile::kNarrow ? d >> 1 : Tile::kMiddle ? 0 : d;
       tr[d] = smem + Tile::at(u) + ((4 * block + c) ^ Tile::swizzle(u)) * 16 + 8 * (i & 1);
     }
   }
@@ -156,7 +164,7 @@ struct AttnRead {
   }
   __device__ __forceinline__ void next_channels(int by) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) tr[i] += by;
+    for (int i = 0; i < kTrAt; ++i) tr[i] += by;
   }
   __device__ __forceinline__ void next(int by) {
     next_rows(by);
@@ -164,15 +172,19 @@ struct AttnRead {
   }
   // rows [32 block, +32) x channels [16 step, +16)
   __device__ __forceinline__ uint4 rows(int tile, int block, int step) const {
-    const v4i x = *reinterpret_cast<const v4i*>(
-        row[(step >> 1) % kRowAt] + (tile * Tile::kBytes + (step & 1) * 32 + (step >> 3) * 256 + block * 2 * Tile::kSixteen));
+    const int at = tile * Tile::kBytes + block * 2 * Tile::kSixteen +
+                   (Tile::kMiddle ? (step >> 1) * 64 : (step & 1) * 32 + (step >> 3) * 256);
+    const v4i x = *reinterpret_cast<const v4i*>(row[Tile::kMiddle ? step & 1 : (step >> 1) % kRowAt] + at);
     return __builtin_bit_cast(uint4, x);
   }
   // channels [32 block, +32) x rows [16 step, +16)
   __device__ __forceinline__ uint4 channels(int tile, int block, int step) const {
-    const int at = tile * Tile::kBytes + (Tile::kNarrow ? 0 : (block >> 2) * 256) + step * Tile::kSixteen;
-    const char* first = tr[Tile::kNarrow ? 2 * block : block & 3] + at;
-    const char* second = Tile::kNarrow ? tr[(2 * block + 1) & 3] + at : first + Tile::at(4);
+    const int at = tile * Tile::kBytes + step * Tile::kSixteen +
+                   (Tile::kNarrow ? 0 : Tile::kMiddle ? block * 64 : (block >> 2) * 256);
+    const char* first = tr[Tile::kNarrow ? 2 * block : Tile::kMiddle ? 0 : block & 3] + at;
+    const char* second = Tile::kNarrow   ? tr[(2 * block + 1) % kTrAt] + at
+                         : Tile::kMiddle ? tr[1] + at
+                                         : first + Tile::at(4);
     const v4s lo = attn_read_tr(first);
     const v4s hi = attn_read_tr(second);
     const uint2 a = __builtin_bit_cast(uint2, lo), b = __builtin_bit_cast(uint2, hi);
@@ -259,13 +271,18 @@ __device__ __forceinline__ v16f_t attn_zero() {
   return z;
 }
 
-// What a row sees of its sequence: tokens up to `last` that are past `from` or
-// below `sinks` (from = -1: all of them).
+// What a row sees of its sequence: `count` tokens from `first` on (of a window; else from 0), and
+// those below `sinks`.
 struct AttnSees {
-  int last, from, sinks;
-  __device__ __forceinline__ AttnSees(const AttnArgs& a, int pos, int n)
-      : last(a.causal ? min(pos, n - 1) : n - 1), from(a.window > 0 ? pos - a.window : -1), sinks(a.sinks) {}
-  __device__ __forceinline__ bool operator()(int j) const { return (j <= last) & ((j > from) | (j < sinks)); }
+  int first, sinks;
+  uint32_t count;
+  __device__ __forceinline__ AttnSees(const AttnArgs& a, int pos, int n) {
+    const int end = a.causal ? min(pos + 1, n) : n;
+    first = a.window > 0 ? pos - a.window + 1 : 0;
+    count = (uint32_t)(end - first);
+    sinks = min(a.sinks, end);
+  }
+  __device__ __forceinline__ bool operator()(int j) const { return ((uint32_t)j - (uint32_t)first < count) | (j < sinks); }
 };
 
 // What rows at tokens lo .. hi of a sequence of n see: `last` and `begin` bound what any of them

@@ -47,18 +47,24 @@ __host__ __device__ inline AttnSeq attn_seq_of(int cu0, int cu1, int T) {
 // 16 bytes of its row a chunk is kept.
 template <int DP>
 struct AttnTile {
-  static constexpr int kPitch = DP <= 64 ? 128 : DP <= 128 ? 256 : 512;  // bytes of a row
+  static constexpr int kPitch = DP <= 64 ? 128 : DP <= 96 ? 192 : DP <= 128 ? 256 : 512;  // bytes of a row
   static constexpr int kChunks = kPitch / 16;
-  static constexpr bool kNarrow = kPitch == 128;
-  static constexpr int kSixteen = 16 * kPitch + 64;  // bytes of 16 rows
+  static constexpr bool kNarrow = kPitch == 128, kMiddle = kPitch == 192;
+  static constexpr int kSixteen = 16 * kPitch + (kMiddle ? 0 : 64);  // bytes of 16 rows
   static constexpr int kBytes = 4 * kSixteen;
   static constexpr int NQ = DP / 16;  // 16-channel steps
   static constexpr int ND = DP / 32;  // 32-channel blocks
   static __host__ __device__ constexpr int swizzle(int row) {
-    return kNarrow ? (row >> 1 & 1) << 2 | (row >> 2 & 1) : (row & 3) << 2;
+    return kNarrow ? (row >> 1 & 1) << 2 | (row >> 2 & 1) : kMiddle ? row >> 2 & 3 : (row & 3) << 2;
   }
   static __host__ __device__ constexpr int at(int row) {
-    return (row >> 4) * kSixteen + (row & 15) * kPitch + (kNarrow ? (row >> 3 & 1) * 32 : (row >> 2 & 3) * 16);
+    return (row >> 4) * kSixteen + (row & 15) * kPitch +
+           (kNarrow ? (row >> 3 & 1) * 32 : kMiddle ? 0 : (row >> 2 & 3) * 16);
+  }
+  // where the 64 chunks of a wavefront's copy go: copy number `copy` of a tile, the copies of W
+  // wavefronts one after the other
+  static __host__ __device__ constexpr int copy_at(int copy) {
+    return kMiddle ? copy * 1024 : at(copy * (1024 / kPitch));
   }
 };
 

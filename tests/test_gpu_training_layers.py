@@ -283,3 +283,19 @@ def test_batches_of_gradients(count):
         assert abs(float(norm) - want) <= 2.0 ** -23 * want, k
         f = np.float32(ref.grad_factor(norm.item(), 0.5))
         assert np.array_equal(torch.cat(wide).cpu().numpy(), torch.cat(grads).cpu().numpy().astype(np.float32) * f), k
+
+
+def test_the_example_runs_and_every_parameter_has_a_gradient():
+    print("[case] example", flush=True)
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "adapter_training.py")
+    spec = importlib.util.spec_from_file_location("adapter_training", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    blocks, losses, norms = example.main(["--layers", "2", "--steps", "3", "--tokens", "300"])
+    assert all(torch.isfinite(x).all() for x in (*losses, *norms)) and all(float(x) > 0 for x in norms)
+    for name, p in blocks.named_parameters():  # B of an adapter was zero in the first step, so A's is of later ones
+        assert p.grad is not None and torch.isfinite(p.grad).all() and float(p.grad.abs().max()) > 0, name
+    total = ref.grad_norm([p.grad.cpu().numpy() for p in blocks.parameters()])
+    assert total <= 0.1 * (1 + 2.0 ** -20)  # clipped

@@ -86,6 +86,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_dq(AttnArgs a) {
   using Tile = AttnTile<DP>;
   constexpr int W = 4, kRows = 32 * W, NQ = Tile::NQ, ND = Tile::ND;
   constexpr int kStage = 2 * Tile::kBytes;  // k, v
+  constexpr int kFew = 4;                   // tiles
   __shared__ __attribute__((aligned(1024))) char smem[2 * kStage + 16];
   int* const flag = reinterpret_cast<int*>(smem + 2 * kStage);
   const int D = a.dim, H = a.heads, G = a.q_heads / H;
@@ -153,6 +154,40 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_dq(AttnArgs a) {
   }
   const float f = fabsf(a.scale) * 1.44269504088896341f;
   const float lse2 = a.lse[(int64_t)qrow * a.q_heads + qh] * 1.44269504088896341f;
+  AttnRead<DP> rd(smem);
+  const AttnSees sees(a, pos, sq.n);
+
+  // o has been rounded, and so is delta off by 2^-12 (2^-9) of do o: little beside the spread of
+  // do V^T where many tokens share a row's weight, as much as all other roundings where few do.
+  // There delta is summed from its definition, sum_j P_ij (do V^T)_ij: two products more.
+  if (tiles <= kFew) {
+    delta = 0.0f;
+#pragma unroll 1
+    for (int i = 0; i < tiles; ++i) {
+      const int stage = i & 1, base = base_of(i);
+      attn_wait_copies();
+      attn_barrier();
+      copy(i + 1, stage ^ 1);
+#pragma unroll
+      for (int sb = 0; sb < 2; ++sb) {
+        if (idle | own.none(base + 32 * sb, 32)) continue;
+        const v16f_t s = attn_rows_product<DP, BF16>(rd, 0, sb, q);
+        const v16f_t t = attn_rows_product<DP, BF16>(rd, 1, sb, g);
+#pragma unroll
+        for (int x = 0; x < 16; ++x)
+          if (sees(base + 32 * sb + 16 * (x >> 3) + 8 * hf + (x & 7)))
+            delta = __builtin_fmaf(__builtin_amdgcn_exp2f(__builtin_fmaf(s[x], f, -lse2)), t[x], delta);
+      }
+      rd.next(stage ? -kStage : kStage);
+    }
+    delta = attn_pair_sum(delta);
+    if (tiles & 1) rd.next(-kStage);
+    attn_wait_copies();
+    attn_barrier();
+    ck.rewind(kp, a.k.token, start);
+    cv.rewind(vp, a.v.token, start);
+    copy(0, 0);
+  }
   const bool mine = row0 + wave * 32 + nn < rows;
   if (mine && hf == 0) {
     float* st = a.stat + (int64_t)qh * a.T + qrow;
@@ -164,8 +199,6 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_dq(AttnArgs a) {
 #pragma unroll
   for (int d = 0; d < ND; ++d) acc[d] = attn_zero();
   Reach<BF16, ND> reach;
-  AttnRead<DP> rd(smem);
-  const AttnSees sees(a, pos, sq.n);
 
   for (int i = 0; i < tiles; ++i) {
     const int stage = i & 1, base = base_of(i);

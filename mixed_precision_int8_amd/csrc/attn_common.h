@@ -128,6 +128,9 @@ struct AttnStream : AttnCopy<DP, W> {
         step_by(128 * token),
         jump_by(2 * jump),
         row((int)(2 * token)) {}
+  __device__ __forceinline__ void rewind(const uint16_t* p, int64_t token, int64_t first) {
+    at = reinterpret_cast<int64_t>(p + first * token);
+  }
   __device__ __forceinline__ void next(int rows, char* to, bool jump) {
     this->issue(at, rows * row, to);
     at += jump ? jump_by : step_by;

@@ -16,11 +16,11 @@ def visible(n, causal, window=0, sinks=0):
     return see
 
 
-def attention(lens, q, k, v, scale, causal=True, window=0, sinks=0, dout=None, unit=None, floor=False):
+def attention(lens, q, k, v, scale, causal=True, window=0, sinks=0, dout=None, unit=None, floor=False, few=False):
     """Packed sequences of ``lens`` tokens; q [T, hq, D], k and v [T, hk, D]. A dict of out, lse and, with ``dout``,
     dq, dk, dv; with ``unit`` (half a step of the 16-bit type) also of ``e_out`` and so on: how far a result may be
     off whose products take P and dS rounded to the type, with fp32 logits and sums (``floor``: the type is fp16,
-    which holds them to a floor as well)."""
+    which holds them to a floor as well; ``few``: delta is summed from P and dP, not from the rounded o)."""
     T, hq, D = q.shape
     hk, G = k.shape[1], hq // k.shape[1]
     q, k, v = (x.astype(np.float64) for x in (q, k, v))
@@ -74,6 +74,8 @@ def attention(lens, q, k, v, scale, causal=True, window=0, sinks=0, dout=None, u
             e_delta = (np.abs(do) * (e_o + D * f32 * np.abs(o))).sum(1, keepdims=True)
             e_dp = (D + 2) * f32 * (np.abs(do) @ np.abs(vi.T))
             e_w = d + d_row + sums + 8 * np.abs(r["lse"][rows, h])[:, None] * f32  # of a weight before it is rounded
+            if few:
+                e_delta = (p * (np.abs(dp) * (e_w + (n + 2) * f32) + e_dp)).sum(1, keepdims=True)
             e_ds = np.abs(ds) * (unit + e_w) + p * (1 + e_w) * (e_dp + e_delta)
             e_q = e_k = e_ds
             if floor:

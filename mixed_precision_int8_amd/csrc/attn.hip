@@ -13,6 +13,13 @@
 // exceeds it by 2^7: w = exp2(u - m + 8) is at most 2^15, so that in fp16 weights
 // down to 2^-32 of the largest count. Statistics and sums are fp32, a weight is
 // rounded to the inputs' type (2^-11 or 2^-8 of itself at most) for the product.
+//
+// Bound by the SIMDs' issue: matrix instructions and the softmax's vector instructions run
+// side by side only from different wavefronts, so two to four share a SIMD. 18000 tokens of
+// 32/8 heads of 128: 900 us, 990 TFLOP/s (a large product reaches 1531; the counters of 15000
+// tokens have the matrix cores busy in 44% of the cycles, LDS in 22%, without a conflict).
+// Without exponentials, maximum or sums it takes 3 to 6% less each, with all copies from one
+// tile 1%: none of them alone is what it waits for.
 #include <type_traits>
 
 #include "attn_common.h"

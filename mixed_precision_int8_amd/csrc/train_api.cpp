@@ -292,7 +292,6 @@ static hipError_t grad_batches_of(const llmint8_grad* grads, int64_t count, Laun
   }
   return hipSuccess;
 }
-// Many tensors in few launches, 16 KB of arguments each; a few are not made to carry those.
 template <class Launch>
 static hipError_t grad_batches(const llmint8_grad* grads, int64_t count, Launch&& launch) {
   return count > kGradFew ? grad_batches_of<kGradMany>(grads, count, launch)

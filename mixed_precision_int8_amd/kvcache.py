@@ -422,6 +422,8 @@ class Int8SelfAttention:
         or written. Rows of no sequence attend to nothing."""
         m8 = _m8()
         self._positions(pos)
+        if self.rope is not None and pos is None and rows.max_len > self.rope.shape[0]:
+            raise ValueError(f"rope: a table of {self.rope.shape[0]} positions for sequences of {rows.max_len} tokens")
         nq, n = self.q_heads, X.shape[0]
         if self.norm is not None:
             X = self.norm(X)

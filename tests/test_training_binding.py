@@ -197,3 +197,14 @@ def test_tensors_are_made_to_fit():
     assert training._fit(x[..., 4:]).data_ptr() == x.data_ptr() + 16 and training._fit(x[:, :2]).data_ptr() == x.data_ptr()
     h = x.half()
     assert training._fit(h[..., 4:]).is_contiguous() and training._fit(h[..., 8:]).data_ptr() == h.data_ptr() + 16
+
+
+def test_sequences_longer_than_the_table_are_refused():
+    layer = object.__new__(m8.Int8SelfAttention)
+    layer.rope, layer.axis, layer.norm = torch.zeros((100, 32)), None, None
+    rows = object.__new__(m8.PackedRows)
+    rows.max_len = 101
+    with pytest.raises(ValueError, match="100 positions"):
+        layer.packed(torch.zeros((101, 8)), rows)
+    with pytest.raises(ValueError, match="pos"):
+        layer.packed(torch.zeros((101, 8)), rows, torch.zeros((101, 1)))

@@ -549,8 +549,8 @@ LLMINT8_API llmint8_status llmint8_kv_attention(const llmint8_kv_cache* cache, c
  *   out = sum_j P_j v_j, P = softmax(scale q . k); lse = log sum_j exp(scale q . k_j)
  *   delta = sum_c dout out; dv = P^T dout; dS = P (dout . v - delta);
  *   dq = scale dS k; dk = scale dS^T q, dk and dv summed over a group's query heads
- * (delta is summed as sum_j P_j (dout . v_j) where rows see few tokens: out has been
- * rounded, which would show there)
+ * (where sums go over few tokens, delta is summed as sum_j P_j (dout . v_j), as out has
+ * been rounded, and P and dS take part to twice the type's bits)
  * Each output is rounded once. Logits, statistics, sums and delta are fp32; exp, log
  * and reciprocals are the hardware's. P and dS are rounded to the 16-bit type for the
  * products that sum over them: to 2^-8 (bf16) or 2^-11 (fp16) of each, in fp16 but for

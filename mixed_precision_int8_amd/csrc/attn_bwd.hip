@@ -82,6 +82,11 @@ struct AttnRowsOf {
   __device__ __forceinline__ bool masked(int base) const { return (base < all_from) | (base + 64 > all_until); }
 };
 
+// Sums over this many tiles at most (256 tokens) are of few enough terms for the rounding of one
+// to show: there P and dS take part to twice the type's bits, by a second product, and delta
+// (a mean over the tokens; over more of them its rounding is a 16th of one's) is summed anew.
+constexpr int kFew = 4;
+
 }  // namespace
 
 template <int DP, bool BF16>
@@ -89,7 +94,6 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_dq(AttnArgs a) {
   using Tile = AttnTile<DP>;
   constexpr int W = 4, kRows = 32 * W, NQ = Tile::NQ, ND = Tile::ND;
   constexpr int kStage = 2 * Tile::kBytes;  // k, v
-  constexpr int kFew = 4;                   // tiles: 256 tokens, whose mean is a 16th of one's size and its rounding too
   __shared__ __attribute__((aligned(1024))) char smem[2 * kStage + 16];
   int* const flag = reinterpret_cast<int*>(smem + 2 * kStage);
   const int D = a.dim, H = a.heads, G = a.q_heads / H;
@@ -203,55 +207,63 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_dq(AttnArgs a) {
   for (int d = 0; d < ND; ++d) acc[d] = attn_zero();
   Reach<BF16, ND> reach;
 
-  for (int i = 0; i < tiles; ++i) {
-    const int stage = i & 1, base = base_of(i);
-    const bool masked = all.masked(base);
-    attn_wait_copies();
-    if (masked) ck.template finite<BF16>(smem + stage * kStage, flag);
-    attn_barrier();
-    copy(i + 1, stage ^ 1);
+  auto loop = [&](auto few) {  // a loop of its own for each, so that the other has nothing of it
+    for (int i = 0; i < tiles; ++i) {
+      const int stage = i & 1, base = base_of(i);
+      const bool masked = all.masked(base);
+      attn_wait_copies();
+      if (masked) ck.template finite<BF16>(smem + stage * kStage, flag);
+      attn_barrier();
+      copy(i + 1, stage ^ 1);
 #pragma unroll
-    for (int sb = 0; sb < 2; ++sb) {
-      if (idle | own.none(base + 32 * sb, 32)) continue;
-      v16f_t s = attn_rows_product<DP, BF16>(rd, 0, sb, q);
-      v16f_t t = attn_rows_product<DP, BF16>(rd, 1, sb, g);
-      // 256 channels leave no registers for operands read this early (172 of them went to memory in
-      // fp16: 1209 us for the gradients of 7000 tokens of 16/4 heads, 751 without)
-      constexpr bool kEarly = DP <= 128;
-      uint4 y[2][kEarly ? ND : 1];
-      if constexpr (kEarly) {
+      for (int sb = 0; sb < 2; ++sb) {
+        if (idle | own.none(base + 32 * sb, 32)) continue;
+        v16f_t s = attn_rows_product<DP, BF16>(rd, 0, sb, q);
+        v16f_t t = attn_rows_product<DP, BF16>(rd, 1, sb, g);
+        // 256 channels leave no registers for operands read this early (172 of them went to memory in
+        // fp16: 1209 us for the gradients of 7000 tokens of 16/4 heads, 751 without)
+        constexpr bool kEarly = DP <= 128;
+        uint4 y[2][kEarly ? ND : 1];
+        if constexpr (kEarly) {
 #pragma unroll
-        for (int d = 0; d < ND; ++d) y[0][d] = rd.channels(0, d, 2 * sb);
-      }
+          for (int d = 0; d < ND; ++d) y[0][d] = rd.channels(0, d, 2 * sb);
+        }
 #pragma unroll
-      for (int x = 0; x < 16; ++x) t[x] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x], f, -lse2)) * (t[x] - delta);
-      if (own.masked(base)) {
+        for (int x = 0; x < 16; ++x) t[x] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x], f, -lse2)) * (t[x] - delta);
+        if (own.masked(base)) {
 #pragma unroll
-        for (int x = 0; x < 16; ++x)
-          if (!sees(base + 32 * sb + 16 * (x >> 3) + 8 * hf + (x & 7))) t[x] = 0.0f;
-      }
-      if constexpr (!BF16) {
-        reach.fit(t, acc);
-        t *= reach.g;
-      }
-      if constexpr (!kEarly) {
-        attn_channels_product<DP, BF16>(rd, 0, sb, t, acc);
-      } else {
+          for (int x = 0; x < 16; ++x)
+            if (!sees(base + 32 * sb + 16 * (x >> 3) + 8 * hf + (x & 7))) t[x] = 0.0f;
+        }
+        if constexpr (!BF16) {
+          reach.fit(t, acc);
+          t *= reach.g;
+        }
+        if constexpr (!kEarly) {
+          attn_channels_product<DP, BF16>(rd, 0, sb, t, acc);
+        } else {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          if (k == 0) {
+          for (int k = 0; k < 2; ++k) {
+            if (k == 0) {
 #pragma unroll
-            for (int d = 0; d < ND; ++d) y[1][d] = rd.channels(0, d, 2 * sb + 1);
+              for (int d = 0; d < ND; ++d) y[1][d] = rd.channels(0, d, 2 * sb + 1);
+            }
+            const uint4 p = attn_pack<BF16>(t, k);
+#pragma unroll
+            for (int d = 0; d < ND; ++d) acc[d] = Act16<BF16>::mma32(y[k][d], p, acc[d]);
+            __builtin_amdgcn_sched_barrier(0);
           }
-          const uint4 p = attn_pack<BF16>(t, k);
-#pragma unroll
-          for (int d = 0; d < ND; ++d) acc[d] = Act16<BF16>::mma32(y[k][d], p, acc[d]);
-          __builtin_amdgcn_sched_barrier(0);
+        }
+        if constexpr (few()) {
+          attn_residual<BF16>(t);
+          attn_channels_product<DP, BF16>(rd, 0, sb, t, acc);
         }
       }
+      rd.next(stage ? -kStage : kStage);
     }
-    rd.next(stage ? -kStage : kStage);
-  }
+  };
+  if (tiles <= kFew) loop(std::true_type{});
+  else loop(std::false_type{});
   attn_wait_copies();
   if (__builtin_expect(uniform(*flag), 0)) {
 #pragma unroll 1
@@ -266,7 +278,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_dq(AttnArgs a) {
   store_sums<DP, BF16>(acc, a.scale / reach.g, a.dq, qrow, qh, D, hf);
 }
 
-// Up to 96 channels a wavefront has the registers for dV and dK of 32 tokens (204 and 252), two
+// Up to 96 channels a wavefront has the registers for dV and dK of 32 tokens (184 and 240), two
 // wavefronts to a SIMD, and nothing goes through LDS between them: 278 us where pairs of
 // wavefronts as below take 561 on 32000 tokens with a window of 500, 16 heads of 64 in fp16;
 // 320 and 446 on 20 images, 16 heads of 80 in bf16.
@@ -343,58 +355,72 @@ __global__ __launch_bounds__(256, 2) void ka_dkv_alone(AttnArgs a) {
   Reach<BF16, ND> reach;
   AttnRead<DP> rd(smem);
   const char* st = smem + kAtStat + 32 * hf;
-  int at = lo;
-  for (int i = 0; i < tiles; ++i) {
-    const int stage = i & 1, base = at << 6;
-    const bool masked = see.masked(base), hidden = own.masked(base);
-    attn_wait_copies();
-    if (masked) {
-      cq.template finite<BF16>(smem + stage * kStage, flag);
-      cg.template finite<BF16>(smem + stage * kStage + Tile::kBytes, flag);
+  auto loop = [&](auto few) {
+    int at = lo;
+    for (int i = 0; i < tiles; ++i) {
+      const int stage = i & 1, base = at << 6;
+      const bool masked = see.masked(base), hidden = own.masked(base);
+      attn_wait_copies();
+      if (masked) {
+        cq.template finite<BF16>(smem + stage * kStage, flag);
+        cg.template finite<BF16>(smem + stage * kStage + Tile::kBytes, flag);
+      }
+      attn_barrier();
+      copy(stage ^ 1);
+#pragma unroll
+      for (int sb = 0; sb < 2; ++sb) {
+        if (idle | (base + 32 * sb + 32 <= own.first) | (base + 32 * sb >= own.end)) continue;
+        auto stat = [&](int which, int e) {
+          return *reinterpret_cast<const v4f*>(st + 256 * which + 128 * sb + 64 * (e >> 1) + 16 * (e & 1));
+        };
+        auto mask = [&](v16f_t& x) {
+          int row = base + 32 * sb + 8 * hf;
+          asm volatile("" : "+v"(row));  // or 16 rows less this token's first one are kept in registers
+#pragma unroll
+          for (int z = 0; z < 16; ++z)
+            if (!see(row + 16 * (z >> 3) + (z & 7))) x[z] = 0.0f;
+        };
+        v16f_t s = attn_rows_product<DP, BF16>(rd, 0, sb, kr);
+        v16f_t t;
+        if constexpr (!few()) t = attn_rows_product<DP, BF16>(rd, 1, sb, vr);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const v4f l = stat(0, e);
+#pragma unroll
+          for (int z = 0; z < 4; ++z) s[4 * e + z] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[4 * e + z], f, l[z]));
+        }
+        if (hidden) mask(s);
+        attn_channels_product<DP, BF16>(rd, 1, sb, s, dv);
+        if constexpr (few()) {
+          v16f_t r = s;
+          attn_residual<BF16>(r);
+          attn_channels_product<DP, BF16>(rd, 1, sb, r, dv);
+          t = attn_rows_product<DP, BF16>(rd, 1, sb, vr);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const v4f l = stat(1, e);
+#pragma unroll
+          for (int z = 0; z < 4; ++z) t[4 * e + z] = s[4 * e + z] * (t[4 * e + z] - l[z]);
+        }
+        if (hidden) mask(t);  // do is not finite in a row that this token does not see, or its delta
+        if constexpr (!BF16) {
+          reach.fit(t, dk);
+          t *= reach.g;
+        }
+        attn_channels_product<DP, BF16>(rd, 0, sb, t, dk);
+        if constexpr (few()) {
+          attn_residual<BF16>(t);
+          attn_channels_product<DP, BF16>(rd, 0, sb, t, dk);
+        }
+      }
+      rd.next(stage ? -kStage : kStage);
+      st += stage ? -512 : 512;
+      if (++at == lo + per) at = lo;
     }
-    attn_barrier();
-    copy(stage ^ 1);
-#pragma unroll
-    for (int sb = 0; sb < 2; ++sb) {
-      if (idle | (base + 32 * sb + 32 <= own.first) | (base + 32 * sb >= own.end)) continue;
-      auto stat = [&](int which, int e) {
-        return *reinterpret_cast<const v4f*>(st + 256 * which + 128 * sb + 64 * (e >> 1) + 16 * (e & 1));
-      };
-      v16f_t s = attn_rows_product<DP, BF16>(rd, 0, sb, kr);
-      v16f_t t = attn_rows_product<DP, BF16>(rd, 1, sb, vr);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const v4f l = stat(0, e);
-#pragma unroll
-        for (int z = 0; z < 4; ++z) s[4 * e + z] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[4 * e + z], f, l[z]));
-      }
-      if (hidden) {
-#pragma unroll
-        for (int z = 0; z < 16; ++z)
-          if (!see(base + 32 * sb + 16 * (z >> 3) + 8 * hf + (z & 7))) s[z] = 0.0f;
-      }
-      attn_channels_product<DP, BF16>(rd, 1, sb, s, dv);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const v4f l = stat(1, e);
-#pragma unroll
-        for (int z = 0; z < 4; ++z) t[4 * e + z] = s[4 * e + z] * (t[4 * e + z] - l[z]);
-      }
-      if (hidden) {  // do is not finite in a row that this token does not see, or its delta
-#pragma unroll
-        for (int z = 0; z < 16; ++z)
-          if (!see(base + 32 * sb + 16 * (z >> 3) + 8 * hf + (z & 7))) t[z] = 0.0f;
-      }
-      if constexpr (!BF16) {
-        reach.fit(t, dk);
-        t *= reach.g;
-      }
-      attn_channels_product<DP, BF16>(rd, 0, sb, t, dk);
-    }
-    rd.next(stage ? -kStage : kStage);
-    st += stage ? -512 : 512;
-    if (++at == lo + per) at = lo;
-  }
+  };
+  if (per <= kFew) loop(std::true_type{});
+  else loop(std::false_type{});
   attn_wait_copies();
   if (__builtin_expect(uniform(*flag), 0)) {
 #pragma unroll 1
@@ -543,6 +569,10 @@ __global__ __launch_bounds__(DP <= 128 ? 512 : 256, DP <= 128 ? 2 : 1) void ka_d
     for (int z = 0; z < 16; ++z)
       if (!see(base + 16 * (z >> 3) + 8 * hf + (z & 7))) s[z] = 0.0f;
   };
+  auto again = [&](v16f_t& s) {
+    attn_residual<BF16>(s);
+    attn_channels_product<DP, BF16>(rd, 0, 0, s, acc);
+  };
   // the end of the first wavefront's step (i, sb)
   auto turn = [&](int i, int sb) {
     if (sb == (kStages == 2)) arrive(i + 1);
@@ -590,6 +620,7 @@ __global__ __launch_bounds__(DP <= 128 ? 512 : 256, DP <= 128 ? 2 : 1) void ka_d
           acc[n % ND] = Act16<BF16>::mma32(ring[n % kRing], x, acc[n % ND]);
           __builtin_amdgcn_sched_barrier(0);
         }
+        if (per <= kFew) again(s);
         rd.next_channels(by);
         st_mine += (stage - was) * 512 + (sb ? -128 : 128);
         turn(i, sb);
@@ -654,6 +685,7 @@ __global__ __launch_bounds__(DP <= 128 ? 512 : 256, DP <= 128 ? 2 : 1) void ka_d
           if (sb == 0 && c == kCopyAt) copy();
           __builtin_amdgcn_sched_barrier(0);
         }
+        if (per <= kFew) again(t);
         rd.next_channels(by);
         st_mine += (stage - was) * 512 + (sb ? -128 : 128);
         rows_products(kBegin, NQ, u);  // nobody's after the last step

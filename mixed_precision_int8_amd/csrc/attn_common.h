@@ -366,6 +366,22 @@ __device__ __forceinline__ uint4 attn_pack(const v16f_t& t, int k) {
                     A::pack2(t[8 * k + 4], t[8 * k + 5]), A::pack2(t[8 * k + 6], t[8 * k + 7]));
 }
 
+// What rounding values to the type leaves of them, nothing where they are not finite: a second
+// product with it takes away the rounding of the first.
+template <bool BF16>
+__device__ __forceinline__ void attn_residual(v16f_t& t) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint4 p = attn_pack<BF16>(t, k);
+    const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float left = t[8 * k + j] - Act16<BF16>::to_f32(j & 1 ? w[j >> 1] >> 16 : w[j >> 1] & 0xffffu);
+      t[8 * k + j] = __builtin_isfinite(left) ? left : 0.0f;
+    }
+  }
+}
+
 // acc += the tile's channels x rows [32 block, +32) times t, operands read two products ahead
 template <int DP, bool BF16>
 __device__ __forceinline__ void attn_channels_product(const AttnRead<DP>& rd, int tile, int block, const v16f_t& t,

@@ -20,7 +20,8 @@ def attention(lens, q, k, v, scale, causal=True, window=0, sinks=0, dout=None, u
     """Packed sequences of ``lens`` tokens; q [T, hq, D], k and v [T, hk, D]. A dict of out, lse and, with ``dout``,
     dq, dk, dv; with ``unit`` (half a step of the 16-bit type) also of ``e_out`` and so on: how far a result may be
     off whose products take P and dS rounded to the type, with fp32 logits and sums (``floor``: the type is fp16,
-    which holds them to a floor as well; ``few``: delta is summed from P and dP, not from the rounded o)."""
+    which holds them to a floor as well; ``few``: delta is summed from P and dP, not from the rounded
+    o, and P and dS enter the gradients' products to twice the type's bits)."""
     T, hq, D = q.shape
     hk, G = k.shape[1], hq // k.shape[1]
     q, k, v = (x.astype(np.float64) for x in (q, k, v))
@@ -76,12 +77,13 @@ def attention(lens, q, k, v, scale, causal=True, window=0, sinks=0, dout=None, u
             e_w = d + d_row + sums + 8 * np.abs(r["lse"][rows, h])[:, None] * f32  # of a weight before it is rounded
             if few:
                 e_delta = (p * (np.abs(dp) * (e_w + (n + 2) * f32) + e_dp)).sum(1, keepdims=True)
-            e_ds = np.abs(ds) * (unit + e_w) + p * (1 + e_w) * (e_dp + e_delta)
+            u = unit * unit if few else unit
+            e_ds = np.abs(ds) * (u + e_w) + p * (1 + e_w) * (e_dp + e_delta)
             e_q = e_k = e_ds
             if floor:
                 e_q = e_ds + 2.0 ** -32 * np.abs(ds).max(1, keepdims=True)
                 e_k = e_ds + 2.0 ** -32 * np.abs(ds).max(0, keepdims=True)
-            e_pv = p * (unit + e_w) + (2.0 ** -39 if floor else 0.0)
+            e_pv = p * (u + e_w) + (2.0 ** -39 if floor else 0.0)
             acc = (n + 8) * f32
             r["e_dq"][rows, h] = abs(scale) * (e_q @ np.abs(ki) + acc * np.abs(ds) @ np.abs(ki))
             r["e_dk"][rows, g] += abs(scale) * (e_k.T @ np.abs(qi) + G * acc * np.abs(ds).T @ np.abs(qi))

@@ -93,20 +93,21 @@ def test_strided_expanded_and_shared_inputs():
 
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("how", [{}, {"causal": False}, {"window": 7, "sinks": 1}])
-def test_gradients_of_short_sequences_do_not_take_the_rounding_of_o(dtype, how):
-    """Where rows see 256 tokens at most (or a short window), dS is off by its own rounding alone: o, rounded to the
-    type, would bring do times half a step of it into every dS of a row."""
-    print(f"[case] short {dtype} {how}", flush=True)
+@pytest.mark.parametrize("dim", [64, 96, 128, 256])
+def test_gradients_of_short_sequences_are_rounded_once(dtype, dim, how):
+    """Where sums go over 256 tokens at most, the result's rounding is the only one to count: P and dS take part to
+    twice the type's bits, and o, rounded, would bring do times half a step of it into every dS of a row."""
+    print(f"[case] short {dtype} {dim} {how}", flush=True)
     lens = [1, 2, 3, 60, 17, 256, 5, 130]
     T = sum(lens)
-    q, k, v, do = (randn(200 + i, T, h, 64, dtype=dtype) for i, h in enumerate((4, 2, 2, 4)))
+    q, k, v, do = (randn(200 + i, T, h, dim, dtype=dtype) for i, h in enumerate((4, 2, 2, 4)))
     v = v + 8  # o is far from zero, its rounding as well
     b = m8.PackedRows.of(lens)
     out, lse = m8.llmint8_attention(b, q, k, v, **how)
     grads = m8.llmint8_attention_backward(b, q, k, v, out, lse, do, **how)
     unit = 2.0 ** -11 if dtype == torch.float16 else 2.0 ** -8
     host = [t.float().cpu().numpy() for t in (q, k, v)]
-    want = ref.attention(lens, *host, 0.125, dout=do.float().cpu().numpy(), unit=unit, floor=dtype == torch.float16,
+    want = ref.attention(lens, *host, np.float32(1 / np.sqrt(dim)), dout=do.float().cpu().numpy(), unit=unit, floor=dtype == torch.float16,
                          few=True, **how)
     for name, t in zip(("dq", "dk", "dv"), grads):
         off = np.abs(t.float().cpu().numpy() - want[name]) / (want["e_" + name] + (2.0 ** -25 if unit == 2.0 ** -11 else 2.0 ** -134))

@@ -83,8 +83,10 @@ struct AttnRowsOf {
 };
 
 // Sums over this many tiles at most (256 tokens) are of few enough terms for the rounding of one
-// to show: there P and dS take part to twice the type's bits, by a second product, and delta
-// (a mean over the tokens; over more of them its rounding is a 16th of one's) is summed anew.
+// to show: there P and dS take part to twice the type's bits, by a second product, and delta is
+// summed anew (3 to 60 tokens, fp16: dq and dk off by 2.1e-4 instead of 3.8e-4 of their size; the
+// three kernels 26 us instead of 23). Over more tokens errors of single terms average out; o is
+// their mean, and its rounding a 16th or less of the spread of do V^T.
 constexpr int kFew = 4;
 
 }  // namespace
@@ -164,8 +166,8 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_dq(AttnArgs a) {
   AttnRead<DP> rd(smem);
   const AttnSees sees(a, pos, sq.n);
 
-  // o has been rounded, and so is delta off by 2^-12 (2^-9) of do o: little beside the spread of
-  // do V^T where many tokens share a row's weight, as much as all other roundings where few do.
+  // o has been rounded, and so is delta off by half a step of it times do: little beside the
+  // spread of do V^T where many tokens share a row's weight, as much as all else where few do.
   // There delta is summed from its definition, sum_j P_ij (do V^T)_ij: two products more.
   if (tiles <= kFew) {
     delta = 0.0f;

@@ -628,7 +628,9 @@ def _fit(t):
     """_dense_channels, in 16-byte pieces as attention reads them."""
     t = _dense_channels(t)
     fine = t.data_ptr() % 16 == 0 and all(s % 8 == 0 for s in t.stride()[:-1])
-    return t if fine else t.contiguous()
+    # a copy even of a contiguous tensor that only begins at an odd place, as slices of a flat one do: contiguous()
+    # would hand back the tensor itself
+    return t if fine else t.clone(memory_format=torch.contiguous_format)
 
 
 _FN = None

@@ -11,7 +11,7 @@ from mixed_precision_int8_amd import training  # noqa: E402
 
 def test_a_contiguous_tensor_at_an_odd_place_is_copied():
     training._library()
-    flat = torch.arange(3 + 6 * 4 * 16).half()
+    flat = torch.arange(8 + 6 * 4 * 16).half()
     for first in (1, 3):
         t = flat[first:first + 6 * 4 * 16].view(6, 4, 16)
         assert t.is_contiguous() and t.data_ptr() % 16 != 0

@@ -419,11 +419,14 @@ class Int8SelfAttention:
 
     def packed(self, X, rows, pos=None):
         """Y [rows, hidden] of whole sequences X [rows, hidden] (``PackedRows``), differentiable; no cache is read
-        or written. Rows of no sequence attend to nothing."""
+        or written. Rows of no sequence attend to nothing. The rope table has to have a row for every position that the
+        batch may have: of its longest sequence, or of ``rows`` where the batch does not know that (a captured call
+        is checked when it is captured)."""
         m8 = _m8()
         self._positions(pos)
-        if self.rope is not None and pos is None and rows.max_len > self.rope.shape[0]:
-            raise ValueError(f"rope: a table of {self.rope.shape[0]} positions for sequences of {rows.max_len} tokens")
+        if self.rope is not None and pos is None and rows.longest() > self.rope.shape[0]:
+            raise ValueError(f"rope: a table of {self.rope.shape[0]} positions for sequences of up to {rows.longest()} "
+                             "tokens (PackedRows takes max_len where the host knows a bound)")
         nq, n = self.q_heads, X.shape[0]
         if self.norm is not None:
             X = self.norm(X)

@@ -126,10 +126,15 @@ def _like(t, stream):
 
 class PackedRows:
     """Sequences one after the other: rows cu[b] .. cu[b+1]-1 (``cu`` int32 [seqs + 1], device memory) are sequence
-    b of a call whose tensors have ``rows`` rows. ``used``, where the host knows it: cu[seqs] (rows past it belong
-    to no sequence). The contents of ``cu`` may change between calls. ``max_len`` is the longest sequence, if known."""
+    b of a call whose tensors have ``rows`` rows. The contents of ``cu`` may change between calls and between a
+    captured graph's replays.
 
-    __slots__ = ("cu", "seqs", "rows", "device", "used", "max_len")
+    ``used``, where the host knows it: cu[seqs] (rows past it belong to no sequence). It is of what cu holds now: after
+    an operation on cu, and in a captured call, it counts as unknown. ``max_len``, if known: no sequence is longer,
+    whatever cu will hold (``of`` knows it of its lengths only). Operations on cu are seen as autograd sees them, by
+    its version; who writes its memory behind that (``cu.data``, a kernel of their own) gives neither."""
+
+    __slots__ = ("cu", "seqs", "rows", "device", "used", "max_len", "_version", "_of")
 
     def __init__(self, cu, rows, max_len=0, used=None):
         _library()
@@ -138,10 +143,12 @@ class PackedRows:
             raise ValueError(f"cu: expected [seqs + 1], got {tuple(cu.shape)}")
         m8._need(cu, torch.int32, (self.seqs + 1,), "cu")
         self.rows = int(rows)
-        if self.rows < 0 or max_len < 0:
-            raise ValueError("rows and max_len: expected >= 0")
+        if self.rows < 0 or max_len < 0 or (used is not None and used < 0):
+            raise ValueError("rows, max_len and used: expected >= 0")
         self.cu, self.device, self.max_len = cu, cu.device, int(max_len)
-        self.used = used
+        self.used = None if used is None else min(int(used), self.rows)
+        self._version = None if cu.is_inference() else cu._version  # None: changes of cu are not seen
+        self._of = False
 
     @classmethod
     def of(cls, lengths, rows=None, device="cuda"):
@@ -154,8 +161,27 @@ class PackedRows:
             at.append(at[-1] + int(n))
         if rows is not None and rows < at[-1]:
             raise ValueError(f"rows: {rows}, and the sequences have {at[-1]}")
-        return cls(torch.tensor(at, dtype=torch.int32).to(device), at[-1] if rows is None else rows,
-                   max_len=max(lengths, default=0), used=at[-1])
+        with torch.inference_mode(False):  # inference tensors have no version
+            cu = torch.tensor(at, dtype=torch.int32).to(device)
+        batch = cls(cu, at[-1] if rows is None else rows, max_len=max(lengths, default=0), used=at[-1])
+        batch._of = True
+        return batch
+
+    def _as_told(self):
+        """cu holds what it held when ``used`` was given, and every run of this call will find that there."""
+        return self._version is not None and self.cu._version == self._version
+
+    def used_rows(self):
+        """``used`` while it holds, else None."""
+        if self.used is None or not self._as_told() or torch.cuda.is_current_stream_capturing():
+            return None
+        return self.used
+
+    def longest(self):
+        """No sequence has more tokens, as far as the host knows."""
+        if getattr(self, "_of", False):
+            return self.max_len if self._as_told() else self.rows
+        return self.max_len or self.rows
 
     def positions(self):
         """int32 [rows]: every row's place in its sequence, from what cu holds now (rows of no sequence: any)."""
@@ -514,10 +540,11 @@ def clip_grad_norm(parameters, max_norm, scale=1.0):
 
 def _unused(t, batch):
     """A new output of a packed call: rows of no sequence are zeros, as the kernels leave them alone."""
-    if batch.used is None:
+    used = batch.used_rows()
+    if used is None:
         t.zero_()
-    elif batch.used < batch.rows:
-        t[batch.used:].zero_()
+    elif used < batch.rows:
+        t[used:].zero_()
     return t
 
 

@@ -56,3 +56,80 @@ def test_attention_takes_tensors_that_begin_at_an_odd_place(first):
     m8.qkv_attention(x, 2, b).backward(g)
     torch.cat([aux, m8.qkv_attention(y, 2, b).flatten()]).backward(torch.cat([aux, g.flatten()]))
     assert torch.equal(x.grad, y.grad)
+
+
+def layer(hidden=256, nq=4, heads=2, dim=64, **kw):
+    rope = m8.llmint8_rope_table(m8.rope_frequencies(dim)[0], 400)
+    return m8.Int8SelfAttention(randn(5, (nq + 2 * heads) * dim, hidden, scale=0.05),
+                                randn(6, hidden, nq * dim, scale=0.05), nq, None, rope, heads=heads, dim=dim, **kw)
+
+
+def poison():
+    """Leaves NaN in the memory that the next tensors get."""
+    held = [torch.full((n,), float("nan"), dtype=torch.float16, device="cuda") for n in (1 << k for k in range(10, 20))]
+    del held
+
+
+def test_rows_of_no_sequence_after_a_change_of_cu():
+    """Rows that a shorter cu leaves to no sequence are zeros, in outputs and gradients; the layer's other rows do not
+    see them."""
+    print("[case] cu shrinks", flush=True)
+    b = m8.PackedRows.of([70, 50])
+    b.cu.copy_(torch.tensor([0, 40, 60], dtype=torch.int32))
+    q, k, v, g = (randn(i, 120, h, 64) for i, h in enumerate((4, 2, 2, 4)))
+    now = m8.PackedRows.of([40, 20], rows=120)
+    got, want = [leaf(t) for t in (q, k, v)], [leaf(t) for t in (q, k, v)]
+    for ts, batch in ((got, b), (want, now)):
+        poison()
+        out = m8.packed_attention(*ts, batch)
+        assert (out[60:] == 0).all()
+        poison()
+        out.backward(g)
+        for t in ts:
+            assert (t.grad[60:] == 0).all()
+    for a, t in zip(got, want):
+        assert torch.equal(a.grad, t.grad)
+    w = leaf(torch.ones(256, device="cuda"))
+    net = layer(norm=m8.LayerNorm(w))
+    X, dy = randn(10, 120, 256), randn(11, 120, 256)
+    res = []
+    for batch in (b, now):
+        x = leaf(X)
+        w.grad = None
+        poison()
+        y = net.packed(x, batch)
+        poison()
+        y.backward(dy)
+        res.append((y.detach(), x.grad, w.grad.clone()))
+    for a, t in zip(*res):
+        assert torch.isfinite(a).all() and torch.equal(a, t)
+
+
+def test_rows_of_no_sequence_in_a_replayed_call():
+    """A call captured with all rows in use, replayed on shorter sequences."""
+    print("[case] replay on a shorter cu", flush=True)
+    b = m8.PackedRows.of([70, 50])
+    q, k, v, g = (randn(i, 120, h, 64) for i, h in enumerate((4, 2, 2, 4)))
+
+    def step():
+        ts = [t.detach().requires_grad_() for t in (q, k, v)]
+        out = m8.packed_attention(*ts, b)
+        return (out.detach(), *torch.autograd.grad(out, ts, g))
+
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        step()
+        stream.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            held = step()
+    for cu in ([0, 70, 120], [0, 10, 25], [0, 0, 0], [0, 70, 120]):
+        b.cu.copy_(torch.tensor(cu, dtype=torch.int32))
+        for t in held:
+            t.fill_(float("nan"))
+        want = step()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, t in zip(held, want):
+            assert torch.equal(a, t) and (a[cu[-1]:] == 0).all(), cu

@@ -133,3 +133,29 @@ def test_rows_of_no_sequence_in_a_replayed_call():
         torch.cuda.synchronize()
         for a, t in zip(held, want):
             assert torch.equal(a, t) and (a[cu[-1]:] == 0).all(), cu
+
+
+def test_a_set_follows_gradients_that_move():
+    """Module.half() and the like give gradients other memory and types: the set's calls clip what is there now, and
+    leave alone what was."""
+    print("[case] moved gradients", flush=True)
+    model = torch.nn.Sequential(*(torch.nn.Linear(33, 33) for _ in range(3))).cuda()
+    params = list(model.parameters())
+    for i, p in enumerate(params):
+        p.grad = randn(i, *p.shape, dtype=torch.float32)
+    gset = m8.GradientSet([p.grad for p in params])
+    for change in (None, model.half, model.float, model.bfloat16):
+        before = [p.grad.detach() for p in params]
+        kept = [t.clone() for t in before]
+        if change is not None:
+            change()
+        now = [p.grad.clone() for p in params]
+        norm = m8.llmint8_grad_norm(gset)
+        m8.llmint8_grad_clip(gset, norm, 0.5)
+        want = ref.grad_norm([t.float().cpu().numpy() for t in now])
+        assert abs(float(norm) / want - 1) <= 2.0 ** -22
+        f = float(ref.grad_factor(norm.item(), 0.5))
+        for p, t in zip(params, now):
+            assert torch.equal(p.grad, (t.float() * f).to(t.dtype)), change
+        if change is not None:
+            assert all(torch.equal(a, b) for a, b in zip(before, kept)), change

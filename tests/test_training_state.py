@@ -112,3 +112,109 @@ def test_the_longest_sequence_after_a_change_of_cu(packed):
     for rows in (bound, m8.PackedRows(b.cu, 100), m8.PackedRows.of([], rows=300, device="cpu")):
         with pytest.raises(Passed):
             run(rows)
+
+
+@pytest.fixture
+def gradients(monkeypatch):
+    """[what the library was handed: (name, [(data, out, n, dtype, out_dtype)])], with tensors that pass for a GPU's."""
+    training._library()
+    calls = []
+
+    class Library:
+        def __getattr__(self, name):
+            def call(*a):
+                if name.endswith("bytes"):
+                    return 8 * sum(a[0][i].n for i in range(a[1]))
+                calls.append((name, [(e.data, e.out, e.n, e.dtype, e.out_dtype) for e in a[0][:a[1]]]))
+                return 0
+            return call
+
+    monkeypatch.setattr(m8, "load_library", Library)
+    monkeypatch.setattr(torch.Tensor, "is_cuda", True)
+    monkeypatch.setattr(training, "_handle", lambda stream, device: 0)
+    return calls
+
+
+CODE = {torch.float16: m8.LLMINT8_DTYPE_F16, torch.bfloat16: m8.LLMINT8_DTYPE_BF16, torch.float32: m8.LLMINT8_DTYPE_F32}
+
+
+def entries(grads, outs):
+    return [(g.data_ptr(), o.data_ptr(), g.numel(), CODE[g.dtype], CODE[o.dtype]) for g, o in zip(grads, outs)]
+
+
+def handed(calls, gset, norm):
+    """What both calls hand over; the workspace is of what they do."""
+    calls.clear()
+    m8.llmint8_grad_norm(gset, norm=norm)
+    m8.llmint8_grad_clip(gset, norm, 1.0)
+    (first, a), (second, b) = calls
+    assert (first, second) == ("llmint8_grad_norm", "llmint8_grad_clip") and a == b
+    assert gset.workspace_bytes() == 8 * sum(e[2] for e in a)
+    return a
+
+
+def test_a_set_follows_gradients_that_move(gradients):
+    norm = torch.zeros(())
+    model = torch.nn.Sequential(torch.nn.Linear(7, 5), torch.nn.Linear(5, 3))
+    for p in model.parameters():
+        p.grad = torch.ones_like(p)
+    grads = [p.grad for p in model.parameters()]
+    gset = m8.GradientSet(grads)
+    assert handed(gradients, gset, norm) == entries(grads, grads)
+    held = [g.detach() for g in grads]  # so that the new ones are elsewhere
+    for change in (model.half, model.bfloat16, model.float):
+        change()
+        assert [p.grad.dtype for p in model.parameters()] == [grads[0].dtype] * 4
+        held += [g.detach() for g in grads]
+        assert handed(gradients, gset, norm) == entries(grads, grads), change
+    grads[1].data = torch.zeros(5)          # the same type, other memory
+    assert handed(gradients, gset, norm) == entries(grads, grads)
+    grads[0].data = grads[0].data[:2]       # the same place, fewer values
+    assert handed(gradients, gset, norm) == entries(grads, grads)
+    grads[1].data = grads[1].data.view(torch.float16)  # the same place, another type
+    assert handed(gradients, gset, norm) == entries(grads, grads)
+
+
+def test_a_set_follows_outputs_that_move(gradients):
+    norm = torch.zeros(())
+    grads, outs = [torch.zeros(9).half(), torch.zeros(4).half()], [torch.zeros(9), torch.zeros(4)]
+    gset = m8.GradientSet(grads, out=outs)
+    assert handed(gradients, gset, norm) == entries(grads, outs)
+    outs[1].data = torch.zeros(4)
+    assert handed(gradients, gset, norm) == entries(grads, outs)
+    outs[0].data = torch.zeros(9).half()
+    assert handed(gradients, gset, norm) == entries(grads, outs)
+
+
+def test_a_set_whose_tensors_no_longer_fit_is_refused(gradients):
+    norm = torch.zeros(())
+    grads, outs = [torch.zeros(9).half(), torch.zeros(4).half()], [torch.zeros(9), torch.zeros(4)]
+    gset = m8.GradientSet(grads, out=outs)
+    gradients.clear()
+    for bad, good in ((torch.zeros(4).bfloat16(), outs[1].data), (torch.zeros(5), outs[1].data),
+                      (outs[0].data[:4], outs[1].data)):
+        outs[1].data = bad
+        for _ in range(2):  # not only the first time
+            with pytest.raises(ValueError):
+                m8.llmint8_grad_norm(gset, norm=norm)
+            with pytest.raises(ValueError):
+                m8.llmint8_grad_clip(gset, norm, 1.0)
+            with pytest.raises(ValueError):
+                gset.workspace_bytes()
+        assert not gradients
+        outs[1].data = good
+        assert handed(gradients, gset, norm) == entries(grads, outs)
+        gradients.clear()
+    gset.out.pop()
+    with pytest.raises(ValueError):
+        m8.llmint8_grad_clip(gset, norm, 1.0)
+
+
+def test_the_list_that_is_returned_is_the_caller_s(gradients):
+    norm = torch.zeros(())
+    grads = [torch.zeros(9), torch.zeros(4)]
+    gset = m8.GradientSet(grads)
+    m8.llmint8_grad_clip(gset, norm, 1.0).append(torch.zeros(6))
+    assert handed(gradients, gset, norm) == entries(grads, grads)
+    gset.grads.append(torch.zeros(6))  # the set's own: as many entries as tensors
+    assert handed(gradients, gset, norm) == entries(gset.grads, gset.grads)

@@ -365,6 +365,8 @@ def llmint8_layer_norm(x, weight=None, bias=None, eps=1e-5, y=None, stats=True, 
         stats = None
     else:
         m8._need(stats, torch.float32, (n, 2), "stats")
+        if stats.device != dev:
+            raise ValueError(f"stats: expected on {dev}, got {stats.device}")
     with _on(dev):
         m8._check(lib.llmint8_layer_norm(*xr, code, n, K, w, b, _dtype(w_dtype, "weight"), float(eps), *yr,
                                          None if stats is None else stats.data_ptr(), _handle(stream, dev)),

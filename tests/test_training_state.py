@@ -218,3 +218,18 @@ def test_the_list_that_is_returned_is_the_caller_s(gradients):
     assert handed(gradients, gset, norm) == entries(grads, grads)
     gset.grads.append(torch.zeros(6))  # the set's own: as many entries as tensors
     assert handed(gradients, gset, norm) == entries(gset.grads, gset.grads)
+
+
+def test_statistics_on_another_device_are_refused(monkeypatch):
+    training._library()
+    called = []
+    monkeypatch.setattr(m8, "load_library", lambda: type("L", (), {"llmint8_layer_norm": lambda s, *a: called.append(a) or 0})())
+    monkeypatch.setattr(m8, "_need", lambda *a: None)
+    monkeypatch.setattr(torch.Tensor, "is_cuda", True)
+    monkeypatch.setattr(training, "_handle", lambda stream, device: 0)
+    x = torch.zeros((6, 24)).half()
+    m8.llmint8_layer_norm(x, stats=torch.zeros((6, 2)))
+    assert len(called) == 1
+    with pytest.raises(ValueError, match="stats"):
+        m8.llmint8_layer_norm(x, stats=torch.zeros((6, 2), device="meta"))
+    assert len(called) == 1

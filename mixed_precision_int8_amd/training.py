@@ -290,8 +290,8 @@ def llmint8_rope(table, pos, axis, q, k=None, interleaved=False, inverse=False, 
     _plain((q, k), "q and k", "rotary")
     dev, dt = q.device, q.dtype
     code = _half(dt)
-    if q.dim() != 3 or (k is not None and k.dim() != 3):
-        raise ValueError("q and k: expected [rows, heads, dim]")
+    if q.dim() != 3 or not q.is_cuda or (k is not None and k.dim() != 3):
+        raise ValueError(f"q and k: expected CUDA [rows, heads, dim], got {tuple(q.shape)} on {q.device}")
     n, heads, dim = q.shape
     if (table.dim() != 2 or table.dtype != torch.float32 or not table.is_contiguous() or table.device != dev):
         raise ValueError(f"table: expected contiguous fp32 [positions, rot] on {dev}, got {table.dtype} "

@@ -233,3 +233,15 @@ def test_statistics_on_another_device_are_refused(monkeypatch):
     with pytest.raises(ValueError, match="stats"):
         m8.llmint8_layer_norm(x, stats=torch.zeros((6, 2), device="meta"))
     assert len(called) == 1
+
+
+def test_rotations_of_host_memory_are_refused(monkeypatch):
+    """Also on a stream of the caller's, where nothing else asks for the device."""
+    training._library()
+    called = []
+    monkeypatch.setattr(m8, "load_library", lambda: type("L", (), {"llmint8_rope": lambda s, *a: called.append(a) or 0})())
+    stream = type("Stream", (), {"cuda_stream": 5})()
+    q, out = torch.zeros((6, 4, 16)).half(), torch.zeros((6, 4, 16)).half()
+    with pytest.raises(ValueError, match="CUDA"):
+        m8.llmint8_rope(torch.zeros((9, 16)), torch.zeros(6, dtype=torch.int32), bytes(8), q, q_out=out, stream=stream)
+    assert not called

@@ -187,7 +187,7 @@ __global__ __launch_bounds__(256, DP <= 64 ? 4 : DP <= 128 ? 2 : 1) void ka_atte
   if (row0 + wave * 32 + n >= rows) return;
   place(n, &pos, &qh);
   const int64_t qrow = (int64_t)sq.row0 + pos;
-  const float inv = l_run == 0.0f ? 0.0f : 1.0f / l_run;
+  const float inv = 1.0f / l_run;  // l_run is zero where all of a row's logits are -infinity: o is NaN, lse -infinity
   uint16_t* op = a.o.p + qrow * a.o.token + (int64_t)qh * a.o.head;
 #pragma unroll
   for (int d = 0; d < ND; ++d)
@@ -200,7 +200,7 @@ __global__ __launch_bounds__(256, DP <= 64 ? 4 : DP <= 128 ? 2 : 1) void ka_atte
                      Act16<BF16>::pack2(acc[d][4 * k + 2] * inv, acc[d][4 * k + 3] * inv));
     }
   if (a.lse && hf == 0)
-    a.lse[qrow * a.q_heads + qh] = l_run == 0.0f ? kAttnNegInf : (m_run - 8.0f + log2f(l_run)) * 0.693147180559945309f;
+    a.lse[qrow * a.q_heads + qh] = (m_run - 8.0f + log2f(l_run)) * 0.693147180559945309f;
 }
 
 template <int DP, bool BF16>

@@ -200,7 +200,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_dq(AttnArgs a) {
   const bool mine = row0 + wave * 32 + nn < rows;
   if (mine && hf == 0) {
     float* st = a.stat + (int64_t)qh * a.T + qrow;
-    st[0] = (BF16 ? 0.0f : 15.0f) - lse2;
+    st[0] = (BF16 ? 0.0f : 15.0f) - lse2 + (lse2 - lse2);  // NaN where lse is -infinity: all of the row's logits are
     st[(int64_t)a.q_heads * a.T] = delta;
   }
 

@@ -159,3 +159,33 @@ def test_a_set_follows_gradients_that_move():
             assert torch.equal(p.grad, (t.float() * f).to(t.dtype)), change
         if change is not None:
             assert all(torch.equal(a, b) for a, b in zip(before, kept)), change
+
+
+def step(b, q, k, v, do, how):
+    out, lse = m8.llmint8_attention(b, q, k, v, **how)
+    return (out, lse, *m8.llmint8_attention_backward(b, q, k, v, out, lse, do, **how))
+
+
+HOW = [{}, {"causal": False}, {"window": 40, "sinks": 3}, {"window": 200}]
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("dim", [64, 80, 128, 256])
+@pytest.mark.parametrize("how", HOW)
+def test_rows_whose_logits_are_all_minus_infinity(dtype, dim, how):
+    """The softmax of such a row is not a number, nor are its output and what it gives to gradients; the others'
+    are what they are without it."""
+    print(f"[case] no logit {dtype} {dim} {how}", flush=True)
+    lens, hq, hk = [70, 1, 330, 2], 4, 2
+    T = sum(lens)
+    q, k, v, do = (randn(i, T, h, dim, dtype=dtype) for i, h in enumerate((hq, hk, hk, hq)))
+    b = m8.PackedRows.of(lens)
+    want = step(b, q, k, v, do, how)
+    q[70], k[70, 0, 3] = q[70].abs() + 0.5, float("-inf")              # a sequence of one token
+    q[401:, :2], k[401:, 0, 7] = q[401:, :2].abs() + 0.5, float("-inf")  # both tokens of one
+    out, lse, dq, dk, dv = step(b, q, k, v, do, how)
+    rows = [70, 401, 402]
+    for x, y, heads in ((out, want[0], 2), (dq, want[2], 2), (dk, want[3], 1), (dv, want[4], 1)):
+        assert torch.isnan(x[rows, :heads]).all()
+        assert torch.equal(x[:70], y[:70]) and torch.equal(x[71:401], y[71:401])
+    assert (lse[rows, :2] == float("-inf")).all() and torch.equal(lse[71:401], want[1][71:401])

@@ -75,10 +75,11 @@ struct AttnRowsOf {
     from = a.causal ? col : 0;
     count = (uint32_t)max((a.window > 0 && col >= a.sinks ? (int)min((int64_t)n, (int64_t)col + a.window) : n) - from, 0);
     all_from = a.causal ? j_hi : 0;
-    all_until = a.window > 0 && j_hi >= a.sinks ? max(j0, (int)min((int64_t)a.sinks, (int64_t)j_hi)) + a.window : INT32_MAX;
+    all_until = a.window > 0 && j_hi >= a.sinks ? min(n, max(j0, (int)min((int64_t)a.sinks, (int64_t)j_hi)) + a.window) : n;
   }
   __device__ __forceinline__ bool operator()(int row) const { return (uint32_t)(row - from) < count; }
-  // a tile that some of the tokens do not see whole
+  // a tile that some of the tokens do not see whole, or that the sequence ends in: the zeros behind it are
+  // rows that give nothing only times what is finite
   __device__ __forceinline__ bool masked(int base) const { return (base < all_from) | (base + 64 > all_until); }
 };
 

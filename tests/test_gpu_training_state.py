@@ -189,3 +189,50 @@ def test_rows_whose_logits_are_all_minus_infinity(dtype, dim, how):
         assert torch.isnan(x[rows, :heads]).all()
         assert torch.equal(x[:70], y[:70]) and torch.equal(x[71:401], y[71:401])
     assert (lse[rows, :2] == float("-inf")).all() and torch.equal(lse[71:401], want[1][71:401])
+
+
+def minus_infinity(dtype, dim, how, lens):
+    """A step where a key's logits are all -infinity, the same with logits far below all others, the rows that see the
+    key, and a call of the step with another value in the infinity's place."""
+    hq, hk, T = 4, 2, sum(lens)
+    first, n = (0, lens[0]) if len(lens) == 1 else (lens[0], lens[1])
+    at = first + 70
+    q, k, v, do = (randn(i, T, h, dim, dtype=dtype) for i, h in enumerate((hq, hk, hk, hq)))
+    q[:, :, CHANNEL] = q[:, :, CHANNEL].abs() + 2.0
+    b = m8.PackedRows.of(lens)
+    k[at, 0] = 0
+    k[at, 0, CHANNEL] = -60000.0  # times 2 / 16 at least, scaled: under -3000
+    want = step(b, q, k, v, do, how)
+    k[at, 0] = randn(9, dim, dtype=dtype)
+
+    def run(value):
+        k[at, 0, CHANNEL] = value
+        got = step(b, q, k, v, do, how)
+        torch.cuda.synchronize()
+        return got
+
+    see = ref.visible(n, how.get("causal", True), how.get("window", 0), how.get("sinks", 0))
+    rows = torch.tensor([first + int(i) for i in np.flatnonzero(see[:, at - first])], device="cuda")
+    assert len(rows) > 30
+    return run(float("-inf")), want, rows, run
+
+
+CHANNEL = 5
+KEYS = [pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16]), pytest.mark.parametrize("dim", [64, 80, 128, 256]),
+        pytest.mark.parametrize("how", HOW), pytest.mark.parametrize("lens", [[100, 150, 30], [700]])]
+
+
+def keys(test):
+    for mark in KEYS:
+        test = mark(test)
+    return test
+
+
+@keys
+def test_a_key_of_minus_infinity_has_no_weight(dtype, dim, how, lens):
+    """A token whose logits are -infinity has the weight 0, as one whose logits are far below all others: the same bits."""
+    print(f"[case] -inf key {dtype} {dim} {how} {lens}", flush=True)
+    got, want, _, _ = minus_infinity(dtype, dim, how, lens)
+    for name, x, y in zip(("out", "lse", "dq", "dk", "dv"), got, want):
+        if name != "dq":
+            assert torch.equal(x, y), name

@@ -557,7 +557,9 @@ LLMINT8_API llmint8_status llmint8_kv_attention(const llmint8_kv_cache* cache, c
  * weights under 2^-29 of one and dS under 2^-30 of the largest of its row (dq) or
  * token (dk). Results do not depend on what else runs: the same call gives the same
  * bits. A NaN or infinity reaches the rows that see its token (its gradients: the
- * tokens that its row sees) and no others.
+ * tokens that its row sees) and no others; an infinity as that or as NaN. A logit of
+ * -infinity is a weight of 0, as the formulas have it: of an infinite key it reaches the
+ * one channel of dq alone. A row that has no other logits is NaN (lse -infinity).
  *   q, out, dout, dq  [rows, q_heads, dim]; k, v, dk, dv [rows, heads, dim]: 16 bits,
  *              dense channels, token and head strides in elements (multiples of 8, token
  *              strides up to 2^23), 16-byte aligned; may be slices of larger tensors.

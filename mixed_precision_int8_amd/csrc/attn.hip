@@ -177,7 +177,7 @@ __global__ __launch_bounds__(256, DP <= 64 ? 4 : DP <= 128 ? 2 : 1) void ka_atte
     for (int i = 0; i < tiles; ++i) {
       const int base = base_of(i);
       if (all.masked(base))
-        attn_others<DP, BF16>(acc, vp, a.v.token, base, sq.n, D, [&](int t) { return sees(base + t); });
+        attn_others<DP, BF16>(acc, vp, a.v.token, base, sq.n, D, true, [&](int t) { return sees(base + t); });
     }
   }
 

@@ -217,11 +217,13 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_dq(AttnArgs a) {
       attn_wait_copies();
       if (masked) ck.template finite<BF16>(smem + stage * kStage, flag);
       attn_barrier();
+      const int cleared = masked ? uniform(*flag) : 0;
       copy(i + 1, stage ^ 1);
 #pragma unroll
       for (int sb = 0; sb < 2; ++sb) {
         if (idle | own.none(base + 32 * sb, 32)) continue;
         v16f_t s = attn_rows_product<DP, BF16>(rd, 0, sb, q);
+        if (__builtin_expect(cleared, 0)) attn_hide<BF16>(s, kp, a.k.token, base + 32 * sb, sq.n, D);
         v16f_t t = attn_rows_product<DP, BF16>(rd, 1, sb, g);
         // 256 channels leave no registers for operands read this early (172 of them went to memory in
         // fp16: 1209 us for the gradients of 7000 tokens of 16/4 heads, 751 without)
@@ -273,7 +275,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_dq(AttnArgs a) {
     for (int i = 0; i < tiles; ++i) {
       const int base = base_of(i);
       if (all.masked(base))
-        attn_others<DP, BF16>(acc, kp, a.k.token, base, sq.n, D, [&](int t) { return sees(base + t); });
+        attn_others<DP, BF16>(acc, kp, a.k.token, base, sq.n, D, false, [&](int t) { return sees(base + t); });
     }
   }
 
@@ -431,8 +433,8 @@ __global__ __launch_bounds__(256, 2) void ka_dkv_alone(AttnArgs a) {
       const int base = (lo + i % per) << 6;
       if (!see.masked(base)) continue;
       auto sees = [&](int t) { return see(base + t); };
-      attn_others<DP, BF16>(dv, gp + (int64_t)(i / per) * a.d_o.head, a.d_o.token, base, sq.n, D, sees);
-      attn_others<DP, BF16>(dk, qp + (int64_t)(i / per) * a.q.head, a.q.token, base, sq.n, D, sees);
+      attn_others<DP, BF16>(dv, gp + (int64_t)(i / per) * a.d_o.head, a.d_o.token, base, sq.n, D, true, sees);
+      attn_others<DP, BF16>(dk, qp + (int64_t)(i / per) * a.q.head, a.q.token, base, sq.n, D, false, sees);
     }
   }
 
@@ -703,7 +705,7 @@ __global__ __launch_bounds__(DP <= 128 ? 512 : 256, DP <= 128 ? 2 : 1) void ka_d
     for (int i = 0; i < tiles; ++i) {
       const int at = (lo + i % per) << 6;
       auto sees = [&](int t) { return see(at + t); };
-      if (see.masked(at)) attn_others<DP, BF16>(acc, (second ? qp : gp) + (int64_t)(i / per) * r.head, r.token, at, sq.n, D, sees);
+      if (see.masked(at)) attn_others<DP, BF16>(acc, (second ? qp : gp) + (int64_t)(i / per) * r.head, r.token, at, sq.n, D, !second, sees);
     }
   }
 

@@ -313,10 +313,11 @@ __device__ __forceinline__ float attn_max(float a, float b, float c) {
 }
 
 // Rows [first, first + 64) of the n at p; `see(row)`: whether this lane's column sees that
-// row of the 64.
+// row of the 64. `weight`: the products' weights are of one sign, and an infinity is added as it
+// is (its weight is taken not to vanish); others may have either sign, or be 0 or NaN: NaN.
 template <int DP, bool BF16, class See>
 __device__ __forceinline__ void attn_others(v16f_t (&acc)[DP / 32], const uint16_t* p, int64_t token, int first, int n,
-                                            int dim, See&& see) {
+                                            int dim, bool weight, See&& see) {
   constexpr uint32_t kInf = BF16 ? 0x7f80u : 0x7c00u;
   const int lane = threadIdx.x & 63, hf = lane >> 5, rows = min(n - first, 64);
 #pragma unroll 1
@@ -329,7 +330,8 @@ __device__ __forceinline__ void attn_others(v16f_t (&acc)[DP / 32], const uint16
       while (left) {
         const int from = __builtin_ctzll(left);
         left &= left - 1;
-        const float x = Act16<BF16>::to_f32((uint32_t)__builtin_amdgcn_readlane((int)v, from));
+        const float value = Act16<BF16>::to_f32((uint32_t)__builtin_amdgcn_readlane((int)v, from));
+        const float x = weight ? value : value - value;
         const int c = c0 + from;
 #pragma unroll
         for (int d = 0; d < DP / 32; ++d)
@@ -339,6 +341,28 @@ __device__ __forceinline__ void attn_others(v16f_t (&acc)[DP / 32], const uint16
       }
     }
   }
+}
+
+// Logits of 32 of the n rows at p, from `first` on, formed from a tile that `finite` has cleared:
+// a row that holds an infinity or NaN gets -infinity, weight 0. Its logit was that or, of a column whose
+// lse is NaN, anything; a cleared tile has some other number for it.
+template <bool BF16>
+__device__ __forceinline__ void attn_hide(v16f_t& s, const uint16_t* p, int64_t token, int first, int n, int dim) {
+  constexpr uint32_t kInf = BF16 ? 0x7f80u : 0x7c00u;
+  const int hf = (threadIdx.x & 63) >> 5;
+  uint32_t odd = 0;
+#pragma unroll 1
+  for (int x = 0; x < 16; ++x) {
+    const int row = first + 16 * (x >> 3) + 8 * hf + (x & 7);
+#pragma unroll 1
+    for (int c = 0; row < n && c < dim; c += 2) {
+      const uint32_t v = *reinterpret_cast<const uint32_t*>(p + (int64_t)row * token + c);
+      if ((v & kInf) == kInf || (v >> 16 & kInf) == kInf) odd |= 1u << x;
+    }
+  }
+#pragma unroll
+  for (int x = 0; x < 16; ++x)
+    if (odd >> x & 1) s[x] = kAttnNegInf;
 }
 
 // s += the tile's rows [32 block, +32) times b, operands read two steps ahead

@@ -236,3 +236,22 @@ def test_a_key_of_minus_infinity_has_no_weight(dtype, dim, how, lens):
     for name, x, y in zip(("out", "lse", "dq", "dk", "dv"), got, want):
         if name != "dq":
             assert torch.equal(x, y), name
+
+
+@keys
+def test_what_a_key_of_minus_infinity_gives_to_dq(dtype, dim, how, lens):
+    """The same bits too, but in the channel of the infinity, which is 0 times it; whether a mask crosses the token's tile
+    makes no difference. Of rows whose logit is infinite or NaN all is NaN, and of no others."""
+    print(f"[case] -inf key, dq {dtype} {dim} {how} {lens}", flush=True)
+    got, want, rows, run = minus_infinity(dtype, dim, how, lens)
+    x, y = got[2].clone(), want[2].clone()
+    assert torch.isnan(x[rows, :2, CHANNEL]).all()
+    x[rows, :2, CHANNEL] = y[rows, :2, CHANNEL] = 0
+    assert torch.equal(x, y)
+    same = torch.ones(len(x), dtype=torch.bool, device="cuda")
+    same[rows] = False
+    for value in (float("inf"), float("nan")):
+        got = run(value)
+        for x, y in zip(got[:3], want[:3]):
+            assert torch.isnan(x[rows, :2]).all()
+            assert torch.equal(x[same], y[same]) and torch.equal(x[:, 2:], y[:, 2:])

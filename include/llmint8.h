@@ -566,6 +566,9 @@ LLMINT8_API llmint8_status llmint8_kv_attention(const llmint8_kv_cache* cache, c
  *              Outputs overlap neither inputs nor each other.
  *   lse        fp32 [rows, q_heads], dense, or NULL in the forward call
  *   dim        a multiple of 8 up to 256; q_heads a multiple of heads
+ *   rows * q_heads up to 2^30; (rows * q_heads / heads / 128 + seqs) * heads below 2^24, and for the
+ *              gradients (rows / 128 + seqs) * heads below 2^24, of 104 to 128 channels below 2^23 (from 136
+ *              on (rows / 64 + seqs) * heads below 2^24): UNSUPPORTED beyond
  *   scale      finite
  *   workspace  llmint8_attention_backward_workspace_bytes(...) bytes, 256-byte aligned,
  *              contents on entry do not matter

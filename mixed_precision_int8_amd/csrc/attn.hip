@@ -205,10 +205,9 @@ __global__ __launch_bounds__(256, DP <= 64 ? 4 : DP <= 128 ? 2 : 1) void ka_atte
 
 template <int DP, bool BF16>
 static hipError_t launch_fwd(const AttnArgs& a, hipStream_t stream) {
-  const int64_t items = ((int64_t)a.T * (a.q_heads / a.heads) >> 7) + a.B;
-  const int64_t blocks = items * a.heads;
-  if (blocks > INT32_MAX) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((ka_attention<DP, BF16>), dim3((unsigned)blocks), dim3(256), 0, stream, a);
+  const AttnGrid g = attn_row_grid(a.T, a.q_heads, a.heads, a.B);
+  if (!g.fits()) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL((ka_attention<DP, BF16>), dim3((unsigned)g.blocks), dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 

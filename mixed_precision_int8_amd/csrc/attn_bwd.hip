@@ -718,15 +718,13 @@ __global__ __launch_bounds__(DP <= 128 ? 512 : 256, DP <= 128 ? 2 : 1) void ka_d
 template <int DP, bool BF16>
 static hipError_t launch_bwd(const AttnArgs& a, hipStream_t stream) {
   constexpr bool kAlone = DP <= 96;
-  constexpr int kShift = DP <= 128 ? 7 : 6;
-  const int64_t rows = (((int64_t)a.T * (a.q_heads / a.heads) >> 7) + a.B) * a.heads;
-  const int64_t cols = (((int64_t)a.T >> kShift) + a.B) * a.heads;
-  if (rows > INT32_MAX || cols > INT32_MAX) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((ka_dq<DP, BF16>), dim3((unsigned)rows), dim3(256), 0, stream, a);
+  const AttnGrid rows = attn_row_grid(a.T, a.q_heads, a.heads, a.B), cols = attn_col_grid(a.T, a.heads, a.B, a.dim);
+  if (!rows.fits() || !cols.fits()) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL((ka_dq<DP, BF16>), dim3((unsigned)rows.blocks), dim3(256), 0, stream, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if constexpr (kAlone) hipLaunchKernelGGL((ka_dkv_alone<DP, BF16>), dim3((unsigned)cols), dim3(256), 0, stream, a);
-  else hipLaunchKernelGGL((ka_dkv<DP, BF16>), dim3((unsigned)cols), dim3(DP <= 128 ? 512 : 256), 0, stream, a);
+  if constexpr (kAlone) hipLaunchKernelGGL((ka_dkv_alone<DP, BF16>), dim3((unsigned)cols.blocks), dim3(256), 0, stream, a);
+  else hipLaunchKernelGGL((ka_dkv<DP, BF16>), dim3((unsigned)cols.blocks), dim3(cols.threads), 0, stream, a);
   return hipGetLastError();
 }
 

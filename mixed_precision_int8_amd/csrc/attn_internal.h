@@ -10,15 +10,28 @@ namespace llmint8 {
 // Rows and (row, head) pairs are counted in 32 bits; a tile of 64 rows has to lie
 // within a buffer window of 2^31 bytes, so strides are limited as well.
 constexpr int64_t kAttnMaxStride = int64_t(1) << 23;
+constexpr int64_t kMaxWorkItems = int64_t(1) << 32;  // of a launch, and fewer
 inline int admit_attention(int64_t seqs, int64_t rows, int64_t q_heads, int64_t heads, int64_t dim) {
   if (seqs < 0 || rows < 0 || q_heads <= 0 || heads <= 0 || dim <= 0) return LLMINT8_ERR_INVALID_ARG;
   if (q_heads % heads != 0) return LLMINT8_ERR_INVALID_ARG;
   if (dim % 8 != 0 || dim > 256 || heads > 4096 || q_heads > 65536) return LLMINT8_ERR_UNSUPPORTED;
   if (rows > kKvMax || seqs > (int64_t(1) << 24)) return LLMINT8_ERR_UNSUPPORTED;
-  // workgroups of a launch: ((rows * group) / 128 + seqs) * heads, or rows / 64 for rows * group / 128
-  if (rows * q_heads > kKvMaxQRows || (rows * q_heads / 64 + (seqs + 1) * heads) >= kTwo31)
-    return LLMINT8_ERR_UNSUPPORTED;
+  if (rows * q_heads > kKvMaxQRows) return LLMINT8_ERR_UNSUPPORTED;
   return LLMINT8_OK;
+}
+
+// The launches of a call: workgroups that take 128 rows of a sequence and key/value head (forward, dq), or
+// 128 or 64 of its tokens (dk and dv). A launch has fewer than 2^32 work items.
+struct AttnGrid {
+  int64_t blocks;
+  int threads;
+  bool fits() const { return blocks * threads < kMaxWorkItems; }
+};
+inline AttnGrid attn_row_grid(int64_t rows, int64_t q_heads, int64_t heads, int64_t seqs) {
+  return {((rows * (q_heads / heads) >> 7) + seqs) * heads, 256};
+}
+inline AttnGrid attn_col_grid(int64_t rows, int64_t heads, int64_t seqs, int64_t dim) {
+  return {((rows >> (dim <= 128 ? 7 : 6)) + seqs) * heads, dim > 96 && dim <= 128 ? 512 : 256};
 }
 
 struct AttnArgs {

@@ -63,6 +63,7 @@ llmint8_status llmint8_attention(const llmint8_attention_shape* shape, int dtype
   if (st != LLMINT8_OK) return st;
   if (lse && !aligned(lse, 4)) return LLMINT8_ERR_INVALID_ARG;
   if (a.B == 0 || a.T == 0) return LLMINT8_OK;
+  if (!attn_row_grid(a.T, a.q_heads, a.heads, a.B).fits()) return LLMINT8_ERR_UNSUPPORTED;
   if ((st = attn_rows(q, a, a.q_heads, &a.q)) != LLMINT8_OK || (st = attn_rows(k, a, a.heads, &a.k)) != LLMINT8_OK ||
       (st = attn_rows(v, a, a.heads, &a.v)) != LLMINT8_OK || (st = attn_rows(out, a, a.q_heads, &a.o)) != LLMINT8_OK)
     return st;
@@ -88,6 +89,8 @@ llmint8_status llmint8_attention_backward(const llmint8_attention_shape* shape, 
   llmint8_status st = attn_args(shape, dtype, &a);
   if (st != LLMINT8_OK) return st;
   if (a.B == 0 || a.T == 0) return LLMINT8_OK;
+  if (!attn_row_grid(a.T, a.q_heads, a.heads, a.B).fits() || !attn_col_grid(a.T, a.heads, a.B, a.dim).fits())
+    return LLMINT8_ERR_UNSUPPORTED;
   const struct {
     const llmint8_rows* in;
     int heads;

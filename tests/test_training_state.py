@@ -245,3 +245,26 @@ def test_rotations_of_host_memory_are_refused(monkeypatch):
     with pytest.raises(ValueError, match="CUDA"):
         m8.llmint8_rope(torch.zeros((9, 16)), torch.zeros(6, dtype=torch.int32), bytes(8), q, q_out=out, stream=stream)
     assert not called
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import os
+    if not os.path.exists(m8.library_path()):
+        pytest.skip("libllmint8.so not built")
+    return m8.load_library()
+
+
+@pytest.mark.parametrize("seqs,rows,q_heads,heads,dim,forward", [
+    (1 << 24, 1 << 24, 1, 1, 64, True), (1 << 21, 100, 8, 8, 64, True), ((1 << 24) - 8, 1 << 10, 1, 1, 64, True),
+    (1 << 20, 1 << 26, 16, 16, 64, True),                # 2^20 + 2^19 for each of 16 heads
+    (1 << 20, 100, 8, 8, 128, False), ((1 << 23) - 8, 1 << 10, 1, 1, 104, False), (1, 1 << 30, 1, 1, 128, True),
+    (1 << 23, 1 << 29, 1, 1, 136, False),                # 2^23 tiles of 64 tokens
+])
+def test_more_work_items_than_a_launch_has_are_refused(lib, seqs, rows, q_heads, heads, dim, forward):
+    P = 0x7f0000000000  # never read: every call is refused
+    shape = training._SHAPE(P, seqs, rows, q_heads, heads, dim, 0.1, 1, 0, 0)
+    other = [training._ROWS(P + 0x1000000 * i, q_heads * heads * 256, 256) for i in range(8)]
+    if forward:
+        assert lib.llmint8_attention(shape, m8.LLMINT8_DTYPE_F16, *other[:4], P, None) == -2
+    assert lib.llmint8_attention_backward(shape, m8.LLMINT8_DTYPE_F16, *other[:4], P, *other[4:], P, 1 << 50, None) == -2

@@ -304,10 +304,11 @@ int norm_groups(int64_t rows, int64_t K, int num_cus) {
 template <int TYPE, int WTYPE, int L, int NV>
 static hipError_t forward(const NormArgs& a, hipStream_t stream) {
   constexpr int TH = L > 256 ? L : 256, R = TH / L;
-  const int64_t n = (a.rows + R - 1) / R;
-  if (n > INT32_MAX) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((kn_forward<TYPE, WTYPE, L, NV>), dim3((unsigned)n), dim3(TH), 0, stream, a);
-  return hipGetLastError();
+  return launch_rows(a.rows, L, TH, [&](int64_t at, int64_t n) {
+    hipLaunchKernelGGL((kn_forward<TYPE, WTYPE, L, NV>), dim3((unsigned)((n + R - 1) / R)), dim3(TH), 0, stream,
+                       norm_rows_of(a, at, n, Elem<TYPE>::kBytes));
+    return hipGetLastError();
+  });
 }
 
 template <int TYPE, int WTYPE, int L, int NV>
@@ -356,9 +357,10 @@ hipError_t launch_norm_backward(const NormArgs& a, int type, int w_type, hipStre
     const bool sums = a.dw || a.db;
     hipError_t e;
     if (a.K > 8192) {
-      if (a.rows > INT32_MAX) return hipErrorInvalidConfiguration;
-      hipLaunchKernelGGL((kn_wide<T, WT>), dim3((unsigned)a.rows), dim3(1024), 0, stream, a);
-      e = hipGetLastError();
+      e = launch_rows(a.rows, 1024, 1024, [&](int64_t at, int64_t n) {
+        hipLaunchKernelGGL((kn_wide<T, WT>), dim3((unsigned)n), dim3(1024), 0, stream, norm_rows_of(a, at, n, Elem<T>::kBytes));
+        return hipGetLastError();
+      });
       if (e != hipSuccess) return e;
       if (sums) hipLaunchKernelGGL((kn_columns<T>), dim3((a.K + 2047) / 2048, a.groups), dim3(256), 0, stream, a);
       e = hipGetLastError();

@@ -86,11 +86,13 @@ static hipError_t launch(const RopeArgs& a, int num_cus, hipStream_t stream) {
   // eight heads to a thread where that leaves four workgroups to a CU (16000 tokens forward and
   // back: 154 us, one head 273), else one (a single token: 3.4 us, eight heads 6.0)
   const bool many = blocks(8) >= 4 * num_cus;
-  const int64_t n = blocks(many ? 8 : 1);
-  if (n > INT32_MAX) return hipErrorInvalidConfiguration;
-  if (many) hipLaunchKernelGGL((kr_rope<BF16, INTERLEAVED, 8>), dim3((unsigned)n), dim3(256), 0, stream, a);
-  else hipLaunchKernelGGL((kr_rope<BF16, INTERLEAVED, 1>), dim3((unsigned)n), dim3(256), 0, stream, a);
-  return hipGetLastError();
+  const int64_t items = chunks * (many ? (heads + 7) / 8 : heads);
+  return launch_rows(a.rows, items, 256, [&](int64_t at, int64_t n) {
+    const dim3 grid((unsigned)((n * items + 255) / 256));
+    if (many) hipLaunchKernelGGL((kr_rope<BF16, INTERLEAVED, 8>), grid, dim3(256), 0, stream, rope_rows_of(a, at, n));
+    else hipLaunchKernelGGL((kr_rope<BF16, INTERLEAVED, 1>), grid, dim3(256), 0, stream, rope_rows_of(a, at, n));
+    return hipGetLastError();
+  });
 }
 
 hipError_t launch_rope(const RopeArgs& a, bool bf16, int num_cus, hipStream_t stream) {

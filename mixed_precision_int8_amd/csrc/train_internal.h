@@ -9,6 +9,18 @@ namespace llmint8 {
 // Element types of these operators, as the ABI numbers them.
 enum : int { kF16 = 0, kF32 = 1, kBF16 = 2 };
 
+// Rows in as few launches as there are work items for (fewer than 2^32 to a launch): launch(first row,
+// rows) with `items` to a row, in workgroups of `threads`.
+template <class Launch>
+hipError_t launch_rows(int64_t rows, int64_t items, int threads, Launch&& launch, int64_t max_items = kMaxWorkItems) {
+  const int64_t most = (max_items - threads) / items;
+  for (int64_t at = 0; at < rows; at += most) {
+    const hipError_t e = launch(at, rows - at < most ? rows - at : most);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 constexpr int64_t kNormMaxWidth = 65536;
 struct NormArgs {
   const void* x;
@@ -27,6 +39,16 @@ struct NormArgs {
   float* parts;  // [groups][2][K]
   int groups;
 };
+// n rows from row `at` on, of elements of `bytes`
+inline NormArgs norm_rows_of(NormArgs a, int64_t at, int64_t n, int bytes) {
+  auto on = [&](auto* p, int64_t by) { return p ? p + by : p; };
+  a.x = static_cast<const char*>(a.x) + at * a.x_row * bytes;
+  a.y = static_cast<char*>(a.y) + at * a.y_row * bytes;
+  a.dy = on(static_cast<const char*>(a.dy), at * a.dy_row * bytes);
+  a.stats = on(a.stats, 2 * at);
+  a.rows = n;
+  return a;
+}
 // Workgroups of the backward pass, each of which leaves one row of partial sums.
 int norm_groups(int64_t rows, int64_t K, int num_cus);
 hipError_t launch_norm(const NormArgs& a, int type, int w_type, hipStream_t stream);
@@ -44,6 +66,16 @@ struct RopeArgs {
   float sign;                                         // of the angles
   uint8_t axis[kRopeMaxPairs];
 };
+inline RopeArgs rope_rows_of(RopeArgs a, int64_t at, int64_t n) {
+  for (int i = 0; i < 2; ++i) {
+    if (a.heads[i] == 0) continue;
+    a.x[i].p += at * a.x[i].token;
+    a.y[i].p += at * a.y[i].token;
+  }
+  a.pos += at * a.axes;
+  a.rows = n;
+  return a;
+}
 hipError_t launch_rope(const RopeArgs& a, bool bf16, int num_cus, hipStream_t stream);
 
 // Gradients: up to N tensors to a launch, as its arguments: 480 of them where there are more

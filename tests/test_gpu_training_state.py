@@ -255,3 +255,15 @@ def test_what_a_key_of_minus_infinity_gives_to_dq(dtype, dim, how, lens):
         for x, y in zip(got[:3], want[:3]):
             assert torch.isnan(x[rows, :2]).all()
             assert torch.equal(x[same], y[same]) and torch.equal(x[:, 2:], y[:, 2:])
+
+
+def test_layer_norm_of_more_rows_than_a_launch_has_work_items_for():
+    """64 work items to a row: 2^26 rows and a few more."""
+    print("[case] many rows", flush=True)
+    n = (1 << 26) + 5
+    x = (torch.arange(n, device="cuda") % 2039).to(torch.float16).view(n, 1)
+    bias = torch.full((1,), 3.0, dtype=torch.float16, device="cuda")
+    y, stats = m8.llmint8_layer_norm(x, None, bias)
+    assert (y == 3.0).all() and torch.equal(stats[:, :1], x.float())
+    y, _ = m8.llmint8_layer_norm(x, None, bias, y=x, stats=False)  # in place
+    assert (x == 3.0).all()

@@ -268,3 +268,18 @@ def test_more_work_items_than_a_launch_has_are_refused(lib, seqs, rows, q_heads,
     if forward:
         assert lib.llmint8_attention(shape, m8.LLMINT8_DTYPE_F16, *other[:4], P, None) == -2
     assert lib.llmint8_attention_backward(shape, m8.LLMINT8_DTYPE_F16, *other[:4], P, *other[4:], P, 1 << 50, None) == -2
+
+
+def test_rows_are_dealt_to_launches(tmp_path):
+    import os
+    import shutil
+    import subprocess
+    cc = next((c for c in ("/opt/rocm/bin/hipcc", shutil.which("hipcc")) if c and os.path.exists(c)), None)
+    if cc is None:
+        pytest.skip("hipcc not found")
+    root, exe = os.path.dirname(os.path.dirname(os.path.abspath(__file__))), str(tmp_path / "rows")
+    r = subprocess.run([cc, "-O1", "-std=c++17", "-I", os.path.join(root, "include"),
+                        os.path.join(root, "tests", "train_rows_check.cpp"), "-o", exe], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-3000:]
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0 and "rows ok" in r.stdout, r.stdout

@@ -16,7 +16,7 @@ LIB = os.path.join(HERE, "libllmint8.so")
 
 SOURCES = ["prep.hip", "gemm.hip", "gemv.hip", "bwd.hip", "blockwise.hip", "fourbit.hip", "noalloc.hip",
            "kvcache.hip", "kvattn.hip", "kvprompt.hip", "attn.hip", "attn_bwd.hip", "rope.hip", "norm.hip", "grads.hip",
-           "api.cpp", "kv_api.cpp", "train_api.cpp"]
+           "api.cpp", "kv_api.cpp", "train_api.cpp", "py_tensors.cpp"]
 # the benchmark's matrix-core rate probe: a library of its own, not part of libllmint8
 PROBE_SRC = os.path.join(HERE, "bench_probe", "probe.hip")
 PROBE_LIB = os.path.join(HERE, "libllmint8_probe.so")

@@ -424,19 +424,22 @@ class GradientSet:
     the gradients of a model others): every call looks at them again. A program whose gradients are the same tensors
     in every step makes it once."""
 
-    __slots__ = ("grads", "out", "device", "_arr", "_need", "_seen")
+    __slots__ = ("_grads", "_out", "device", "_arr", "_need", "_both", "_seen")
 
     def __init__(self, grads, out=None):
         _library()
-        self.grads = [g for g in grads if g is not None]
-        self.out = self.grads if out is None else list(out)
+        self._grads = tuple(g for g in grads if g is not None)
+        self._out = self._grads if out is None else tuple(out)
         self._read()
+
+    grads = property(lambda self: self._grads, doc="The gradients, those that were None left out.")
+    out = property(lambda self: self._out, doc="The tensors that are written.")
 
     def _read(self):
         """The tensors' memory, as the library takes it, and what it was read from."""
         if len(self.out) != len(self.grads):
             raise ValueError(f"out: {len(self.out)} tensors for {len(self.grads)} gradients")
-        self._seen = None
+        self._seen, self._both = None, ((), None)
         self.device = self.grads[0].device if self.grads else None
         self._arr = (_Grad * max(1, len(self.grads)))()
         for a, g, o in zip(self._arr, self.grads, self.out):
@@ -465,18 +468,25 @@ class GradientSet:
                 if first < end[1] or (written and first < end[0]):
                     raise ValueError("gradients: two of them, or two outputs, share memory that is written")
                 end[1 if written else 0] = max(end[1 if written else 0], last)
-        self._seen = self._looks()
-
-    def _looks(self):
-        """Address, count and type of every tensor. One list after the other: 0.12 us a tensor, a loop over the tensors
-        takes half as much again."""
         both = self.grads if self.out is self.grads else self.grads + self.out
-        return (len(self.grads), list(map(torch.Tensor.data_ptr, both)), list(map(torch.Tensor.numel, both)),
-                [t.dtype for t in both])
+        self._both = both, None
+        if _describe() is not None:
+            held, seen = (ctypes.py_object * max(1, len(both)))(*both), ctypes.create_string_buffer(32 * max(1, len(both)))
+            if _tensors(held, len(both), seen, 1) == 0:
+                self._both, self._seen = (both, held), seen
+                return
+        self._seen = _looks(both)
 
     def _current(self):
         """The set, read again if a tensor is not as it was: an address of before may be another tensor's by now."""
-        if self._seen is None or self._looks() != self._seen:
+        both, held = self._both
+        if self._seen is None:
+            same = False
+        elif held is not None:
+            same = _tensors(held, len(both), self._seen, 0) == 1
+        else:
+            same = _looks(both) == self._seen
+        if not same:
             self._read()
         return self
 
@@ -491,6 +501,39 @@ class GradientSet:
         if self._need is None:
             self._need = int(_library().llmint8_grad_norm_workspace_bytes(self._arr, len(self)))
         return self._need
+
+
+def _looks(tensors):
+    """Address, count and type of every tensor. One list after the other: 0.12 us a tensor, a loop over the tensors takes
+    half as much again."""
+    return (list(map(torch.Tensor.data_ptr, tensors)), list(map(torch.Tensor.numel, tensors)), [t.dtype for t in tensors])
+
+
+_TABLE = False  # not asked for yet
+
+
+def _describe():
+    """(llmint8_py_tensors, the exchange table of torch's tensors), which looks at them in a tenth of the time; None
+    where this torch has no such table."""
+    global _TABLE
+    if _TABLE is False:
+        try:
+            get = ctypes.pythonapi.PyCapsule_GetPointer
+            get.argtypes, get.restype = [ctypes.py_object, ctypes.c_char_p], _vp
+            fn = ctypes.PyDLL(m8.library_path()).llmint8_py_tensors
+            fn.argtypes, fn.restype = [_vp, _vp, _i64, _vp, ctypes.c_int], ctypes.c_int
+            _TABLE = fn, get(torch.Tensor.__dlpack_c_exchange_api__, b"dlpack_exchange_api")
+        except (AttributeError, OSError, ValueError):
+            _TABLE = None
+    return _TABLE
+
+
+def _tensors(held, n, seen, write):
+    fn, table = _TABLE
+    try:
+        return fn(table, held, n, seen, write)
+    except Exception:  # a tensor that the table does not describe
+        return -1
 
 
 def _dense(t):

@@ -173,9 +173,10 @@ class PackedRows:
 
     def used_rows(self):
         """``used`` while it holds, else None."""
-        if self.used is None or not self._as_told() or torch.cuda.is_current_stream_capturing():
+        if self.used is None or not self._as_told():
             return None
-        return self.used
+        with _on(self.device):  # torch asks about the current device's stream
+            return None if torch.cuda.is_current_stream_capturing() else self.used
 
     def longest(self):
         """No sequence has more tokens, as far as the host knows."""

@@ -297,3 +297,24 @@ def test_a_set_of_tensors_of_every_kind(gradients):
         g.data = g.data.clone()
         assert handed(gradients, gset, norm) == entries(grads, grads)
     assert len(m8.GradientSet([])) == 0 and len(m8.GradientSet([])._current()) == 0
+
+
+def test_used_rows_of_a_call_captured_on_another_device(packed, monkeypatch):
+    """Asked of the device that the batch is on, whatever the current one is."""
+    import contextlib
+    filled, _ = packed
+    b = m8.PackedRows.of([3, 2], device="cpu")
+    b.device = torch.device("cuda", 1)
+    at = [0]
+
+    @contextlib.contextmanager
+    def on(device):
+        at.append(device.index)
+        yield
+        at.pop()
+
+    monkeypatch.setattr(training, "_on", on)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: at[-1] == 1)
+    assert b.used_rows() is None and at == [0]
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: at[-1] == 0)
+    assert b.used_rows() == 5

@@ -598,11 +598,12 @@ def _grad_clip(grads, norm, max_norm, scale, stream=None):
 
 
 def clip_grad_norm(parameters, max_norm, scale=1.0):
-    """Clips the gradients of ``parameters`` (tensors; those without one are left out) in place, so that their norm
+    """Clips the gradients of ``parameters`` (tensors, or one; those without one are left out) in place, so that their norm
     is at most ``max_norm``; ``scale`` (1 / loss scale) is applied first. Returns the norm before clipping, an fp32
     scalar on the device."""
     _library()
-    parameters = list(parameters)
+    # a tensor is its own only parameter: as a list it would be its rows, which have no gradient
+    parameters = [parameters] if isinstance(parameters, torch.Tensor) else list(parameters)
     grads = GradientSet([p.grad for p in parameters])
     if not len(grads):
         return torch.zeros((), dtype=torch.float32, device=parameters[0].device if parameters else "cuda")

@@ -318,3 +318,14 @@ def test_used_rows_of_a_call_captured_on_another_device(packed, monkeypatch):
     assert b.used_rows() is None and at == [0]
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: at[-1] == 0)
     assert b.used_rows() == 5
+
+
+def test_one_parameter_is_clipped(gradients):
+    p = torch.nn.Parameter(torch.zeros(4, 3))
+    p.grad = torch.ones(4, 3)
+    gradients.clear()
+    m8.clip_grad_norm(p, 1.0)
+    assert [c for c in gradients] == [(name, entries([p.grad], [p.grad])) for name in ("llmint8_grad_norm", "llmint8_grad_clip")]
+    gradients.clear()
+    m8.clip_grad_norm((x for x in [p, torch.nn.Parameter(torch.zeros(2))]), 1.0)
+    assert [len(c[1]) for c in gradients] == [1, 1]

@@ -16,8 +16,8 @@
 //
 // Bound by the SIMDs' issue: matrix instructions and the softmax's vector instructions run
 // side by side only from different wavefronts, so two to four share a SIMD. 18000 tokens of
-// 32/8 heads of 128: 900 us, 990 TFLOP/s (a large product reaches 1531; the counters of 15000
-// tokens have the matrix cores busy in 44% of the cycles, LDS in 22%, without a conflict).
+// 32/8 heads of 128: 880 us, 1010 TFLOP/s (a large product reaches 1531; the counters of 15000
+// tokens have the matrix cores busy in 43% of the cycles, LDS in 22%, without a conflict).
 // Without exponentials, maximum or sums it takes 3 to 6% less each, with all copies from one
 // tile 1%: none of them alone is what it waits for.
 #include <type_traits>

@@ -15,7 +15,9 @@
 // when a tile exceeds it. bf16 needs neither.
 //
 // Like the forward pass bound by the SIMDs' issue. 15000 tokens of 32/8 heads of 128: ka_dq
-// 620 us (920 TFLOP/s), ka_dkv 860 (890); matrix cores busy in 47 and 46% of the cycles.
+// 590 us (960 TFLOP/s), ka_dkv 840 (910); matrix cores busy in 49 and 46% of the cycles. A token's dk and dv
+// are one workgroup's over all query heads of its group: few key/value heads leave most CUs idle (8192 tokens of
+// 8 query heads of 128: 503 us for the gradients with 8 key/value heads, 1809 with one).
 #include <type_traits>
 
 #include "attn_common.h"
@@ -226,7 +228,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_dq(AttnArgs a) {
         if (__builtin_expect(cleared, 0)) attn_hide<BF16>(s, kp, a.k.token, base + 32 * sb, sq.n, D);
         v16f_t t = attn_rows_product<DP, BF16>(rd, 1, sb, g);
         // 256 channels leave no registers for operands read this early (172 of them went to memory in
-        // fp16: 1209 us for the gradients of 7000 tokens of 16/4 heads, 751 without)
+        // fp16, and the gradients took 1.6 times as long)
         constexpr bool kEarly = DP <= 128;
         uint4 y[2][kEarly ? ND : 1];
         if constexpr (kEarly) {
@@ -284,9 +286,9 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void ka_dq(AttnArgs a) {
 }
 
 // Up to 96 channels a wavefront has the registers for dV and dK of 32 tokens (184 and 240), two
-// wavefronts to a SIMD, and nothing goes through LDS between them: 278 us where pairs of
+// wavefronts to a SIMD, and nothing goes through LDS between them: 290 us where pairs of
 // wavefronts as below take 561 on 32000 tokens with a window of 500, 16 heads of 64 in fp16;
-// 320 and 446 on 20 images, 16 heads of 80 in bf16.
+// 334 and 446 on 20 images, 16 heads of 80 in bf16.
 template <int DP, bool BF16>
 __global__ __launch_bounds__(256, 2) void ka_dkv_alone(AttnArgs a) {
   using Tile = AttnTile<DP>;
@@ -451,7 +453,7 @@ __global__ __launch_bounds__(256, 2) void ka_dkv_alone(AttnArgs a) {
 // 32x32x16 and 16 multiply-adds take what each takes alone, together, from one wavefront;
 // the longer of the two from two), so that two to a SIMD are what overlaps them, and one
 // wavefront with both sums of 128 channels needs 450 registers and runs alone (1355 us where
-// this takes 860: 15000 tokens of 32/8 heads of 128).
+// this takes 840: 15000 tokens of 32/8 heads of 128).
 template <int DP, bool BF16>
 __global__ __launch_bounds__(DP <= 128 ? 512 : 256, DP <= 128 ? 2 : 1) void ka_dkv(AttnArgs a) {
   using Tile = AttnTile<DP>;

@@ -12,8 +12,10 @@
 // Rows wider than 8192 channels read x and dy once more for the columns' sums, as the
 // registers do not hold them.
 //
-// Bound by memory: 8190 rows of 4096 in bf16 take 27 us forward (5.0 TB/s) and 37 backward
-// (5.4 TB/s, part of it from the caches), and 4.4 the second launch.
+// Bound by memory where rows fill their lanes: 8190 rows of 4096 in bf16 take 33 us forward (4.0 TB/s)
+// and 37 backward right after it (5.4 TB/s, part of it from the caches), and 4.8 the second launch;
+// backward alone is 47 with that. A row has 64 lanes at least, 16 channels to a lane: narrow ones leave
+// most of them idle (500000 rows of 64 in fp16: 201 us forward, 0.6 TB/s, and 631 backward, 0.3 TB/s).
 #include <algorithm>
 #include <type_traits>
 

@@ -79,8 +79,8 @@ inline RopeArgs rope_rows_of(RopeArgs a, int64_t at, int64_t n) {
 hipError_t launch_rope(const RopeArgs& a, bool bf16, int num_cus, hipStream_t stream);
 
 // Gradients: up to N tensors to a launch, as its arguments: 480 of them where there are more
-// than 120 (448 tensors of 4096 to 180000 values: 41 us for norm and clipping, 74 in launches
-// of 120), else 120 (65 tensors: 28 us, 37 with the 16 KB of arguments of 480). A workgroup takes
+// than 120 (tensors of 4096 to 180000 values, norm and clipping replayed from a graph: 121 of them 19 us
+// and 26 in launches of 120, 240 of them 26 and 35, 448 of them 37 and 67, 600 of them 56 and 85), else 120 (65 tensors: 28 us, 37 with the 16 KB of arguments of 480). A workgroup takes
 // `chunk` values of one; tensor t's workgroups begin at `start`. One entry is 32 bytes
 // for all that is read of a tensor: beside an array of bytes indexed by the tensor the
 // compiler has split 8 t into t and 7 t for a scalar load of an address, and scalar

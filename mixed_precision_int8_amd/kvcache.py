@@ -406,6 +406,9 @@ class Int8SelfAttention:
         qkv = self.qkv(X).view(X.shape[0], nq + 2 * c.heads, c.dim)
         rope = self.rope
         if pos is not None:
+            # the append turns along one axis only: here keys are rounded to 16 bits after the rotation and once more
+            # when they become codes (the append's own rotation hands it fp32). At most half a 16-bit step of a key
+            # beside half a step of its code, which is a 254th of the page's largest
             turn = qkv[:, :nq + c.heads]
             m8.llmint8_rope(rope, pos, self.axis, turn, interleaved=self.interleaved, q_out=turn)
             rope = None

@@ -130,11 +130,12 @@ class PackedRows:
     captured graph's replays.
 
     ``used``, where the host knows it: cu[seqs] (rows past it belong to no sequence). It is of what cu holds now: after
-    an operation on cu, and in a captured call, it counts as unknown. ``max_len``, if known: no sequence is longer,
-    whatever cu will hold (``of`` knows it of its lengths only). Operations on cu are seen as autograd sees them, by
-    its version; who writes its memory behind that (``cu.data``, a kernel of their own) gives neither."""
+    an operation on cu, and in a captured call, it counts as unknown, until it is assigned anew. ``max_len``, if known:
+    no sequence is longer, whatever cu will hold (``of`` knows it of its lengths only; it may be assigned). Operations
+    on cu are seen as autograd sees them, by its version; who writes its memory behind that (``cu.data``, a kernel of
+    their own) gives neither."""
 
-    __slots__ = ("cu", "seqs", "rows", "device", "used", "max_len", "_version", "_of")
+    __slots__ = ("cu", "seqs", "rows", "device", "_used", "_max_len", "_version", "_of")
 
     def __init__(self, cu, rows, max_len=0, used=None):
         _library()
@@ -143,12 +144,31 @@ class PackedRows:
             raise ValueError(f"cu: expected [seqs + 1], got {tuple(cu.shape)}")
         m8._need(cu, torch.int32, (self.seqs + 1,), "cu")
         self.rows = int(rows)
-        if self.rows < 0 or max_len < 0 or (used is not None and used < 0):
-            raise ValueError("rows, max_len and used: expected >= 0")
-        self.cu, self.device, self.max_len = cu, cu.device, int(max_len)
-        self.used = None if used is None else min(int(used), self.rows)
-        self._version = None if cu.is_inference() else cu._version  # None: changes of cu are not seen
-        self._of = False
+        if self.rows < 0:
+            raise ValueError(f"rows: expected >= 0, got {rows}")
+        self.cu, self.device = cu, cu.device
+        self.max_len, self.used = max_len, used
+
+    @property
+    def used(self):
+        return self._used
+
+    @used.setter
+    def used(self, used):
+        if used is not None and used < 0:
+            raise ValueError(f"used: expected >= 0, got {used}")
+        self._used = None if used is None else min(int(used), self.rows)
+        self._version = None if self.cu.is_inference() else self.cu._version  # None: changes of cu are not seen
+
+    @property
+    def max_len(self):
+        return self._max_len
+
+    @max_len.setter
+    def max_len(self, max_len):
+        if max_len < 0:
+            raise ValueError(f"max_len: expected >= 0, got {max_len}")
+        self._max_len, self._of = int(max_len), None
 
     @classmethod
     def of(cls, lengths, rows=None, device="cuda"):
@@ -164,24 +184,20 @@ class PackedRows:
         with torch.inference_mode(False):  # inference tensors have no version
             cu = torch.tensor(at, dtype=torch.int32).to(device)
         batch = cls(cu, at[-1] if rows is None else rows, max_len=max(lengths, default=0), used=at[-1])
-        batch._of = True
+        batch._of = batch._version
         return batch
-
-    def _as_told(self):
-        """cu holds what it held when ``used`` was given, and every run of this call will find that there."""
-        return self._version is not None and self.cu._version == self._version
 
     def used_rows(self):
         """``used`` while it holds, else None."""
-        if self.used is None or not self._as_told():
+        if self.used is None or self._version is None or self.cu._version != self._version:
             return None
         with _on(self.device):  # torch asks about the current device's stream
             return None if torch.cuda.is_current_stream_capturing() else self.used
 
     def longest(self):
         """No sequence has more tokens, as far as the host knows."""
-        if getattr(self, "_of", False):
-            return self.max_len if self._as_told() else self.rows
+        if self._of is not None:
+            return self.max_len if self.cu._version == self._of else self.rows
         return self.max_len or self.rows
 
     def positions(self):

@@ -329,3 +329,22 @@ def test_one_parameter_is_clipped(gradients):
     gradients.clear()
     m8.clip_grad_norm((x for x in [p, torch.nn.Parameter(torch.zeros(2))]), 1.0)
     assert [len(c[1]) for c in gradients] == [1, 1]
+
+
+def test_what_the_host_knows_may_be_assigned(packed):
+    """After a change of cu, by a program that keeps the batch."""
+    filled, _ = packed
+    b = m8.PackedRows.of([60, 60], device="cpu")
+    b.cu.copy_(torch.tensor([0, 30, 90], dtype=torch.int32))
+    assert b.used_rows() is None and b.longest() == 120
+    b.used = 90
+    assert b.used == 90 and torch.isnan(filled(b)[:90]).all() and (filled(b)[90:] == 0).all() and b.longest() == 120
+    b.max_len = 60
+    assert b.longest() == 60 and b.used_rows() == 90
+    b.cu.copy_(torch.tensor([0, 60, 80], dtype=torch.int32))
+    assert b.longest() == 60 and b.used_rows() is None and (filled(b) == 0).all()
+    for name in ("used", "max_len"):
+        with pytest.raises(ValueError, match=name):
+            setattr(b, name, -1)
+    b.used = None
+    assert b.used_rows() is None
